@@ -10,6 +10,8 @@ of the page "fp8_kernel.py — FP8 量化内核" (section 1): an [M, N] matrix
 and a [BLOCK_M, BLOCK_N] block size in, ``(fp8_data, descale)`` out, with the
 descale shaped [ceil(M/bm), ceil(N/bn)].  ``quantize_many`` is the grouped
 form of the per-weight loop of the page "vllm_fp8_utils.py" (section 3).
+``KvCache``, ``kv_append`` and ``kv_attention`` keep keys and values in the
+same format, a page and head being the block.
 """
 
 import ctypes
@@ -47,6 +49,9 @@ EXPORTS = (
     "fp8bq_row_shard_edges",
     "fp8bq_row_shards_begin",
     "fp8bq_row_shards_finish",
+    "fp8bq_kv_append",
+    "fp8bq_kv_attention",
+    "fp8bq_kv_attention_workspace_bytes",
     "fp8bq_set_resident_wait_us",
     "fp8bq_status_string",
     "fp8bq_last_hip_error",
@@ -153,6 +158,13 @@ def load_library() -> ctypes.CDLL:
     lib.fp8bq_row_shards_begin.restype = ctypes.c_int
     lib.fp8bq_row_shards_finish.argtypes = [ctypes.POINTER(RowShardEntry), c_i32, c_i32, c_i32, c_vp]
     lib.fp8bq_row_shards_finish.restype = ctypes.c_int
+    # structs packed by kv.py
+    lib.fp8bq_kv_append.argtypes = [c_vp, c_vp, c_vp, c_vp]
+    lib.fp8bq_kv_append.restype = ctypes.c_int
+    lib.fp8bq_kv_attention.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]
+    lib.fp8bq_kv_attention.restype = ctypes.c_int
+    lib.fp8bq_kv_attention_workspace_bytes.argtypes = [c_i32, c_i32, c_i32, c_i32, c_i64]
+    lib.fp8bq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.fp8bq_encode_e4m3.argtypes = [c_vp, c_vp, c_i64, c_vp]
     lib.fp8bq_encode_e4m3.restype = ctypes.c_int
     lib.fp8bq_set_resident_wait_us.argtypes = [c_i64]
@@ -758,7 +770,10 @@ def encode_e4m3(y):
     return q
 
 
+from .kv import KvCache, kv_append, kv_attention, kv_attention_workspace_bytes  # noqa: E402
+
 __all__ = [
+    "KvCache", "kv_append", "kv_attention", "kv_attention_workspace_bytes",
     "DqEntry", "EXPORTS", "Fp8bqError", "TensorEntry", "block_shape", "dequantize",
     "dequantize_many", "encode_e4m3",
     "load_library", "local_grid", "quantize_with_amax", "quantize_with_amax_many", "tile_amax",

@@ -25,9 +25,14 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "fp8bq.hip")
-KERNEL_SOURCES = [os.path.join(HERE, "csrc", "kernels.hpp"), SRC, os.path.join(HERE, "csrc", "div31.hpp")]
-DEPS = KERNEL_SOURCES + [os.path.join(ROOT, "include", "fp8bq.h")]
+# One translation unit, which includes the others.
+SRC = os.path.join(HERE, "csrc", "lib.hip")
+# The weight quantizers (what the committed counter profiles are keyed on),
+# and the key/value cache beside them.
+KERNEL_SOURCES = [os.path.join(HERE, "csrc", "kernels.hpp"), os.path.join(HERE, "csrc", "fp8bq.hip"),
+                  os.path.join(HERE, "csrc", "div31.hpp")]
+KV_SOURCES = [SRC, os.path.join(HERE, "csrc", "kv.hip"), os.path.join(HERE, "csrc", "kv_kernels.hpp")]
+DEPS = KERNEL_SOURCES + KV_SOURCES + [os.path.join(ROOT, "include", "fp8bq.h")]
 LIB = os.path.join(HERE, "libfp8bq.so")
 ARCH = "gfx950"
 
@@ -94,8 +99,8 @@ def fingerprint(paths, extra: str = "") -> str:
 
 
 def kernel_sha() -> str:
-    """Fingerprint of the kernel sources alone (what the committed counter
-    profiles are keyed on)."""
+    """Fingerprint of the weight quantizers' sources alone (what the committed
+    counter profiles are keyed on)."""
     return fingerprint(KERNEL_SOURCES)
 
 

@@ -1,0 +1,248 @@
+// Host side of the blockwise e4m3 key/value cache: the fp8bq_kv_* calls of
+// include/fp8bq.h.  Every argument check runs before the first HIP call;
+// the calls enqueue on the caller's stream and neither allocate nor wait.
+
+#include "kv_kernels.hpp"
+
+namespace {
+
+int kv_log2_page(int32_t page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    case 256: return 8;
+    default: return -1;
+  }
+}
+
+bool kv_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// Grids and in-kernel row numbers stay in 32 bits.
+constexpr int64_t kKvMaxRows = int64_t{1} << 25;   // query tokens x query heads
+constexpr int32_t kKvMaxBatch = 1 << 20;
+
+bool kv_cache_ok(const fp8bq_kv_cache* c) {
+  if (c == nullptr || kv_log2_page(c->page_size) < 0) return false;
+  if (c->head_dim < 64 || c->head_dim > 256 || c->head_dim % 64 != 0) return false;
+  if (c->kv_heads < 1 || c->kv_heads > 65535 || c->num_pages < 1 || c->num_pages > INT32_MAX) return false;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return false;
+  if (!kv_aligned(c->k, 16) || !kv_aligned(c->v, 16) || !kv_aligned(c->k_scale, 4) ||
+      !kv_aligned(c->v_scale, 4)) {
+    return false;
+  }
+  const uint64_t blocks = static_cast<uint64_t>(c->num_pages) * static_cast<uint64_t>(c->kv_heads);
+  const uint64_t codes = blocks * static_cast<uint64_t>(c->page_size) * static_cast<uint64_t>(c->head_dim);
+  const void* at[4] = {c->k, c->v, c->k_scale, c->v_scale};
+  const uint64_t size[4] = {codes, codes, 4 * blocks, 4 * blocks};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j) {
+      if (overlap(at[i], size[i], at[j], size[j])) return false;
+    }
+  }
+  return true;
+}
+
+bool kv_batch_ok(const fp8bq_kv_batch* b, int64_t tokens) {
+  if (b == nullptr || b->count < 0 || b->count > kKvMaxBatch || b->max_pages < 0 || tokens < 0) return false;
+  if (b->count == 0) return true;
+  if (b->table_stride < b->max_pages || (b->max_pages > 0 && !b->block_table) || !b->seq_lens) return false;
+  if (!kv_aligned(b->block_table, 4) || !kv_aligned(b->seq_lens, 4) || !kv_aligned(b->query_start, 4)) return false;
+  return b->query_start != nullptr || tokens == b->count;
+}
+
+// Rows of 16-byte words: base and strides.
+bool kv_rows_ok(const void* p, int64_t tok, int64_t head) {
+  return p != nullptr && kv_aligned(p, 16) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0;
+}
+
+fp8bq::KvCache kv_device(const fp8bq_kv_cache& c) {
+  fp8bq::KvCache d;
+  d.k = static_cast<uint8_t*>(c.k);
+  d.v = static_cast<uint8_t*>(c.v);
+  d.ks = c.k_scale;
+  d.vs = c.v_scale;
+  d.pages = static_cast<int32_t>(c.num_pages);
+  d.heads = c.kv_heads;
+  d.log_s = kv_log2_page(c.page_size);
+  return d;
+}
+
+fp8bq::KvBatch kv_device(const fp8bq_kv_batch& b) {
+  return fp8bq::KvBatch{b.block_table, b.seq_lens, b.query_start, b.table_stride, b.count, b.max_pages};
+}
+
+// f(std::integral_constant<int, D>) for the cache's head_dim.
+template <typename F>
+void kv_for_dim(int32_t dim, F&& f) {
+  switch (dim) {
+    case 64: f(std::integral_constant<int, 64>{}); break;
+    case 128: f(std::integral_constant<int, 128>{}); break;
+    case 192: f(std::integral_constant<int, 192>{}); break;
+    default: f(std::integral_constant<int, 256>{}); break;
+  }
+}
+
+// How an attention call is cut up: from the shapes alone, so that the
+// workspace can be sized, and a launch captured, before any length is known.
+struct KvShape {
+  int32_t group;       // query heads per key/value head
+  int32_t rows;        // query rows (tokens x heads of a group) of a workgroup
+  int32_t slots;       // workgroups per key/value head
+  int32_t target;      // of these, how many splitting the keys aims at; 0: no splits
+  int32_t min_tiles;
+  size_t rows_at, ml_at, bytes;   // workspace: partial sums at 0, then these
+};
+
+KvShape kv_shape(int32_t kv_heads, int32_t dim, int32_t q_heads, int32_t count, int64_t tokens) {
+  KvShape s;
+  s.group = q_heads / kv_heads;
+  const int64_t per_seq = ceil_div(tokens * s.group, count);
+  s.rows = per_seq <= 16 ? 16 : 32;
+  const int64_t base = tokens * s.group / s.rows + count;
+  s.target = base * kv_heads >= 4096 ? 0 : static_cast<int32_t>(ceil_div(1024, kv_heads));
+  s.min_tiles = 4;
+  s.slots = static_cast<int32_t>(base + s.target);
+  const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(kv_heads) * static_cast<size_t>(s.rows);
+  s.ml_at = n * static_cast<size_t>(dim) * 4;
+  s.rows_at = s.ml_at + n * 8;
+  s.bytes = s.target == 0 ? 0 : s.rows_at + static_cast<size_t>(tokens) * static_cast<size_t>(q_heads) * 8;
+  return s;
+}
+
+bool kv_heads_ok(int32_t q_heads, int32_t kv_heads, int64_t tokens) {
+  return q_heads >= 1 && q_heads % kv_heads == 0 && tokens <= kKvMaxRows / q_heads;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, const fp8bq_kv_tokens* t,
+                    void* stream) {
+  if (!kv_cache_ok(cache) || t == nullptr || !kv_batch_ok(batch, t->tokens)) return FP8BQ_ERR_INVALID_ARGUMENT;
+  if (t->rot_dim < 0 || t->rot_dim > cache->head_dim || t->rot_dim % 16 != 0) return FP8BQ_ERR_INVALID_ARGUMENT;
+  if (!kv_heads_ok(t->q ? t->q_heads : cache->kv_heads, cache->kv_heads, t->tokens)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (batch->count == 0 || t->tokens == 0) return FP8BQ_OK;
+  if (!kv_rows_ok(t->k, t->k_token_stride, t->k_head_stride) ||
+      !kv_rows_ok(t->v, t->v_token_stride, t->v_head_stride)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (t->q && (!kv_rows_ok(t->q, t->q_token_stride, t->q_head_stride) ||
+               !kv_rows_ok(t->q_out, t->q_out_token_stride, t->q_out_head_stride))) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (t->rot_dim > 0 && (!t->cos || !t->sin || !kv_aligned(t->cos, 16) || !kv_aligned(t->sin, 16) ||
+                         t->positions < 0)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  const int rc = device_check();
+  if (rc != FP8BQ_OK) return rc;
+  const fp8bq::KvCache c = kv_device(*cache);
+  const fp8bq::KvBatch b = kv_device(*batch);
+  fp8bq::KvTokens d;
+  d.k = static_cast<const uint16_t*>(t->k);
+  d.v = static_cast<const uint16_t*>(t->v);
+  d.q = static_cast<const uint16_t*>(t->q);
+  d.q_out = static_cast<uint16_t*>(t->q_out);
+  d.cos = t->cos;
+  d.sin = t->sin;
+  d.k_tok = t->k_token_stride;
+  d.k_head = t->k_head_stride;
+  d.v_tok = t->v_token_stride;
+  d.v_head = t->v_head_stride;
+  d.q_tok = t->q_token_stride;
+  d.q_head = t->q_head_stride;
+  d.o_tok = t->q_out_token_stride;
+  d.o_head = t->q_out_head_stride;
+  d.positions = t->positions;
+  d.tokens = static_cast<int32_t>(t->tokens);
+  d.group = t->q ? t->q_heads / cache->kv_heads : 0;
+  d.half = t->rot_dim / 2;
+  d.interleaved = t->interleaved != 0;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  kv_for_dim(cache->head_dim, [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (batch->query_start == nullptr) {
+      const int64_t waves = static_cast<int64_t>(batch->count) * cache->kv_heads;
+      hipLaunchKernelGGL(fp8bq::kv_append_step<D>, dim3(static_cast<unsigned>(ceil_div(waves, 4))),
+                         dim3(fp8bq::kThreads), 0, st, c, b, d);
+    } else {
+      const int64_t slots = (t->tokens >> c.log_s) + 2 * static_cast<int64_t>(batch->count);
+      hipLaunchKernelGGL(fp8bq::kv_append_pages<D>,
+                         dim3(static_cast<unsigned>(slots), static_cast<unsigned>(cache->kv_heads)),
+                         dim3(fp8bq::kThreads), 0, st, c, b, d);
+    }
+  });
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? FP8BQ_OK : hip_failed(e);
+}
+
+size_t fp8bq_kv_attention_workspace_bytes(int32_t kv_heads, int32_t head_dim, int32_t q_heads, int32_t count,
+                                          int64_t tokens) {
+  if (kv_heads < 1 || count < 1 || tokens < 1 || !kv_heads_ok(q_heads, kv_heads, tokens)) return 0;
+  return kv_shape(kv_heads, head_dim, q_heads, count, tokens).bytes;
+}
+
+int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, const fp8bq_kv_query* q,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (!kv_cache_ok(cache) || q == nullptr || !kv_batch_ok(batch, q->tokens)) return FP8BQ_ERR_INVALID_ARGUMENT;
+  if (!kv_heads_ok(q->q_heads, cache->kv_heads, q->tokens) || q->window < 0 || !(q->scale - q->scale == 0.0f)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (batch->count == 0 || q->tokens == 0) return FP8BQ_OK;
+  if (!kv_rows_ok(q->q, q->q_token_stride, q->q_head_stride) ||
+      !kv_rows_ok(q->out, q->out_token_stride, q->out_head_stride) || !kv_aligned(q->lse, 4)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  const KvShape s = kv_shape(cache->kv_heads, cache->head_dim, q->q_heads, batch->count, q->tokens);
+  if (s.bytes > 0 && (workspace == nullptr || workspace_bytes < s.bytes || !kv_aligned(workspace, 16))) {
+    return FP8BQ_ERR_WORKSPACE;
+  }
+  const int rc = device_check();
+  if (rc != FP8BQ_OK) return rc;
+  const fp8bq::KvCache c = kv_device(*cache);
+  const fp8bq::KvBatch b = kv_device(*batch);
+  fp8bq::KvQuery d;
+  d.q = static_cast<const uint16_t*>(q->q);
+  d.out = static_cast<uint16_t*>(q->out);
+  d.lse = q->lse;
+  char* ws = static_cast<char*>(workspace);
+  const bool split = s.target > 0;
+  d.part = split ? reinterpret_cast<float*>(ws) : nullptr;
+  d.part_ml = split ? reinterpret_cast<float2*>(ws + s.ml_at) : nullptr;
+  d.rows = split ? reinterpret_cast<int2*>(ws + s.rows_at) : nullptr;
+  d.q_tok = q->q_token_stride;
+  d.q_head = q->q_head_stride;
+  d.o_tok = q->out_token_stride;
+  d.o_head = q->out_head_stride;
+  d.tokens = static_cast<int32_t>(q->tokens);
+  d.group = s.group;
+  d.window = q->window;
+  d.slots = s.slots;
+  d.target = s.target;
+  d.min_tiles = s.min_tiles;
+  d.scale = q->scale * 1.4426950408889634f;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  kv_for_dim(cache->head_dim, [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    const dim3 grid(static_cast<unsigned>(s.slots), static_cast<unsigned>(cache->kv_heads));
+    if (s.rows == 16) {
+      hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 1>), grid, dim3(fp8bq::kThreads), 0, st, c, b, d);
+    } else {
+      hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 2>), grid, dim3(fp8bq::kThreads), 0, st, c, b, d);
+    }
+    if (split) {
+      const int64_t rows = q->tokens * q->q_heads;
+      hipLaunchKernelGGL(fp8bq::kv_attend_join<D>, dim3(static_cast<unsigned>(ceil_div(rows, 4))),
+                         dim3(fp8bq::kThreads), 0, st, b, d, c.heads, s.rows);
+    }
+  });
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? FP8BQ_OK : hip_failed(e);
+}
+
+}  // extern "C"

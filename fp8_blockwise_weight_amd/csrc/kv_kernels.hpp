@@ -1,0 +1,890 @@
+// Device code of the blockwise e4m3 key/value cache (gfx950): appending
+// rotated tokens to paged blocks, and attention over them.
+//
+// A page of S tokens holds, for each key/value head, two e4m3 blocks with one
+// fp32 descale each, as fp8bq_quantize lays out a weight's tiles:
+//   k  [S, D]  a token's channels side by side
+//   v  [D, S]  a channel's tokens side by side
+// Both products of attention then read their 8-bit operand in 16-byte loads
+// in the order the matrix instruction wants it: the scores contract over
+// channels (rows of k), the weighted sum over tokens (rows of v).  With v
+// token-major, every lane would gather the 8 tokens of an operand byte by
+// byte, or transpose each tile through LDS on every read; the transposition
+// is paid once instead, when a token is stored.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernels.hpp"
+
+namespace fp8bq {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+
+struct KvCache {
+  uint8_t* k;      // e4m3 [pages, heads, S, D]
+  uint8_t* v;      // e4m3 [pages, heads, D, S]
+  float* ks;       // fp32 [pages, heads]
+  float* vs;
+  int32_t pages;
+  int32_t heads;
+  int32_t log_s;   // S = 1 << log_s, 16 .. 256
+};
+
+struct KvBatch {
+  const int32_t* table;   // [count, max_pages], rows `stride` apart
+  const int32_t* lens;    // [count]
+  const int32_t* starts;  // [count + 1], or null: one token each
+  int64_t stride;
+  int32_t count;
+  int32_t max_pages;
+};
+
+struct KvTokens {
+  const uint16_t* k;    // BF16 rows
+  const uint16_t* v;
+  const uint16_t* q;    // or null
+  uint16_t* q_out;
+  const float* cos;     // fp32 [positions, half]
+  const float* sin;
+  int64_t k_tok, k_head, v_tok, v_head, q_tok, q_head, o_tok, o_head;  // strides in elements
+  int64_t positions;    // rows of cos / sin (a limit only where half > 0)
+  int32_t tokens;
+  int32_t group;        // query heads per key/value head
+  int32_t half;         // rotated channel pairs
+  int32_t interleaved;
+};
+
+// ------------------------------------------------------------------ append
+//
+// s = the smallest power of two with 448 s >= max|x| (448 = 1.75 * 2^8), not
+// amax / 448 as for weights: a page's maximum grows while tokens arrive, and
+// every growth takes the stored codes along.  With a ratio of powers of two
+// that is a change of exponent, exact except below the smallest normal code;
+// with any other ratio each growth would round every earlier token again.
+
+__device__ __forceinline__ float kv_fit_scale(float amax) {
+  const uint32_t bits = __float_as_uint(fmaxf(amax, kEps));   // normal: kEps > 2^-126
+  return __uint_as_float(((bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0)) << 23);
+}
+
+// 1 / s of a power of two (exact).
+__device__ __forceinline__ float kv_inverse(float s) {
+  return __uint_as_float((254u << 23) - __float_as_uint(s));
+}
+
+__device__ __forceinline__ int32_t kv_clamp(int32_t v, int32_t hi) {
+  return v < 0 ? 0 : (v > hi ? hi : v);
+}
+
+// Four codes times `ratio`, rounded to codes again.
+__device__ __forceinline__ uint32_t kv_recode4(uint32_t w, float ratio) {
+  const f32x4 x = dq4(w, ratio);
+  return cvt4(clamp448(x.x), clamp448(x.y), clamp448(x.z), clamp448(x.w));
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+// The largest b in [0, n) with f(b) <= w for a non-decreasing f (0 if none),
+// 64 values of f at a time: one round of loads for up to 64 sequences, two
+// for up to 4096.  The same in every lane.
+template <typename F>
+__device__ __forceinline__ int32_t kv_find(int32_t n, int64_t w, F&& f) {
+  const int32_t lane = threadIdx.x & 63;
+  int32_t lo = 0, span = n;
+  while (span > 1) {
+    const int32_t step = (span + 63) >> 6;
+    const int32_t at = lane * step;
+    const bool below = at < span && f(lo + at) <= w;
+    const int32_t c = __popcll(__ballot(below));
+    if (c == 0) return lo;
+    lo += (c - 1) * step;
+    span = min(step, span - (c - 1) * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Channels of pair p: (p, p + half) or (2p, 2p + 1) where it is rotated, and
+// (2p, 2p + 1) behind the rotated ones.
+__device__ __forceinline__ void pair_channels(int32_t p, int32_t half, int32_t interleaved, int32_t& a,
+                                              int32_t& b) {
+  const bool split = p < half && !interleaved;
+  a = split ? p : 2 * p;
+  b = split ? p + half : 2 * p + 1;
+}
+
+__device__ __forceinline__ float bf16_up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t bf16_down(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// One token for every sequence: a wave for each (sequence, key/value head),
+// lanes over channel pairs.  There is nothing to reuse: the time is the chain
+// of dependent loads (length -> page -> scale) and the launch.
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv_append_step(KvCache c, KvBatch bt, KvTokens t) {
+  constexpr int kP = (D / 2 + 63) / 64;   // pairs of a lane
+  const int32_t lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (item >= (int64_t)bt.count * c.heads) return;
+  const int32_t b = (int32_t)(item / c.heads), h = (int32_t)(item - (int64_t)b * c.heads);
+  const int32_t pos = bt.lens[b] - 1;
+  if (pos < 0 || (t.half > 0 && pos >= t.positions)) return;
+  const int32_t S = 1 << c.log_s, slot = pos & (S - 1), j = pos >> c.log_s;
+  const int32_t page = j < bt.max_pages ? bt.table[(int64_t)b * bt.stride + j] : -1;
+  const bool stored = page >= 0 && page < c.pages;
+
+  float kx[kP], ky[kP], cs[kP], sn[kP];
+  uint32_t vw[kP];
+  float ka = 0.0f, va = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int32_t p = lane + 64 * i;
+    cs[i] = 1.0f;
+    sn[i] = 0.0f;
+    if (p < t.half) {
+      cs[i] = t.cos[(int64_t)pos * t.half + p];
+      sn[i] = t.sin[(int64_t)pos * t.half + p];
+    }
+    kx[i] = ky[i] = 0.0f;
+    vw[i] = 0;
+    if (p < D / 2) {
+      int32_t ca, cb;
+      pair_channels(p, t.half, t.interleaved, ca, cb);
+      const uint16_t* kr = t.k + b * t.k_tok + h * t.k_head;
+      const float x = bf16_up(kr[ca]), y = bf16_up(kr[cb]);
+      kx[i] = p < t.half ? x * cs[i] - y * sn[i] : x;
+      ky[i] = p < t.half ? y * cs[i] + x * sn[i] : y;
+      vw[i] = *(const uint32_t*)(t.v + b * t.v_tok + h * t.v_head + 2 * p);
+      ka = fmaxf(ka, fmaxf(fabsf(kx[i]), fabsf(ky[i])));
+      va = fmaxf(va, fmaxf(fabsf(bf_lo(vw[i])), fabsf(bf_hi(vw[i]))));
+    }
+  }
+  if (stored) {
+    const int64_t block = (int64_t)page * c.heads + h;
+    float k_was = slot ? c.ks[block] : 0.0f, v_was = slot ? c.vs[block] : 0.0f;
+    const float k_fit = kv_fit_scale(wave_max(ka)), v_fit = kv_fit_scale(wave_max(va));
+    const float k_s = slot ? fmaxf(k_was, k_fit) : k_fit, v_s = slot ? fmaxf(v_was, v_fit) : v_fit;
+    uint8_t* kb = c.k + block * S * D;
+    uint8_t* vb = c.v + block * S * D;
+    const float kr = kv_inverse(k_s), vr = kv_inverse(v_s);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int32_t p = lane + 64 * i;
+      if (p >= D / 2) continue;
+      int32_t ca, cb;
+      pair_channels(p, t.half, t.interleaved, ca, cb);
+      const uint32_t kc = cvt4(clamp448(kx[i] * kr), clamp448(ky[i] * kr), 0.0f, 0.0f);
+      kb[slot * D + ca] = (uint8_t)kc;
+      kb[slot * D + cb] = (uint8_t)(kc >> 8);
+      const uint32_t vc = cvt4(clamp448(bf_lo(vw[i]) * vr), clamp448(bf_hi(vw[i]) * vr), 0.0f, 0.0f);
+      vb[(2 * p) * S + slot] = (uint8_t)vc;
+      vb[(2 * p + 1) * S + slot] = (uint8_t)(vc >> 8);
+    }
+    if (lane == 0) {
+      c.ks[block] = k_s;
+      c.vs[block] = v_s;
+    }
+    // Growth takes the earlier tokens along: whole 16-token runs of a channel
+    // as vectors, the run the new byte lies in byte by byte (only its earlier
+    // bytes), so that no two stores of the wave overlap.
+    if (slot > 0 && k_s > k_was) {
+      const float ratio = k_was * kr;
+      for (int32_t i = lane; i < slot * (D / 16); i += 64) {
+        u32x4* at = (u32x4*)kb + i;
+        u32x4 w = *at;
+        for (int x = 0; x < 4; ++x) w[x] = kv_recode4(w[x], ratio);
+        *at = w;
+      }
+    }
+    if (slot > 0 && v_s > v_was) {
+      const float ratio = v_was * vr;
+      const int32_t runs = slot >> 4, rest = slot & 15;
+      for (int32_t d = lane; d < D; d += 64) {
+        for (int32_t r = 0; r < runs; ++r) {
+          u32x4* at = (u32x4*)(vb + d * S) + r;
+          u32x4 w = *at;
+          for (int x = 0; x < 4; ++x) w[x] = kv_recode4(w[x], ratio);
+          *at = w;
+        }
+        for (int32_t x = 0; x < rest; ++x) {
+          uint8_t* at = vb + d * S + (slot & ~15) + x;
+          *at = (uint8_t)kv_recode4(*at, ratio);
+        }
+      }
+    }
+  }
+  if (t.q == nullptr) return;
+  for (int32_t g = 0; g < t.group; ++g) {
+    const uint16_t* qr = t.q + b * t.q_tok + ((int64_t)h * t.group + g) * t.q_head;
+    uint16_t* qo = t.q_out + b * t.o_tok + ((int64_t)h * t.group + g) * t.o_head;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int32_t p = lane + 64 * i;
+      if (p >= D / 2) continue;
+      int32_t ca, cb;
+      pair_channels(p, t.half, t.interleaved, ca, cb);
+      const float x = bf16_up(qr[ca]), y = bf16_up(qr[cb]);
+      qo[ca] = bf16_down(p < t.half ? x * cs[i] - y * sn[i] : x);
+      qo[cb] = bf16_down(p < t.half ? y * cs[i] + x * sn[i] : y);
+    }
+  }
+}
+
+// 16 channels of a row, in two runs of 8 at channels a and b: both halves of
+// 8 rotated pairs, or 16 channels side by side.
+__device__ __forceinline__ void unit_channels(int32_t u, int32_t half, int32_t interleaved, int32_t& a,
+                                              int32_t& b) {
+  const bool split = 8 * u < half && !interleaved;
+  a = split ? 8 * u : 16 * u;
+  b = split ? half + 8 * u : 16 * u + 8;
+}
+
+// Rotates the 16 values of unit u (read as two 16-byte words) in place.
+__device__ __forceinline__ void unit_rotate(u32x4 lo, u32x4 hi, const float* cs, const float* sn, bool turn,
+                                            int32_t interleaved, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf_lo(lo[i]);
+    x[2 * i + 1] = bf_hi(lo[i]);
+    x[8 + 2 * i] = bf_lo(hi[i]);
+    x[8 + 2 * i + 1] = bf_hi(hi[i]);
+  }
+  if (!turn) return;
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = a * cs[i] - b * sn[i];
+      x[2 * i + 1] = b * cs[i] + a * sn[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[i], b = x[8 + i];
+      x[i] = a * cs[i] - b * sn[i];
+      x[8 + i] = b * cs[i] + a * sn[i];
+    }
+  }
+}
+
+// Sequences with any number of new tokens: a workgroup for each (page that a
+// sequence writes, key/value head), which owns the block's scale: no other
+// workgroup touches it, so there are no atomics and the result does not
+// depend on any order.  Slot w of the grid belongs to the sequence with
+// floor(starts[b] / S) + 2 b <= w, which leaves every sequence at least as
+// many slots as its tokens can span pages.
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv_append_pages(KvCache c, KvBatch bt, KvTokens t) {
+  constexpr int kU = D / 16;
+  __shared__ float red[8];
+  const int32_t tid = threadIdx.x, h = blockIdx.y;
+  const int32_t S = 1 << c.log_s;
+  const int64_t w = blockIdx.x;
+  auto first_slot = [&](int32_t b) {
+    return (int64_t)(kv_clamp(bt.starts[b], t.tokens) >> c.log_s) + 2 * (int64_t)b;
+  };
+  const int32_t b = kv_find(bt.count, w, first_slot);
+  const int64_t j0 = w - first_slot(b);
+  const int32_t row0 = kv_clamp(bt.starts[b], t.tokens);
+  const int32_t n = kv_clamp(bt.starts[b + 1], t.tokens) - row0;
+  if (j0 < 0 || n <= 0) return;
+  const int64_t len = bt.lens[b], start = len - n;
+  const int64_t begin = start < 0 ? 0 : start;
+  const int64_t j = (begin >> c.log_s) + j0;
+  const int64_t lo = max(begin, j << c.log_s);
+  int64_t hi = min(len, (j + 1) << c.log_s);
+  if (t.half > 0) hi = min(hi, t.positions);
+  if (lo >= hi) return;
+  const int32_t page = j < bt.max_pages ? bt.table[(int64_t)b * bt.stride + j] : -1;
+  const bool stored = page >= 0 && page < c.pages;
+  const int32_t held = (int32_t)(lo - (j << c.log_s));   // earlier tokens in the page
+  const int32_t count = (int32_t)(hi - lo);
+  const int64_t row = row0 + (lo - start);               // input row of the first token
+
+  auto unit = [&](const uint16_t* base, int64_t pos, int32_t u, float* x) {
+    int32_t ca, cb;
+    unit_channels(u, t.half, t.interleaved, ca, cb);
+    const u32x4 a = *(const u32x4*)(base + ca), z = *(const u32x4*)(base + cb);
+    const bool turn = 8 * u < t.half;
+    float cs[8], sn[8];
+    if (turn) {
+      const f32x4* cp = (const f32x4*)(t.cos + pos * t.half + 8 * u);
+      const f32x4* sp = (const f32x4*)(t.sin + pos * t.half + 8 * u);
+      *(f32x4*)cs = cp[0];
+      *(f32x4*)(cs + 4) = cp[1];
+      *(f32x4*)sn = sp[0];
+      *(f32x4*)(sn + 4) = sp[1];
+    }
+    unit_rotate(a, z, cs, sn, turn, t.interleaved, x);
+  };
+
+  if (stored) {
+    float ka = 0.0f, va = 0.0f;
+    for (int32_t i = tid; i < count * kU; i += kThreads) {
+      const int32_t tok = i / kU, u = i - tok * kU;
+      float x[16];
+      unit(t.k + (row + tok) * t.k_tok + h * t.k_head, lo + tok, u, x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ka = fmaxf(ka, fabsf(x[e]));
+      const u32x4* vp = (const u32x4*)(t.v + (row + tok) * t.v_tok + h * t.v_head + 16 * u);
+      const uint32_t m = halves_max(pk_max_u16(fold_abs(vp[0]), fold_abs(vp[1])));
+      va = fmaxf(va, __uint_as_float(m << 16));
+    }
+    ka = wave_max(ka);
+    va = wave_max(va);
+    if ((tid & 63) == 0) {
+      red[tid >> 6] = ka;
+      red[4 + (tid >> 6)] = va;
+    }
+    const int64_t block = (int64_t)page * c.heads + h;
+    const float k_was = held ? c.ks[block] : 0.0f, v_was = held ? c.vs[block] : 0.0f;
+    __syncthreads();
+    ka = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    va = fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7]));
+    const float k_fit = kv_fit_scale(ka), v_fit = kv_fit_scale(va);
+    const float k_s = held ? fmaxf(k_was, k_fit) : k_fit, v_s = held ? fmaxf(v_was, v_fit) : v_fit;
+    const float kr = kv_inverse(k_s), vr = kv_inverse(v_s);
+    if (tid == 0) {
+      c.ks[block] = k_s;
+      c.vs[block] = v_s;
+    }
+    uint8_t* kb = c.k + block * S * D;
+    uint8_t* vb = c.v + block * S * D;
+    if (held > 0 && k_s > k_was) {
+      const float ratio = k_was * kr;
+      for (int32_t i = tid; i < held * kU; i += kThreads) {
+        u32x4* at = (u32x4*)kb + i;
+        u32x4 x = *at;
+        for (int e = 0; e < 4; ++e) x[e] = kv_recode4(x[e], ratio);
+        *at = x;
+      }
+    }
+    for (int32_t i = tid; i < count * kU; i += kThreads) {
+      const int32_t tok = i / kU, u = i - tok * kU;
+      float x[16];
+      unit(t.k + (row + tok) * t.k_tok + h * t.k_head, lo + tok, u, x);
+      int32_t ca, cb;
+      unit_channels(u, t.half, t.interleaved, ca, cb);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = clamp448(x[e] * kr);
+      uint8_t* to = kb + (held + tok) * D;
+      *(u32x2*)(to + ca) = u32x2{cvt4(x[0], x[1], x[2], x[3]), cvt4(x[4], x[5], x[6], x[7])};
+      *(u32x2*)(to + cb) = u32x2{cvt4(x[8], x[9], x[10], x[11]), cvt4(x[12], x[13], x[14], x[15])};
+    }
+    // v: a thread owns 16 tokens of two channels, reads a row of channel
+    // pairs per wave and writes 16 bytes of each channel; runs that only
+    // partly hold new tokens are read, merged and written back.
+    const bool grown = held > 0 && v_s > v_was;
+    const float v_ratio = v_was * vr;
+    const int32_t r0 = grown ? 0 : held >> 4, r1 = (held + count + 15) >> 4;
+    for (int32_t i = tid; i < (r1 - r0) * (D / 2); i += kThreads) {
+      const int32_t r = r0 + i / (D / 2), p = i % (D / 2);
+      const int32_t a = 16 * r - held;                    // new token of the run's first byte
+      u32x4* at[2] = {(u32x4*)(vb + (2 * p) * S) + r, (u32x4*)(vb + (2 * p + 1) * S) + r};
+      const uint16_t* src = t.v + row * t.v_tok + h * t.v_head + 2 * p;
+      const bool whole = a >= 0 && a + 16 <= count;
+      u32x4 out[2];
+      uint32_t pairs[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        pairs[e] = 0;
+        if (a + e >= 0 && a + e < count) pairs[e] = *(const uint32_t*)(src + (int64_t)(a + e) * t.v_tok);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        out[0][x] = cvt4(clamp448(bf_lo(pairs[4 * x]) * vr), clamp448(bf_lo(pairs[4 * x + 1]) * vr),
+                         clamp448(bf_lo(pairs[4 * x + 2]) * vr), clamp448(bf_lo(pairs[4 * x + 3]) * vr));
+        out[1][x] = cvt4(clamp448(bf_hi(pairs[4 * x]) * vr), clamp448(bf_hi(pairs[4 * x + 1]) * vr),
+                         clamp448(bf_hi(pairs[4 * x + 2]) * vr), clamp448(bf_hi(pairs[4 * x + 3]) * vr));
+      }
+      if (!whole) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const u32x4 was = *at[y];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t again = grown ? kv_recode4(was[x], v_ratio) : was[x];
+            uint32_t m_new = 0, m_old = 0;   // bytes of new tokens, of earlier ones
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int32_t tok = a + 4 * x + e;
+              if (tok < 0) m_old |= 0xFFu << (8 * e);
+              else if (tok < count) m_new |= 0xFFu << (8 * e);
+            }
+            out[y][x] = (out[y][x] & m_new) | (again & m_old) | (was[x] & ~(m_new | m_old));
+          }
+        }
+      }
+      *at[0] = out[0];
+      *at[1] = out[1];
+    }
+  }
+  if (t.q == nullptr) return;
+  for (int32_t i = tid; i < count * kU; i += kThreads) {
+    const int32_t tok = i / kU, u = i - tok * kU;
+    int32_t ca, cb;
+    unit_channels(u, t.half, t.interleaved, ca, cb);
+    for (int32_t g = 0; g < t.group; ++g) {
+      const int64_t head = (int64_t)h * t.group + g;
+      float x[16];
+      unit(t.q + (row + tok) * t.q_tok + head * t.q_head, lo + tok, u, x);
+      uint16_t* to = t.q_out + (row + tok) * t.o_tok + head * t.o_head;
+      bf16x8 y, z;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = (__bf16)x[e];
+        z[e] = (__bf16)x[8 + e];
+      }
+      *(bf16x8*)(to + ca) = y;
+      *(bf16x8*)(to + cb) = z;
+    }
+  }
+}
+
+// --------------------------------------------------------------- attention
+
+struct KvQuery {
+  const uint16_t* q;   // BF16 rows
+  uint16_t* out;
+  float* lse;          // fp32 [tokens, query heads], or null
+  float* part;         // partial sums [heads, slots, R, D], or null: no splits
+  float2* part_ml;     // their maxima and sums [heads, slots, R]
+  int2* rows;          // first slot and count of each query row's partials
+  int64_t q_tok, q_head, o_tok, o_head;
+  int32_t tokens;
+  int32_t group;
+  int32_t window;      // 0: none
+  int32_t slots;       // work items per key/value head
+  int32_t target;      // items per head that splitting aims at; 0: no splits
+  int32_t min_tiles;   // least key tiles of a split
+  float scale;         // of the scores, times log2(e)
+};
+
+constexpr int kKeyTile = 64;
+
+// The work of one workgroup: a tile of query rows of a sequence and a range
+// of its key tiles.
+struct KvWork {
+  int32_t b, n, row0;       // sequence, its query tokens, their first row
+  int32_t first, count;     // first query row (token * group + head in group) of the tile; rows of the sequence
+  int64_t pos0;             // position of the sequence's first query token
+  int32_t tile0, tile1;     // key tiles
+  int32_t splits, split;
+};
+
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Which work item w is.  Every wave reads the batch's lengths and lays the
+// items out by itself: sequence b has ceil(rows / R) row tiles of
+// ceil(key tiles / chunk) splits each, with one chunk for the whole batch
+// such that about `target` items come out of it.  The grid depends on the
+// number of sequences and query tokens alone, so a captured launch stays
+// right, and balanced, as the lengths grow.
+template <int R>
+__device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int32_t log_s, int32_t w,
+                                        KvWork& k) {
+  const int32_t lane = threadIdx.x & 63;
+  const int64_t cap = (int64_t)bt.max_pages << log_s;
+  struct Seq {
+    int32_t row0, n, rtiles, tile0, tiles;
+    int64_t pos0;
+  };
+  auto seq = [&](int32_t b) {
+    Seq s{0, 0, 0, 0, 0, 0};
+    if (b >= bt.count) return s;
+    const int64_t len = bt.lens[b];
+    if (bt.starts) {
+      s.row0 = kv_clamp(bt.starts[b], p.tokens);
+      s.n = max(kv_clamp(bt.starts[b + 1], p.tokens) - s.row0, 0);
+    } else {
+      s.row0 = b;
+      s.n = 1;
+    }
+    s.pos0 = len - s.n;
+    s.rtiles = (int32_t)(((int64_t)s.n * p.group + R - 1) / R);
+    const int64_t hi = min(len, cap);
+    const int64_t lo = p.window > 0 ? max(s.pos0 + 1 - p.window, (int64_t)0) : 0;
+    if (s.n > 0 && hi > lo) {
+      s.tile0 = (int32_t)(lo / kKeyTile);
+      s.tiles = (int32_t)((hi + kKeyTile - 1) / kKeyTile) - s.tile0;
+    }
+    return s;
+  };
+  Seq mine = seq(lane);
+  int32_t chunk = INT32_MAX;
+  if (p.target > 0) {
+    int64_t total = (int64_t)mine.rtiles * mine.tiles;
+    for (int32_t b = 64; b < bt.count; b += 64) {
+      const Seq s = seq(b + lane);
+      total += (int64_t)s.rtiles * s.tiles;
+    }
+    total = wave_sum(total);
+    const int64_t per = (total + p.target - 1) / p.target;
+    chunk = (int32_t)min(max(per, (int64_t)p.min_tiles), (int64_t)INT32_MAX);
+  }
+  int64_t before = 0;
+  for (int32_t b0 = 0; b0 < bt.count; b0 += 64) {
+    if (b0 > 0) mine = seq(b0 + lane);
+    const int32_t splits = max(1, (int32_t)(((int64_t)mine.tiles + chunk - 1) / chunk));
+    const int32_t items = (int32_t)min((int64_t)mine.rtiles * splits, (int64_t)1 << 24);
+    int32_t sum = items;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(sum, d);
+      if (lane >= d) sum += o;
+    }
+    const uint64_t past = __ballot(before + sum > w);
+    if (past != 0) {
+      const int32_t at = __ffsll((unsigned long long)past) - 1;
+      k.b = b0 + at;
+      k.row0 = __shfl(mine.row0, at);
+      k.n = __shfl(mine.n, at);
+      k.pos0 = __shfl(mine.pos0, at);
+      k.splits = __shfl(splits, at);
+      const int32_t tile0 = __shfl(mine.tile0, at), tiles = __shfl(mine.tiles, at);
+      const int32_t local = (int32_t)(w - before) - (__shfl(sum, at) - __shfl(items, at));
+      const int32_t rtile = local / k.splits;
+      k.split = local - rtile * k.splits;
+      k.first = rtile * R;
+      k.count = k.n * p.group;
+      k.tile0 = tile0 + min((int64_t)k.split * chunk, (int64_t)tiles);
+      k.tile1 = tile0 + min((int64_t)(k.split + 1) * chunk, (int64_t)tiles);
+      return true;
+    }
+    before += __shfl(sum, 63);
+  }
+  return false;
+}
+
+// Eight codes (two dwords) as BF16, exactly.
+__device__ __forceinline__ bf16x8 kv_widen(uint32_t a, uint32_t b) {
+  const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const bf16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const bf16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
+}
+
+// Few query rows: R = 16 NT rows of a sequence (tokens times the query heads
+// that share a key head) in each of four waves, which take every fourth key
+// tile of the workgroup's range and join their sums at its end.
+//
+// Scores are computed transposed, S^T = K Q^T, a tile of 64 keys as four
+// 16x16x32 products per 32 channels.  Row m of product t is given token
+// 16 (m / 4) + 4 t + m % 4, so that lane group g (16 lanes) ends up with the
+// 16 consecutive tokens 16 g .. 16 g + 15 of its query row: one page, one pair
+// of scales, and exactly the operand order of O^T = V^T P^T, whose lanes read
+// 16 tokens of a channel in one load.  Nothing goes through LDS, and softmax
+// needs one exchange across the four lane groups per tile.
+//
+// Codes are widened to BF16 exactly and multiplied there (BF16 products with
+// fp32 sums); scales enter in fp32, k's with the score, v's with the weight,
+// which is then rounded to BF16 once (relative 2^-9, its sum is not).
+template <int D, int NT>
+__global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_attend_rows(KvCache c, KvBatch bt,
+                                                                                         KvQuery p) {
+  constexpr int R = 16 * NT;
+  constexpr int kI = D / 64;    // 64-channel pieces
+  constexpr int kDt = D / 16;   // 16-channel tiles of the output
+  constexpr int kPitch = D + 4;
+  __shared__ float lds_o[R * kPitch];
+  __shared__ float lds_m[4][R], lds_l[4][R];
+  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t col = lane & 15, grp = lane >> 4;
+  const int32_t h = blockIdx.y;
+  KvWork wk;
+  if (!kv_plan<R>(bt, p, c.log_s, blockIdx.x, wk)) return;
+  const int32_t S = 1 << c.log_s;
+  const int64_t cap = (int64_t)bt.max_pages << c.log_s;
+
+  // This lane's query rows, and what the whole tile sees.
+  int64_t row_hi[NT], row_lo[NT];
+  bf16x8 q[NT][kI][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int32_t r = wk.first + nt * 16 + col;
+    const bool live = r < wk.count;
+    const int32_t tok = live ? r / p.group : 0;
+    const int32_t g = live ? r - tok * p.group : 0;
+    const int64_t pos = wk.pos0 + tok;
+    row_hi[nt] = live ? min(pos + 1, cap) : 0;
+    row_lo[nt] = p.window > 0 ? max(pos + 1 - p.window, (int64_t)0) : 0;
+    const uint16_t* src = p.q + (wk.row0 + tok) * p.q_tok + ((int64_t)h * p.group + g) * p.q_head;
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        q[nt][i][x] = *(const bf16x8*)(src + 64 * i + 16 * grp + 8 * x);
+        if (!live) q[nt][i][x] = bf16x8{};
+      }
+    }
+  }
+  const int32_t tok_a = wk.first / p.group, tok_z = min(wk.first + R - 1, wk.count - 1) / p.group;
+  const int64_t see_hi = min(wk.pos0 + tok_z + 1, cap), all_hi = min(wk.pos0 + tok_a + 1, cap);
+  const int64_t see_lo = p.window > 0 ? max(wk.pos0 + tok_a + 1 - p.window, (int64_t)0) : 0;
+  const int64_t all_lo = p.window > 0 ? max(wk.pos0 + tok_z + 1 - p.window, (int64_t)0) : 0;
+  int32_t tile0 = wk.tile0, tile1 = wk.tile1;
+  tile0 = (int32_t)max((int64_t)tile0, see_lo / kKeyTile);
+  tile1 = (int32_t)min((int64_t)tile1, (max(see_hi, (int64_t)0) + kKeyTile - 1) / kKeyTile);
+
+  f32x4 o[NT][kDt];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = -INFINITY;
+    l[nt] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDt; ++i) o[nt][i] = f32x4{0, 0, 0, 0};
+  }
+
+  const int32_t* table = bt.table + (int64_t)wk.b * bt.stride;
+  // Page of the 16 tokens from t0 on, -1 where none of them is seen or the
+  // table's entry is no page.
+  auto page_of = [&](int64_t t0) {
+    int32_t pg = -1;
+    if (t0 < see_hi && t0 + 16 > see_lo) pg = table[t0 >> c.log_s];
+    return pg >= 0 && pg < c.pages ? pg : -1;
+  };
+  const int32_t k_run = col >> 2;
+  struct Tile {
+    u32x4 k[4][kI], v[kDt];
+    float ks, vs;
+    int32_t pv;
+    bool bad;
+  };
+  auto load = [&](int32_t tile, int32_t pk, int32_t pv, Tile& x) {
+    const int64_t tk = (int64_t)tile * kKeyTile + 16 * k_run, tv = (int64_t)tile * kKeyTile + 16 * grp;
+    const int64_t kblock = (int64_t)max(pk, 0) * c.heads + h, vblock = (int64_t)max(pv, 0) * c.heads + h;
+    const uint8_t* kp = c.k + kblock * S * D + ((tk & (S - 1)) + (col & 3)) * D + 16 * grp;
+    const uint8_t* vp = c.v + vblock * S * D + (int64_t)col * S + (tv & (S - 1));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int i = 0; i < kI; ++i) x.k[t][i] = *(const u32x4*)(kp + t * 4 * D + 64 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < kDt; ++i) x.v[i] = *(const u32x4*)(vp + i * 16 * S);
+    x.ks = c.ks[vblock];
+    x.vs = c.vs[vblock];
+    x.pv = pv;
+    x.bad = __ballot(pv < 0) != 0;
+  };
+  auto compute = [&](int32_t tile, Tile& x) {
+    const int64_t t0 = (int64_t)tile * kKeyTile;
+    f32x4 s[NT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const bf16x8 a = kv_widen(x.k[t][i][0], x.k[t][i][1]), b = kv_widen(x.k[t][i][2], x.k[t][i][3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[nt][i][0], s[nt][t], 0, 0, 0);
+          s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, q[nt][i][1], s[nt][t], 0, 0, 0);
+        }
+      }
+    }
+    const bool edge = x.bad || t0 < all_lo || t0 + kKeyTile > all_hi;
+    const int64_t run = t0 + 16 * grp;
+    float vs = x.vs;
+    const float ks = x.ks * p.scale;
+    if (edge) {
+      // What nobody sees counts as code 0 with weight 0, whatever is there.
+      const bool ok = x.pv >= 0;
+      if (!ok) vs = 0.0f;
+      const int32_t lo = (int32_t)min(max(see_lo - run, (int64_t)0), (int64_t)16);
+      const int32_t hi = ok ? (int32_t)min(max(see_hi - run, (int64_t)0), (int64_t)16) : 0;
+      u32x4 keep;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if (4 * e + y >= lo && 4 * e + y < hi) w |= 0xFFu << (8 * y);
+        }
+        keep[e] = w;
+      }
+#pragma unroll
+      for (int i = 0; i < kDt; ++i) x.v[i] &= keep;
+    }
+    bf16x8 w[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float top = -INFINITY;
+      float z[16];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[4 * t + r] = s[nt][t][r] * ks;
+      }
+      if (edge) {
+        const int64_t lo = row_lo[nt] - run, hi = x.pv >= 0 ? row_hi[nt] - run : 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = (e >= lo && e < hi) ? z[e] : -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, z[e]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__ballot(top > m[nt]) != 0) {
+        const float now = fmaxf(m[nt], top);
+        const float f = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
+        m[nt] = now;
+        l[nt] *= f;
+#pragma unroll
+        for (int i = 0; i < kDt; ++i) o[nt][i] *= f;
+      }
+      const float base = m[nt] == -INFINITY ? 0.0f : m[nt];
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float pe = __builtin_amdgcn_exp2f(z[e] - base);
+        sum += pe;
+        w[nt][e >> 3][e & 7] = (__bf16)(pe * vs);
+      }
+      l[nt] += sum;
+    }
+#pragma unroll
+    for (int i = 0; i < kDt; ++i) {
+      const bf16x8 a = kv_widen(x.v[i][0], x.v[i][1]), b = kv_widen(x.v[i][2], x.v[i][3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w[nt][0], o[nt][i], 0, 0, 0);
+        o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, w[nt][1], o[nt][i], 0, 0, 0);
+      }
+    }
+  };
+  for (int32_t tile = tile0 + wave; tile < tile1; tile += 4) {
+    const int64_t t0 = (int64_t)tile * kKeyTile;
+    Tile x;
+    load(tile, page_of(t0 + 16 * k_run), page_of(t0 + 16 * grp), x);
+    compute(tile, x);
+  }
+
+  // Join the four waves: common maximum, then their sums one after another.
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    l[nt] += __shfl_xor(l[nt], 16);
+    l[nt] += __shfl_xor(l[nt], 32);
+    if (grp == 0) {
+      lds_m[wave][nt * 16 + col] = m[nt];
+      lds_l[wave][nt * 16 + col] = l[nt];
+    }
+  }
+  __syncthreads();
+  float f[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float top = -INFINITY;
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][nt * 16 + col]);
+    f[nt] = m[nt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[nt] - top);
+  }
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < kDt; ++i) {
+          f32x4* at = (f32x4*)&lds_o[(nt * 16 + col) * kPitch + i * 16 + 4 * grp];
+          *at = w == 0 ? o[nt][i] * f[nt] : *at + o[nt][i] * f[nt];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int64_t slot = (int64_t)h * p.slots + blockIdx.x;
+  for (int32_t i = threadIdx.x; i < R * (D / 8); i += kThreads) {
+    const int32_t rr = i / (D / 8), d = (i - rr * (D / 8)) * 8, r = wk.first + rr;
+    if (r >= wk.count) continue;
+    const int32_t tok = r / p.group, g = r - tok * p.group;
+    float top = -INFINITY, sum = 0.0f;
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][rr]);
+    for (int w = 0; w < 4; ++w) {
+      if (lds_m[w][rr] != -INFINITY) sum += lds_l[w][rr] * __builtin_amdgcn_exp2f(lds_m[w][rr] - top);
+    }
+    const f32x4 a = *(const f32x4*)&lds_o[rr * kPitch + d], z = *(const f32x4*)&lds_o[rr * kPitch + d + 4];
+    const int64_t head = (int64_t)h * p.group + g, row = wk.row0 + tok;
+    if (wk.splits > 1) {
+      f32x4* to = (f32x4*)(p.part + (slot * R + rr) * D + d);
+      to[0] = a;
+      to[1] = z;
+      if (d == 0) p.part_ml[slot * R + rr] = float2{top, sum};
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      bf16x8 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = (__bf16)(a[e] * inv);
+        y[4 + e] = (__bf16)(z[e] * inv);
+      }
+      *(bf16x8*)(p.out + row * p.o_tok + head * p.o_head + d) = y;
+      if (d == 0 && p.lse) {
+        p.lse[row * ((int64_t)c.heads * p.group) + head] =
+            sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+      }
+    }
+    if (d == 0 && p.rows && wk.split == 0) {
+      p.rows[row * ((int64_t)c.heads * p.group) + head] =
+          int2{(int)((blockIdx.x * R) + rr), wk.splits};
+    }
+  }
+}
+
+// Joins the partial sums of each query row whose keys were split: a wave per
+// row, which finds them through `rows` (first slot times R plus row in tile,
+// and how many slots, one after another).
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv_attend_join(KvBatch bt, KvQuery p, int32_t heads, int32_t R) {
+  constexpr int kV = D / 64;
+  const int32_t lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int32_t all = heads * p.group;
+  if (item >= (int64_t)p.tokens * all) return;
+  const int64_t row = item / all;
+  const int32_t head = (int32_t)(item - row * all);
+  // rows that belong to no sequence stay as they are
+  if (bt.starts && (row < kv_clamp(bt.starts[0], p.tokens) || row >= kv_clamp(bt.starts[bt.count], p.tokens))) return;
+  const int2 at = p.rows[item];
+  const int32_t slot0 = at.x / R, rr = at.x - slot0 * R;
+  if (at.y <= 1 || at.x < 0 || slot0 >= p.slots) return;
+  const int32_t n = min(at.y, p.slots - slot0);
+  const int64_t base = ((int64_t)(head / p.group) * p.slots + slot0) * R + rr;
+  float top = -INFINITY;
+  for (int32_t i = lane; i < n; i += 64) top = fmaxf(top, p.part_ml[base + (int64_t)i * R].x);
+  top = wave_max(top);
+  float sum = 0.0f, acc[kV] = {};
+  if (top != -INFINITY) {
+#pragma unroll 4
+    for (int32_t i = 0; i < n; ++i) {
+      const int64_t e = base + (int64_t)i * R;
+      const float2 ml = p.part_ml[e];
+      const float f = __builtin_amdgcn_exp2f(ml.x - top);
+      sum += ml.y * f;
+      const float* src = p.part + e * D + lane * kV;
+#pragma unroll
+      for (int x = 0; x < kV; ++x) acc[x] += src[x] * f;
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* to = p.out + row * p.o_tok + head * p.o_head + lane * kV;
+#pragma unroll
+  for (int x = 0; x < kV; ++x) to[x] = bf16_down(acc[x] * inv);
+  if (lane == 0 && p.lse) {
+    p.lse[item] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace fp8bq

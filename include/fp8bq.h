@@ -359,6 +359,143 @@ int fp8bq_dequantize_many(const fp8bq_dq_tensor* list, int32_t count, int32_t bm
                           int32_t out_dtype, void* stream);
 
 /*
+ * A paged key/value cache in e4m3, one descale for each page and head.
+ *
+ * The rollout engine that the quantized weights go to also keeps its keys and
+ * values in 8 bits (the FP8 KV-cache of the abstract's stack).  A page of one
+ * head is a block of tokens by channels with one descale, the operation of
+ * fp8bq_quantize on data that arrives token by token:
+ *   fp8bq_kv_append     rotates new keys (and queries) by their positions and
+ *                       stores keys and values
+ *   fp8bq_kv_attention  attends over what is stored
+ *
+ * All pointers in these structs are device pointers, the structs themselves
+ * host memory that is read before the call returns.
+ */
+typedef struct fp8bq_kv_cache {
+  void* k;            /* e4m3fn [num_pages, kv_heads, page_size, head_dim], 16-byte aligned */
+  void* v;            /* e4m3fn [num_pages, kv_heads, head_dim, page_size], 16-byte aligned: a
+                         channel's tokens side by side */
+  float* k_scale;     /* fp32 [num_pages, kv_heads]; positive and finite for every page in use */
+  float* v_scale;
+  int64_t num_pages;  /* 1 .. 2^31 - 1 */
+  int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t kv_heads;   /* 1 .. 65535 */
+  int32_t head_dim;   /* 64, 128, 192 or 256 */
+  int32_t reserved;   /* ignored */
+} fp8bq_kv_cache;
+
+/*
+ * The sequences of a call.  Sequence b holds seq_lens[b] tokens once the
+ * call's own are counted; token p lies in page block_table[b][p / page_size]
+ * at slot p % page_size.  Its own tokens are rows query_start[b] ..
+ * query_start[b + 1] - 1 of the call's inputs (non-decreasing, within 0 ..
+ * tokens), the last ones of the sequence; with query_start NULL every sequence
+ * has one, row b.
+ *
+ * These arrays live on the device and are not checked by the host.  The
+ * kernels read and write nothing outside the buffers whatever they hold:
+ * tokens whose page number is not in 0 .. num_pages - 1, or whose position is
+ * negative or beyond max_pages pages, are neither stored nor seen, and
+ * query_start is clamped to 0 .. tokens.  Rows of no sequence are left as they
+ * are.
+ */
+typedef struct fp8bq_kv_batch {
+  const int32_t* block_table;  /* [count, max_pages], rows table_stride apart */
+  const int32_t* seq_lens;     /* [count] */
+  const int32_t* query_start;  /* [count + 1], or NULL */
+  int64_t table_stride;        /* elements, >= max_pages */
+  int32_t count;               /* sequences, 0 .. 2^20 */
+  int32_t max_pages;           /* columns of the table */
+} fp8bq_kv_batch;
+
+/* New tokens.  Rows are BF16, head_dim contiguous values each, 16-byte
+ * aligned; strides are in elements and multiples of 8. */
+typedef struct fp8bq_kv_tokens {
+  const void* k;      /* [tokens, kv_heads, head_dim] */
+  const void* v;      /* [tokens, kv_heads, head_dim] */
+  const void* q;      /* [tokens, q_heads, head_dim], or NULL */
+  void* q_out;        /* the rotated queries; may be q itself (same strides) */
+  const float* cos;   /* [positions, rot_dim / 2], contiguous, 16-byte aligned */
+  const float* sin;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride;
+  int64_t tokens;     /* tokens * q_heads (or kv_heads without q) <= 2^25 */
+  int64_t positions;  /* rows of cos and sin: tokens at later positions are left out */
+  int32_t q_heads;    /* a multiple of kv_heads */
+  int32_t rot_dim;    /* rotated channels, the first ones: 0 .. head_dim, a multiple of 16 */
+  int32_t interleaved;  /* pairs are channels (i, i + rot_dim/2) if 0, (2i, 2i + 1) if not */
+  int32_t reserved;   /* ignored */
+} fp8bq_kv_tokens;
+
+/*
+ * Append: for the tokens of each sequence at positions p,
+ *   (a, b) -> (a cos[p] - b sin[p], b cos[p] + a sin[p])   for each rotated
+ *             pair of q and k, products and sums each rounded to fp32
+ *   q_out   = BF16 of the rotated q (nearest, ties to even)
+ * and for each (page, head) and for k and v alike,
+ *   fit     = the smallest power of two with 448 * fit >= max(max|x|, FP8BQ_EPS),
+ *             over the call's tokens in the page
+ *   scale'  = max(scale, fit) if the page holds earlier tokens of the sequence
+ *             (slots before the first new one), fit if it does not
+ *   earlier codes c become e4m3fn(c * scale / scale'), new ones
+ *             e4m3fn(clamp(x / scale', -448, 448)), nearest, ties to even
+ * A power of two, unlike the amax / 448 of weights, lets a page's scale grow
+ * without rounding the earlier codes again (other than below e4m3's smallest
+ * normal value).  Slots behind the new tokens keep their bytes.  Values must
+ * be finite: a block with others gets unspecified codes.  A page may belong to
+ * several sequences as long as no more than one of them stores into it in a
+ * call.  fp8bq_dequantize decodes a page's block.
+ * No workspace; one launch; may be captured in a graph.
+ * Returns an fp8bq_status.
+ */
+int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
+                    const fp8bq_kv_tokens* tokens, void* stream);
+
+/* Queries of an attention call, rows as in fp8bq_kv_tokens. */
+typedef struct fp8bq_kv_query {
+  const void* q;      /* BF16 [tokens, q_heads, head_dim] */
+  void* out;          /* BF16 [tokens, q_heads, head_dim]; may be q itself (same strides) */
+  float* lse;         /* fp32 [tokens, q_heads], contiguous: log of the sum of exp(score); or NULL */
+  int64_t q_token_stride, q_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int64_t tokens;     /* tokens * q_heads <= 2^25 */
+  int32_t q_heads;    /* a multiple of kv_heads; query head i reads key head i / (q_heads / kv_heads) */
+  int32_t window;     /* a query sees its own position and the window - 1 before it; 0: all */
+  float scale;        /* of the scores, finite */
+  int32_t reserved;   /* ignored */
+} fp8bq_kv_query;
+
+/* Device workspace bytes of fp8bq_kv_attention (0: none).  They depend on the
+ * shapes alone, not on any length. */
+size_t fp8bq_kv_attention_workspace_bytes(int32_t kv_heads, int32_t head_dim, int32_t q_heads,
+                                          int32_t count, int64_t tokens);
+
+/*
+ * Attention over the cache: for the query at position p of its sequence,
+ *   s_j = scale * (q . decode(k_j) * k_scale)    j <= p, j > p - window
+ *   out = sum_j exp(s_j - max s) decode(v_j) v_scale / sum_j exp(s_j - max s)
+ *   lse = max s + log sum_j exp(s_j - max s)
+ * A query that sees no token gets zeros and lse = -inf.  Scores, maxima and
+ * sums are fp32; the weights exp(s - max) * v_scale are rounded to BF16 before
+ * their product with the values, the output once more.  Any positive scales
+ * are taken, not powers of two alone.  What lies in pages beyond the sequence
+ * is never used, NaN codes included; the codes of a sequence's own tokens must
+ * be finite.
+ *   workspace        device buffer of at least fp8bq_kv_attention_workspace_bytes
+ *   workspace_bytes  bytes, 16-byte aligned, needing no initial value; calls that
+ *                    may overlap (other streams, graphs) need one each
+ * The launch depends on the shapes alone: captured in a graph, it follows
+ * block_table, seq_lens and query_start as they change between replays.
+ * Results do not depend on timing.  Returns an fp8bq_status.
+ */
+int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
+                       const fp8bq_kv_query* query, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
  * The final cast alone (clamp to +-448, round to e4m3fn), for checking the
  * hardware convert over every float32 input.
  *   y  device, fp32 [n];  q  device, uint8 [n];  n >= 0.

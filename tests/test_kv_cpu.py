@@ -1,0 +1,158 @@
+"""The key/value cache's calls without a GPU: every bad argument is refused
+before a device is touched, shapes alone size the workspace, and the plain
+reference that the GPU tests compare with meets the format's definition."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_blockwise_weight_amd as fq
+from fp8_blockwise_weight_amd import kv
+import kv_reference as ref
+
+INVALID, WORKSPACE = fq.ERR_INVALID_ARGUMENT, fq.ERR_WORKSPACE
+no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0,
+                            reason="fake addresses are passed only where no GPU is visible")
+
+# Fake, never dereferenced addresses.
+K, V, KS, VS, TB, LN, ST, A, B, C, D, CO, SI, WS = (0x10_0000_0000 * i for i in range(1, 15))
+
+
+def cache(k=K, v=V, ks=KS, vs=VS, pages=100, size=64, heads=8, dim=128):
+    return kv._CACHE.pack(k, v, ks, vs, pages, size, heads, dim, 0)
+
+
+def batch(table=TB, lens=LN, starts=ST, stride=16, count=4, width=16):
+    return kv._BATCH.pack(table, lens, starts, stride, count, width)
+
+
+def tokens(k=A, v=B, q=C, q_out=D, cos=CO, sin=SI, strides=(1024, 128, 1024, 128, 4096, 128, 4096, 128), tokens=9,
+           positions=4096, q_heads=32, rot=128, interleaved=0):
+    return kv._TOKENS.pack(k, v, q, q_out, cos, sin, *strides, tokens, positions, q_heads, rot, interleaved, 0)
+
+
+def query(q=A, out=B, lse=0, strides=(4096, 128, 4096, 128), tokens=9, q_heads=32, window=0, scale=0.1):
+    return kv._QUERY.pack(q, out, lse, *strides, tokens, q_heads, window, scale, 0)
+
+
+BAD_CACHES = [dict(k=0), dict(v=0), dict(ks=0), dict(vs=0), dict(k=K + 8), dict(v=V + 1), dict(ks=KS + 2),
+              dict(pages=0), dict(pages=1 << 31), dict(size=8), dict(size=48), dict(size=512), dict(heads=0),
+              dict(heads=-1), dict(heads=1 << 16), dict(dim=0), dict(dim=96), dict(dim=320), dict(v=K + 16),
+              dict(ks=K + 64), dict(vs=KS + 4)]
+BAD_BATCHES = [dict(table=0), dict(lens=0), dict(stride=15), dict(width=-1), dict(count=-1), dict(count=1 << 21),
+               dict(table=TB + 2), dict(lens=LN + 1), dict(starts=ST + 2), dict(starts=0)]
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", BAD_CACHES)
+def test_bad_cache(bad):
+    lib = fq.load_library()
+    assert lib.fp8bq_kv_append(cache(**bad), batch(), tokens(), None) == INVALID
+    assert lib.fp8bq_kv_attention(cache(**bad), batch(), query(), WS, 1 << 40, None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", BAD_BATCHES)
+def test_bad_batch(bad):
+    lib = fq.load_library()
+    assert lib.fp8bq_kv_append(cache(), batch(**bad), tokens(), None) == INVALID
+    assert lib.fp8bq_kv_attention(cache(), batch(**bad), query(), WS, 1 << 40, None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [
+    dict(k=0), dict(v=0), dict(k=A + 8), dict(v=B + 2), dict(q_out=0), dict(q=C + 4), dict(q_out=D + 8),
+    dict(strides=(1020, 128, 1024, 128, 4096, 128, 4096, 128)), dict(strides=(1024, 132, 1024, 128, 4096, 128, 4096, 128)),
+    dict(strides=(1024, 128, 1024, 128, 4096, 128, -4096, 128)), dict(tokens=-1), dict(q_heads=0), dict(q_heads=12),
+    dict(rot=-16), dict(rot=24), dict(rot=144), dict(cos=0), dict(sin=0), dict(cos=CO + 4), dict(positions=-1),
+    dict(tokens=1 << 25),
+])
+def test_bad_tokens(bad):
+    assert fq.load_library().fp8bq_kv_append(cache(), batch(), tokens(**bad), None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [
+    dict(q=0), dict(out=0), dict(q=A + 8), dict(out=B + 2), dict(lse=2), dict(strides=(4100, 128, 4096, 128)),
+    dict(strides=(4096, 128, 4096, -128)), dict(tokens=-1), dict(tokens=1 << 25), dict(q_heads=0), dict(q_heads=-8),
+    dict(q_heads=20), dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")),
+])
+def test_bad_query(bad):
+    assert fq.load_library().fp8bq_kv_attention(cache(), batch(), query(**bad), WS, 1 << 40, None) == INVALID
+
+
+@no_gpu
+def test_null_structs_and_workspace():
+    lib = fq.load_library()
+    assert lib.fp8bq_kv_append(None, batch(), tokens(), None) == INVALID
+    assert lib.fp8bq_kv_append(cache(), None, tokens(), None) == INVALID
+    assert lib.fp8bq_kv_append(cache(), batch(), None, None) == INVALID
+    assert lib.fp8bq_kv_attention(None, batch(), query(), WS, 1 << 40, None) == INVALID
+    assert lib.fp8bq_kv_attention(cache(), None, query(), WS, 1 << 40, None) == INVALID
+    assert lib.fp8bq_kv_attention(cache(), batch(), None, WS, 1 << 40, None) == INVALID
+    need = lib.fp8bq_kv_attention_workspace_bytes(8, 128, 32, 4, 9)
+    assert need > 0
+    assert lib.fp8bq_kv_attention(cache(), batch(), query(), None, need, None) == WORKSPACE
+    assert lib.fp8bq_kv_attention(cache(), batch(), query(), WS, need - 1, None) == WORKSPACE
+    assert lib.fp8bq_kv_attention(cache(), batch(), query(), WS + 8, need, None) == WORKSPACE
+
+
+def test_nothing_to_do_touches_no_device():
+    lib = fq.load_library()
+    assert lib.fp8bq_kv_append(cache(), batch(count=0), tokens(), None) == fq.OK
+    assert lib.fp8bq_kv_append(cache(), batch(), tokens(tokens=0), None) == fq.OK
+    assert lib.fp8bq_kv_attention(cache(), batch(count=0), query(), None, 0, None) == fq.OK
+    assert lib.fp8bq_kv_attention(cache(), batch(), query(tokens=0), None, 0, None) == fq.OK
+
+
+def test_workspace_depends_on_shapes_alone():
+    f = fq.load_library().fp8bq_kv_attention_workspace_bytes
+    for bad in ((0, 128, 32, 1, 1), (8, 128, 12, 1, 1), (8, 128, 32, 0, 1), (8, 128, 32, 1, 0), (8, 128, 32, 1, 1 << 40)):
+        assert f(*bad) == 0
+    assert f(8, 128, 32, 1, 1) < 1 << 28
+    assert f(1, 64, 1, 1, 1) > 0
+
+
+def test_struct_sizes():
+    assert (kv._CACHE.size, kv._BATCH.size, kv._TOKENS.size, kv._QUERY.size) == (56, 40, 144, 80)
+
+
+def test_cpu_tensors_are_refused():
+    k = torch.zeros((2, 1, 16, 64), dtype=torch.float8_e4m3fn)
+    v = torch.zeros((2, 1, 64, 16), dtype=torch.float8_e4m3fn)
+    s = torch.ones((2, 1))
+    with pytest.raises(TypeError, match="GPU"):
+        fq.KvCache(k, v, s, s.clone())
+    with pytest.raises(TypeError, match="float8"):
+        fq.KvCache(k.float(), v, s, s)
+    with pytest.raises(ValueError, match="expected"):
+        fq.KvCache(k, k, s, s)
+    with pytest.raises(ValueError, match="page_size"):
+        fq.KvCache(k[:, :, :8].contiguous(), v, s, s)
+    with pytest.raises(ValueError, match="head_dim"):
+        fq.KvCache(k[..., :32].contiguous(), v, s, s)
+    with pytest.raises(ValueError, match="contiguous"):
+        fq.KvCache(k, v.transpose(2, 3), s, s)
+    with pytest.raises(ValueError, match="k_scale"):
+        fq.KvCache(k, v, s[:1], s)
+    with pytest.raises(TypeError, match="4-D"):
+        fq.KvCache(k[0], v, s, s)
+
+
+def test_reference_codes_are_the_format():
+    """Every code decodes and encodes to itself, and midpoints go to even."""
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], dtype=np.uint8)
+    assert np.array_equal(ref.encode(ref.decode(codes)), codes)
+    pos = ref.decode(np.arange(0, 127, dtype=np.uint8))
+    mids = (pos[:-1] + pos[1:]) / 2
+    want = np.arange(0, 126) + (np.arange(0, 126) & 1)
+    assert np.array_equal(ref.encode(mids), want.astype(np.uint8))
+
+
+@pytest.mark.parametrize("amax,want", [(448.0, 1.0), (448.1, 2.0), (224.0, 0.5), (1.0, 2.0 ** -8), (0.0, 2.0 ** -42),
+                                       (3.0e38, 2.0 ** 120), (7.0, 2.0 ** -6), (6.9, 2.0 ** -6), (7.1, 2.0 ** -5)])
+def test_reference_scale(amax, want):
+    s = ref.fit(amax)
+    assert s == want and 448.0 * s >= amax and (amax < 1e-9 or 448.0 * s / 2 < amax)

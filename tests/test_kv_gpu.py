@@ -1,0 +1,566 @@
+"""The key/value cache on the GPU against the plain definitions of
+kv_reference.py: stored bytes, scales and rotated queries equal, attention
+within the error that its documented roundings allow."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def host(cache):
+    """The reference's form of a cache: numpy bytes and scales."""
+    return [cache.k.view(torch.uint8).cpu().numpy().copy(), cache.v.view(torch.uint8).cpu().numpy().copy(),
+            cache.k_scale.cpu().numpy().copy(), cache.v_scale.cpu().numpy().copy()]
+
+
+def same_cache(cache, want):
+    for name, got, exp in zip(("k", "v", "k_scale", "v_scale"), host(cache), want):
+        off = np.argwhere(got.view(np.uint8) != exp.view(np.uint8))
+        assert len(off) == 0, (name, len(off), off[:4].tolist())
+
+
+def random_cache(fq, g, pages, heads, size, dim, pow2=True):
+    """Finite codes everywhere, mixed scales."""
+    def codes(*shape):
+        c = torch.randint(0, 256, shape, generator=g, dtype=torch.uint8)
+        c[(c & 0x7F) == 0x7F] = 0x38
+        return c.to(DEV).view(torch.float8_e4m3fn)
+
+    def scales():
+        s = torch.exp2(torch.randint(-9, -5, (pages, heads), generator=g).float())
+        return (s if pow2 else s * (1 + 0.9 * torch.rand((pages, heads), generator=g))).to(DEV)
+
+    return fq.KvCache(codes(pages, heads, size, dim), codes(pages, heads, dim, size), scales(), scales())
+
+
+def tables(g, counts, width, pages):
+    order = torch.randperm(pages, generator=g).tolist()
+    rows, at = [], 0
+    for c in counts:
+        rows.append(order[at:at + c] + [-1] * (width - c))
+        at += c
+    return rows
+
+
+def rotation(positions, rot):
+    half = rot // 2
+    a = np.arange(positions)[:, None] * 10000.0 ** (-np.arange(half) / max(1, half))
+    return np.cos(a).astype(np.float32), np.sin(a).astype(np.float32)
+
+
+def starts_of(new):
+    return [0] + list(np.cumsum(new))
+
+
+# ---------------------------------------------------------------- append
+
+APPEND = [
+    # dim, page, heads, group, rot, interleaved, lens, new
+    (128, 64, 2, 4, 128, False, [1, 64, 65, 200, 7], None),
+    (64, 16, 3, 1, 32, True, [16, 17, 33, 1], None),
+    (192, 32, 1, 5, 192, False, [31, 32, 33], None),
+    (256, 256, 2, 2, 64, True, [300, 256, 5], None),
+    (128, 128, 1, 1, 0, False, [129, 128], None),
+    (128, 64, 2, 4, 128, False, [64, 65, 200, 7, 130], [64, 1, 150, 7, 2]),
+    (64, 16, 5, 3, 32, True, [100, 16, 33, 9, 50], [100, 3, 17, 0, 33]),
+    (192, 32, 2, 1, 96, False, [70, 1, 64], [70, 1, 32]),
+    (256, 256, 1, 2, 256, False, [513, 256], [300, 256]),
+    (256, 16, 1, 1, 16, True, [40], [39]),
+    (128, 128, 4, 8, 128, True, [255, 1], [250, 1]),
+]
+
+
+def append_inputs(g, T, heads, group, dim, spread=1.0):
+    qkv = torch.randn((T, heads * (group + 2) * dim), generator=g)
+    qkv = (qkv * torch.exp(spread * torch.randn((T, 1), generator=g))).to(torch.bfloat16)
+    at = heads * group * dim
+    q = qkv[:, :at].view(T, heads * group, dim)
+    k = qkv[:, at:at + heads * dim].view(T, heads, dim)
+    v = qkv[:, at + heads * dim:].view(T, heads, dim)
+    return qkv, q, k, v
+
+
+@pytest.mark.parametrize("dim,page,heads,group,rot,interleaved,lens,new", APPEND)
+def test_append_equals_the_definition(gpu_lib, dim, page, heads, group, rot, interleaved, lens, new):
+    fq, g = gpu_lib, torch.Generator().manual_seed(dim + page + len(lens))
+    one = new is None
+    n = [1] * len(lens) if one else new
+    starts = starts_of(n)
+    width = max(-(-x // page) for x in lens)
+    table = tables(g, [-(-x // page) for x in lens], width, len(lens) * width + 2)
+    cache = random_cache(fq, g, len(lens) * width + 2, heads, page, dim)
+    want = host(cache)
+    qkv, q, k, v = append_inputs(g, starts[-1], heads, group, dim)
+    cos, sin = rotation(max(lens), rot)
+    q_want = torch.zeros_like(q)
+    ref.append(want, k, v, table, lens, starts, q, q_want, cos, sin, interleaved)
+    d = qkv.to(DEV)
+    T, at = starts[-1], heads * group * dim
+    dq = d[:, :at].view(T, heads * group, dim)
+    dk = d[:, at:at + heads * dim].view(T, heads, dim)
+    dv = d[:, at + heads * dim:].view(T, heads, dim)
+    got = fq.kv_append(cache, dk, dv, i32(table), i32(lens), None if one else i32(starts), q=dq,
+                       cos=torch.from_numpy(cos).to(DEV) if rot else None,
+                       sin=torch.from_numpy(sin).to(DEV) if rot else None, interleaved=interleaved)
+    torch.cuda.synchronize()
+    same_cache(cache, want)
+    assert torch.equal(got.cpu().view(torch.int16), q_want.view(torch.int16))
+    assert torch.equal(d.cpu().view(torch.int16), qkv.view(torch.int16))
+    # the queries in place, within the projection's output, and the same again
+    out = fq.kv_append(cache, dk, dv, i32(table), i32(lens), None if one else i32(starts), q=dq, q_out=dq,
+                       cos=torch.from_numpy(cos).to(DEV) if rot else None,
+                       sin=torch.from_numpy(sin).to(DEV) if rot else None, interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert out is dq
+    assert torch.equal(dq.cpu().view(torch.int16), q_want.view(torch.int16))
+    assert torch.equal(d[:, at:].cpu().view(torch.int16), qkv[:, at:].view(torch.int16))
+    same_cache(cache, want)
+
+
+@pytest.mark.parametrize("dim,page,step", [(128, 64, 1), (64, 16, 1), (192, 128, 1), (128, 64, 5), (256, 32, 7)])
+def test_page_grows_token_by_token(gpu_lib, dim, page, step):
+    """Magnitudes that double again and again: the earlier codes of the page
+    follow the scale at each call, through the subnormal codes to zero."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(7)
+    heads, total = 2, page + page // 2
+    width = -(-total // page)
+    table = [list(range(width))]
+    cache = random_cache(fq, g, width, heads, page, dim)
+    want = host(cache)
+    k = (torch.randn((total, heads, dim), generator=g) * torch.exp2(torch.arange(total) / 3.0)[:, None, None]).to(torch.bfloat16)
+    v = (torch.randn((total, heads, dim), generator=g) * torch.exp2(torch.arange(total) / 2.0 - 9)[:, None, None]).to(torch.bfloat16)
+    for at in range(0, total, step):
+        n = min(step, total - at)
+        kk, vv = k[at:at + n], v[at:at + n]
+        ref.append(want, kk, vv, table, [at + n], [0, n])
+        assert fq.kv_append(cache, kk.to(DEV), vv.to(DEV), i32(table), i32([at + n]),
+                            None if step == 1 else i32([0, n])) is None
+    torch.cuda.synchronize()
+    same_cache(cache, want)
+    # a page decodes as the package's dequantize decodes any block
+    x = fq.dequantize(cache.k[0, 1], cache.k_scale[0, 1].view(1, 1), (page, dim))
+    assert np.array_equal(x.cpu().numpy(), (ref.decode(want[0][0, 1]) * want[2][0, 1]).astype(np.float32))
+
+
+def test_power_of_two_growth_rounds_once(gpu_lib):
+    """Codes of a page filled token by token equal those of the whole page
+    stored at once wherever they are normal numbers at every step."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(11)
+    S, D = 64, 128
+    x = ((1 + torch.rand((S, 1, D), generator=g)) * torch.exp2(torch.arange(S) / 16.0)[:, None, None]).to(torch.bfloat16).to(DEV)
+    one, all_ = (fq.KvCache.empty(1, 1, D, S, device=DEV) for _ in range(2))
+    table = i32([[0]])
+    fq.kv_append(all_, x, x, table, i32([S]), i32([0, S]))
+    for t in range(S):
+        fq.kv_append(one, x[t:t + 1], x[t:t + 1], table, i32([t + 1]))
+    torch.cuda.synchronize()
+    same_cache(one, host(all_))
+
+
+@pytest.mark.parametrize("single", [True, False])
+def test_append_leaves_out_what_has_no_place(gpu_lib, single):
+    """Pages that are none, positions beyond the table, beyond the rotation's
+    rows or below zero, sequences of no tokens, rows of no sequence: nothing of
+    theirs is stored, everything else is."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(3)
+    D, S, heads, group, pages, width = 64, 16, 2, 2, 12, 3
+    cache = random_cache(fq, g, pages, heads, S, D)
+    want = host(cache)
+    table = [[0, 1, -1], [2, 99, 3], [4, -2147483648, 2147483647], [5, 6, 7], [8, 12, 9], [10, 11, 3]]   # 3: read by two, stored by one
+    lens = [33, 20, 40, 100, 0, 48]
+    new = [1] * 6 if single else [20, 9, 40, 60, 3, 17]
+    starts = starts_of(new)
+    if not single:
+        starts = [s + 2 for s in starts]            # two rows before the first sequence, three behind the last
+    T = starts[-1] + (0 if single else 3)
+    _, q, k, v = append_inputs(g, T, heads, group, D)
+    cos, sin = rotation(46, 64)
+    marker = torch.full((T, heads * group, D), 7.0, dtype=torch.bfloat16)
+    q_want = marker.clone()
+    ref.append(want, k, v, table, lens, starts, q, q_want, cos, sin)
+    got = marker.to(DEV)
+    fq.kv_append(cache, k.to(DEV), v.to(DEV), i32(table), i32(lens), None if single else i32(starts), q=q.to(DEV),
+                 q_out=got, cos=torch.from_numpy(cos).to(DEV), sin=torch.from_numpy(sin).to(DEV))
+    torch.cuda.synchronize()
+    same_cache(cache, want)
+    assert torch.equal(got.cpu().view(torch.int16), q_want.view(torch.int16))
+
+
+# -------------------------------------------------------------- attention
+
+def check_attention(fq, cache, q, table, lens, starts, one, **kw):
+    out, lse, tol, tol_lse = ref.attention(host(cache), q, table, lens, starts, **kw)
+    dq = q.to(DEV)
+    got, got_lse = fq.kv_attention(cache, dq, i32(table), i32(lens), None if one else i32(starts), return_lse=True, **kw)
+    again = fq.kv_attention(cache, dq, i32(table), i32(lens), None if one else i32(starts), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+    got, got_lse = got.cpu().double(), got_lse.cpu().double()
+    rows = [r for b in range(len(lens)) for r in range(starts[b], starts[b + 1])]
+    off = (got[rows] - out[rows]).abs()
+    assert not torch.isnan(off).any()
+    assert (off <= tol[rows]).all(), float((off / tol[rows]).max())
+    empty = torch.isinf(lse[rows])
+    assert torch.equal(empty, torch.isinf(got_lse[rows])) and (got_lse[rows][empty] < 0).all()
+    off = (got_lse[rows] - lse[rows])[~empty].abs()
+    assert (off <= tol_lse[rows][~empty]).all()
+    return got
+
+
+ATTENTION = [
+    # dim, page, heads, group, lens, new, window
+    (128, 64, 2, 4, [1, 64, 65, 300, 2], None, 0),
+    (64, 16, 3, 1, [1, 16, 17, 63, 129], None, 0),
+    (192, 32, 1, 5, [31, 257], None, 0),
+    (256, 256, 2, 2, [1, 255, 513], None, 0),
+    (128, 128, 1, 16, [129, 1000], None, 0),
+    (64, 64, 1, 37, [200, 3], None, 0),                 # more query heads than a tile's rows
+    (128, 16, 2, 3, [700, 5], None, 100),
+    (64, 16, 2, 1, [500, 64, 65], None, 1),
+    (128, 64, 2, 4, [300, 70, 9, 64], [5, 3, 9, 1], 0),
+    (64, 32, 1, 7, [129, 33, 10], [29, 33, 0], 0),
+    (192, 16, 2, 2, [90, 200], [17, 40], 33),
+    (256, 128, 1, 1, [300], [70], 0),
+    (128, 64, 1, 8, [200, 131], [150, 131], 0),         # prompts
+    (128, 64, 2, 2, [330], [257], 64),
+    (64, 64, 1, 1, [400], [400], 0),
+]
+
+
+@pytest.mark.parametrize("pow2", [True, False])
+@pytest.mark.parametrize("dim,page,heads,group,lens,new,window", ATTENTION)
+def test_attention_within_its_roundings(gpu_lib, dim, page, heads, group, lens, new, window, pow2):
+    fq, g = gpu_lib, torch.Generator().manual_seed(dim + page + sum(lens))
+    one = new is None
+    starts = starts_of([1] * len(lens) if one else new)
+    width = max(-(-x // page) for x in lens)
+    pages = len(lens) * width + 1
+    cache = random_cache(fq, g, pages, heads, page, dim, pow2)
+    table = tables(g, [-(-x // page) for x in lens], width, pages)
+    q = torch.randn((starts[-1], heads * group, dim), generator=g).to(torch.bfloat16)
+    check_attention(fq, cache, q, table, lens, starts, one, window=window)
+
+
+@pytest.mark.parametrize("length", [5000, 20001])
+def test_attention_split_over_a_long_sequence(gpu_lib, length):
+    fq, g = gpu_lib, torch.Generator().manual_seed(5)
+    cache = random_cache(fq, g, -(-length // 64) + 1, 1, 64, 128)
+    table = tables(g, [-(-length // 64)], -(-length // 64), cache.num_pages)
+    q = torch.randn((1, 8, 128), generator=g).to(torch.bfloat16)
+    check_attention(fq, cache, q, table, [length], [0, 1], True)
+    q = torch.randn((3, 8, 128), generator=g).to(torch.bfloat16)
+    check_attention(fq, cache, q, table, [length], [0, 3], False, scale=0.05)
+
+
+def test_attention_of_many_sequences(gpu_lib):
+    """More than 64 sequences, two rounds of the planning scan, mixed lengths
+    and some without tokens."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(6)
+    n = 150
+    lens = [(37 * b) % 210 for b in range(n)]
+    counts = [-(-x // 16) for x in lens]
+    cache = random_cache(fq, g, sum(counts) + 1, 1, 16, 64)
+    table = tables(g, counts, max(counts), cache.num_pages)
+    q = torch.randn((n, 2, 64), generator=g).to(torch.bfloat16)
+    got = check_attention(fq, cache, q, table, lens, list(range(n + 1)), True)
+    assert (got[[b for b in range(n) if lens[b] == 0]] == 0).all()
+    new = [min(lens[b], b % 5) for b in range(n)]
+    starts = starts_of(new)
+    q = torch.randn((starts[-1], 2, 64), generator=g).to(torch.bfloat16)
+    check_attention(fq, cache, q, table, lens, starts, False)
+
+
+@pytest.mark.parametrize("one", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_what_no_query_sees_has_no_effect(gpu_lib, one, dim):
+    """NaN codes and NaN scales in slots behind the sequence, in pages of
+    nobody, below the window, and page numbers that are none: the tokens that
+    are there count, nothing else does; a row that sees nothing is zero."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(8)
+    S = 16
+    cache = random_cache(fq, g, 24, 2, S, dim)
+    table = [[0, 1, 2, 3, 4, 5], [6, -1, 7, 99, 8, 9], [10, 11, 2147483647, -5, 12, 13], [-1] * 6, [14, 15, 16, 17, 18, 19]]
+    lens, window = [37, 96, 61, 50, 200], 70
+    new = [1] * 5 if one else [3, 20, 1, 2, 120]
+    starts = starts_of(new)
+    kb, vb = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    used = {(p, j) for b in range(5) for j, p in enumerate(table[b]) if 0 <= p < 24}
+    clean = set()
+    for b in range(5):
+        lo = max(0, lens[b] - new[b] + 1 - window)
+        for j, p in enumerate(table[b]):
+            if not 0 <= p < 24:
+                continue
+            for s in range(S):
+                if lo <= j * S + s < lens[b]:
+                    clean.add((p, s))
+    for p in range(24):
+        for s in range(S):
+            if (p, s) not in clean:
+                kb[p, :, s] = 0x7F
+                vb[p, :, :, s] = 0xFF
+        if not any((p, s) in clean for s in range(S)):
+            cache.k_scale[p] = float("nan")
+            cache.v_scale[p] = float("inf")
+    assert used
+    q = torch.randn((starts[-1], 6, dim), generator=g).to(torch.bfloat16)
+    got = check_attention(fq, cache, q, table, lens, starts, one, window=window)
+    assert (got[starts[3]:starts[4]] == 0).all()
+
+
+def test_more_query_tokens_than_the_sequence_holds(gpu_lib):
+    """Rows before a sequence's first token see nothing; rows of no sequence
+    keep what they hold, in every output."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(9)
+    cache = random_cache(fq, g, 6, 1, 16, 64)
+    lens, starts, table = [3, 20], [2, 9, 12], [[0, 1], [2, 3]]
+    q = torch.randn((15, 4, 64), generator=g).to(torch.bfloat16)
+    want, lse, tol, _ = ref.attention(host(cache), q, table, lens, starts)
+    out = torch.full((15, 4, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    ls = torch.full((15, 4), 9.0, device=DEV)
+    fq.kv_attention(cache, q.to(DEV), i32(table), i32(lens), i32(starts), out=out, lse=ls)
+    torch.cuda.synchronize()
+    assert (out[:2] == 5).all() and (out[12:] == 5).all() and (ls[:2] == 9).all() and (ls[12:] == 9).all()
+    assert (out[2:6] == 0).all() and torch.isinf(ls[2:6]).all()
+    assert ((out.cpu().double() - want).abs()[2:12] <= tol[2:12]).all()
+
+
+def test_starts_that_are_no_offsets_stay_in_bounds(gpu_lib):
+    """query_start is clamped: negative, decreasing and far values reach no
+    memory outside the buffers (their rows are unspecified)."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(10)
+    pad = 4
+    cache = random_cache(fq, g, 8, 2, 16, 64)
+    before = host(cache)
+    buf = torch.full((pad + 9 + pad, 4, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    q = torch.randn((9, 4, 64), generator=g).to(torch.bfloat16).to(DEV)
+    kv = q[:, :2].contiguous()
+    table = i32([[0, 1], [2, 3], [4, 5]])
+    for starts in ([-5, 3, 2, 1 << 30], [9, 0, 9, 0], [1 << 30, -1, 1 << 30, 4], [4, 4, 4, 4]):
+        for lens in ([20, 30, 7], [-3, 1 << 30, 0]):
+            fq.kv_attention(cache, q, table, i32(lens), i32(starts), out=buf[pad:pad + 9])
+            fq.kv_append(cache, kv, kv, table, i32(lens), i32(starts), q=q, q_out=buf[pad:pad + 9])
+    torch.cuda.synchronize()
+    assert (buf[:pad] == 3).all() and (buf[pad + 9:] == 3).all()
+    after = host(cache)
+    for a, b in zip(before, after):
+        assert np.array_equal(a[6:].view(np.uint8), b[6:].view(np.uint8))
+
+
+def test_strided_rows_and_in_place_output(gpu_lib):
+    fq, g = gpu_lib, torch.Generator().manual_seed(12)
+    cache = random_cache(fq, g, 10, 2, 32, 128)
+    lens, starts, table = [70, 40], [0, 6, 8], [[0, 1, 2], [3, 4, 5]]
+    q = torch.randn((8, 8, 128), generator=g).to(torch.bfloat16)
+    want = fq.kv_attention(cache, q.to(DEV), i32(table), i32(lens), i32(starts))
+    wide = torch.zeros((8, 12, 136), dtype=torch.bfloat16, device=DEV)
+    wide[:, 2:10, 8:] = q.to(DEV)
+    view = wide[:, 2:10, 8:]
+    heads_first = q.to(DEV).transpose(0, 1).contiguous().transpose(0, 1)
+    big = torch.full((2, 5), -7, dtype=torch.int32, device=DEV)
+    big[:, :3] = i32(table)
+    got = fq.kv_attention(cache, view, big[:, :3], i32(lens), i32(starts))
+    got2 = fq.kv_attention(cache, heads_first, i32(table), i32(lens), i32(starts), out=torch.empty_like(heads_first))
+    assert torch.equal(got, want) and torch.equal(got2, want)
+    back = fq.kv_attention(cache, view, i32(table), i32(lens), i32(starts), out=view)
+    torch.cuda.synchronize()
+    assert torch.equal(back, want)
+    wide[:, 2:10, 8:] = 0
+    assert (wide == 0).all()
+
+
+def test_offsets_beyond_32_bits(gpu_lib):
+    """Blocks that lie more than 2^32 bytes into the cache."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(13)
+    heads, S, D = 8, 256, 256
+    pages = (1 << 32) // (heads * S * D) + 4
+    cache = fq.KvCache(*(torch.empty(s, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+                         for s in ((pages, heads, S, D), (pages, heads, D, S))),
+                       torch.ones((pages, heads), device=DEV), torch.ones((pages, heads), device=DEV))
+    small = fq.KvCache.empty(4, heads, D, S, device=DEV)
+    lens, starts = [300, 258], [0, 300, 303]
+    k, v = (torch.randn((303, heads, D), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    q = torch.randn((303, heads, D), generator=g).to(torch.bfloat16).to(DEV)
+    far = [[pages - 1, pages - 3], [pages - 2, pages - 4]]
+    near = [[3, 1], [2, 0]]
+    for b in (0, 1):
+        small.k[near[b][0]].zero_()
+        cache.k[far[b][0]].zero_()
+        cache.v[far[b][0]].zero_()
+        cache.k[far[b][1]].zero_()
+        cache.v[far[b][1]].zero_()
+    outs = []
+    for c, table in ((cache, far), (small, near)):
+        fq.kv_append(c, k, v, i32(table), i32(lens), i32(starts))
+        fq.kv_append(c, k[:2], v[:2], i32(table), i32([301, 259]))
+        outs.append(fq.kv_attention(c, q, i32(table), i32(lens), i32(starts)))
+        outs.append(fq.kv_attention(c, q[:2], i32(table), i32([301, 259])))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    for b in (0, 1):
+        for x, y in zip(far[b], near[b]):
+            assert torch.equal(cache.k[x].view(torch.uint8), small.k[y].view(torch.uint8))
+            assert torch.equal(cache.v[x].view(torch.uint8), small.v[y].view(torch.uint8))
+
+
+# ------------------------------------------------------------ run together
+
+def test_prompt_steps_and_drafts_together(gpu_lib):
+    """As a rollout runs them: prompts enter the cache, then single tokens,
+    then drafted tokens of which some are taken back; every attention is that
+    of the tokens stored so far, in 64 bits."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(14)
+    dim, page, heads, group = 128, 32, 2, 4
+    B, width = 3, 5
+    cache = fq.KvCache.empty(B * width + 1, heads, dim, page, device=DEV)
+    want = host(cache)
+    table = tables(g, [width] * B, width, B * width + 1)
+    cos, sin = rotation(160, 128)
+    dcos, dsin = torch.from_numpy(cos).to(DEV), torch.from_numpy(sin).to(DEV)
+    lens = [0] * B
+    for new, taken in (([70, 5, 33], None), ([1] * 3, None), ([1] * 3, None), ([4, 1, 6], [2, 1, 0]), ([1] * 3, None),
+                       ([0, 3, 8], None)):
+        starts = starts_of(new)
+        lens = [a + b for a, b in zip(lens, new)]
+        one = new == [1] * B
+        _, q, k, v = append_inputs(g, starts[-1], heads, group, dim, 0.3)
+        q_want = torch.zeros_like(q)
+        ref.append(want, k, v, table, lens, starts, q, q_want, cos, sin)
+        ds = None if one else i32(starts)
+        turned = fq.kv_append(cache, k.to(DEV), v.to(DEV), i32(table), i32(lens), ds, q=q.to(DEV), cos=dcos, sin=dsin)
+        assert torch.equal(turned.cpu().view(torch.int16), q_want.view(torch.int16))
+        got = fq.kv_attention(cache, turned, i32(table), i32(lens), ds)
+        out, _, tol, _ = ref.attention(want, q_want, table, lens, starts)
+        torch.cuda.synchronize()
+        same_cache(cache, want)
+        assert ((got.cpu().double() - out).abs() <= tol).all()
+        if taken is not None:
+            lens = [n - a + t for n, a, t in zip(lens, new, taken)]
+
+
+def test_captured_step_follows_the_lengths(gpu_lib):
+    """One graph of a decoding step (append, then attention), replayed while
+    the sequences grow across pages, equals the eager calls each time; two
+    graphs on streams of their own do not disturb each other."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(15)
+    dim, page, heads, group, B, width = 128, 16, 2, 4, 5, 8
+    cos, sin = (torch.from_numpy(x).to(DEV) for x in rotation(width * page, 128))
+    table = i32(tables(g, [width] * B, width, B * width))
+    sets = []
+    for i in range(2):
+        cache, eager = (fq.KvCache.empty(B * width, heads, dim, page, device=DEV) for _ in range(2))
+        lens = i32([1 + 7 * i, 15, 16, 30, 2])
+        qkv = torch.zeros((B, heads * (group + 2), dim), dtype=torch.bfloat16, device=DEV)
+        q, k, v = qkv[:, :heads * group], qkv[:, heads * group:heads * (group + 1)], qkv[:, heads * (group + 1):]
+        turned = torch.empty((B, heads * group, dim), dtype=torch.bfloat16, device=DEV)
+        out = torch.empty_like(turned)
+        ws = torch.empty(max(16, fq.kv_attention_workspace_bytes(cache, heads * group, B, B)), dtype=torch.uint8, device=DEV)
+        stream = torch.cuda.Stream()
+
+        def step(c, o):
+            fq.kv_append(c, k, v, table, lens, q=q, q_out=turned, cos=cos, sin=sin)
+            fq.kv_attention(c, turned, table, lens, out=o, workspace=ws)
+
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            step(cache, out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(cache, out)
+        for c in (cache, eager):
+            c.k.view(torch.uint8).zero_()
+            c.v.view(torch.uint8).zero_()
+        sets.append((graph, stream, cache, eager, lens, qkv, out, q, k, v))
+    torch.cuda.synchronize()
+    for _ in range(12):
+        for graph, stream, cache, eager, lens, qkv, out, *_ in sets:
+            qkv.copy_(torch.randn(qkv.shape, generator=g).to(torch.bfloat16))
+        torch.cuda.synchronize()
+        for graph, stream, *_ in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, stream, cache, eager, lens, qkv, out, q, k, v in sets:
+            t = fq.kv_append(eager, k, v, table, lens, q=q, cos=cos, sin=sin)
+            want = fq.kv_attention(eager, t, table, lens)
+            torch.cuda.synchronize()
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+            same_cache(cache, host(eager))
+            lens += 3
+        torch.cuda.synchronize()
+
+
+def test_side_stream(gpu_lib):
+    """Work goes to the current stream, in order with the caller's other work."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(16)
+    cache = random_cache(fq, g, 40, 4, 64, 128)
+    table, lens = i32([list(range(20)), list(range(20, 40))]), i32([1270, 1100])
+    q = torch.randn((2, 16, 128), generator=g).to(torch.bfloat16).to(DEV)
+    want = fq.kv_attention(cache, q, table, lens)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        x = torch.zeros_like(q)
+        for _ in range(20):
+            x.copy_(q * 0.5)
+            x.add_(x)
+            got = fq.kv_attention(cache, x, table, lens)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+# ----------------------------------------------------------------- refusals
+
+def test_refusals(gpu_lib):
+    fq = gpu_lib
+    cache = fq.KvCache.empty(4, 2, 64, 16, device=DEV)
+    table, lens, starts = i32([[0, 1]]), i32([5]), i32([0, 3])
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16, device=DEV)
+    cos = torch.zeros((8, 32), device=DEV)
+    ap = lambda k=x, v=x, tb=table, ln=lens, st=starts, **kw: fq.kv_append(cache, k, v, tb, ln, st, **kw)  # noqa: E731
+    at = lambda q=q, tb=table, ln=lens, st=starts, **kw: fq.kv_attention(cache, q, tb, ln, st, **kw)       # noqa: E731
+    ap()
+    at()
+    for call in (lambda: ap(k=x.float()), lambda: at(q=q.half()), lambda: ap(tb=table.long()), lambda: at(ln=lens.long()),
+                 lambda: at(st=starts.long()), lambda: ap(cos=cos.half(), sin=cos.half())):
+        with pytest.raises(TypeError):
+            call()
+    odd = torch.zeros((3, 2, 68), dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: ap(k=x[:2]), lambda: ap(v=x[:, :1]), lambda: ap(st=None), lambda: at(st=None),
+                 lambda: ap(k=odd[:, :, 4:]), lambda: ap(k=x.transpose(1, 2).contiguous().transpose(1, 2)),
+                 lambda: at(q=q[:, :3]), lambda: at(q=q[:, :, :32]), lambda: at(window=-1), lambda: at(window=1 << 31),
+                 lambda: at(scale=float("nan")), lambda: at(scale=1e39), lambda: ap(cos=cos), lambda: ap(sin=cos),
+                 lambda: ap(cos=cos[:, :4].contiguous(), sin=cos[:, :4].contiguous()), lambda: ap(cos=cos, sin=cos[:4]),
+                 lambda: ap(cos=torch.zeros((8, 40), device=DEV), sin=torch.zeros((8, 40), device=DEV)),
+                 lambda: ap(q_out=q), lambda: ap(q=q[:, :3]), lambda: ap(q=q, q_out=q[:2]),
+                 lambda: ap(q=q, q_out=q[:1].expand(3, 4, 64)), lambda: at(out=q[:, :1].expand(3, 4, 64)),
+                 lambda: at(tb=table[0]), lambda: at(tb=i32([[0], [1]])), lambda: at(tb=i32([[0, 1], [2, 3]]).t()[:1]),
+                 lambda: at(st=i32([0, 1, 3])), lambda: ap(k=x.cpu()), lambda: at(tb=table.cpu()), lambda: at(st=starts.cpu()),
+                 lambda: at(lse=torch.zeros((3, 3), device=DEV)), lambda: at(workspace=torch.zeros(64, dtype=torch.uint8)),
+                 lambda: fq.KvCache.empty(1, 1, 64, 24, device=DEV), lambda: fq.KvCache.empty(0, 1, 64, 16, device=DEV)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    with pytest.raises(fq.Fp8bqError, match="workspace"):
+        at(workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    empty = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device=DEV)
+    assert at(q=empty, st=i32([0, 0])).shape == (0, 4, 64)
+    assert ap(k=empty[:, :2], v=empty[:, :2], st=i32([0, 0])) is None
+    none = torch.zeros((0, 2), dtype=torch.int32, device=DEV)
+    assert at(q=empty, tb=none, ln=i32([]), st=None).shape == (0, 4, 64)
+    assert (at(q=q, tb=torch.zeros((1, 0), dtype=torch.int32, device=DEV)) == 0).all()
+    torch.cuda.synchronize()
+    assert math.isfinite(float(at().float().sum()))
