@@ -22,6 +22,7 @@ bool kv_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 // Grids and in-kernel row numbers stay in 32 bits.
 constexpr int64_t kKvMaxRows = int64_t{1} << 25;   // query tokens x query heads
 constexpr int32_t kKvMaxBatch = 1 << 20;
+constexpr int64_t kKvMaxBlocks = int64_t{1} << 22;  // sequences x key/value heads
 
 bool kv_cache_ok(const fp8bq_kv_cache* c) {
   if (c == nullptr || kv_log2_page(c->page_size) < 0) return false;
@@ -99,7 +100,7 @@ KvShape kv_shape(int32_t kv_heads, int32_t dim, int32_t q_heads, int32_t count, 
   KvShape s;
   s.group = q_heads / kv_heads;
   const int64_t per_seq = ceil_div(tokens * s.group, count);
-  s.rows = per_seq <= 16 ? 16 : 32;
+  s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 ? 64 : 128));
   const int64_t base = tokens * s.group / s.rows + count;
   s.target = base * kv_heads >= 4096 ? 0 : static_cast<int32_t>(ceil_div(1024, kv_heads));
   s.min_tiles = 4;
@@ -111,8 +112,11 @@ KvShape kv_shape(int32_t kv_heads, int32_t dim, int32_t q_heads, int32_t count, 
   return s;
 }
 
-bool kv_heads_ok(int32_t q_heads, int32_t kv_heads, int64_t tokens) {
-  return q_heads >= 1 && q_heads % kv_heads == 0 && tokens <= kKvMaxRows / q_heads;
+// A grid of `slots` workgroups per head stays below 2^32 work-items for
+// count * kv_heads <= 2^22 (slots <= rows / 16 + count + 1024 / kv_heads + 1).
+bool kv_heads_ok(int32_t q_heads, int32_t kv_heads, int32_t count, int64_t tokens) {
+  return q_heads >= 1 && q_heads % kv_heads == 0 && tokens <= kKvMaxRows / q_heads &&
+         static_cast<int64_t>(count) * kv_heads <= kKvMaxBlocks;
 }
 
 }  // namespace
@@ -123,7 +127,7 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
                     void* stream) {
   if (!kv_cache_ok(cache) || t == nullptr || !kv_batch_ok(batch, t->tokens)) return FP8BQ_ERR_INVALID_ARGUMENT;
   if (t->rot_dim < 0 || t->rot_dim > cache->head_dim || t->rot_dim % 16 != 0) return FP8BQ_ERR_INVALID_ARGUMENT;
-  if (!kv_heads_ok(t->q ? t->q_heads : cache->kv_heads, cache->kv_heads, t->tokens)) {
+  if (!kv_heads_ok(t->q ? t->q_heads : cache->kv_heads, cache->kv_heads, batch->count, t->tokens)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   if (batch->count == 0 || t->tokens == 0) return FP8BQ_OK;
@@ -183,14 +187,14 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
 
 size_t fp8bq_kv_attention_workspace_bytes(int32_t kv_heads, int32_t head_dim, int32_t q_heads, int32_t count,
                                           int64_t tokens) {
-  if (kv_heads < 1 || count < 1 || tokens < 1 || !kv_heads_ok(q_heads, kv_heads, tokens)) return 0;
+  if (kv_heads < 1 || count < 1 || tokens < 1 || !kv_heads_ok(q_heads, kv_heads, count, tokens)) return 0;
   return kv_shape(kv_heads, head_dim, q_heads, count, tokens).bytes;
 }
 
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, const fp8bq_kv_query* q,
                        void* workspace, size_t workspace_bytes, void* stream) {
   if (!kv_cache_ok(cache) || q == nullptr || !kv_batch_ok(batch, q->tokens)) return FP8BQ_ERR_INVALID_ARGUMENT;
-  if (!kv_heads_ok(q->q_heads, cache->kv_heads, q->tokens) || q->window < 0 || !(q->scale - q->scale == 0.0f)) {
+  if (!kv_heads_ok(q->q_heads, cache->kv_heads, batch->count, q->tokens) || q->window < 0 || !(q->scale - q->scale == 0.0f)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   if (batch->count == 0 || q->tokens == 0) return FP8BQ_OK;
@@ -229,11 +233,12 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   hipStream_t st = static_cast<hipStream_t>(stream);
   kv_for_dim(cache->head_dim, [&](auto dim) {
     constexpr int D = decltype(dim)::value;
-    const dim3 grid(static_cast<unsigned>(s.slots), static_cast<unsigned>(cache->kv_heads));
-    if (s.rows == 16) {
-      hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 1>), grid, dim3(fp8bq::kThreads), 0, st, c, b, d);
-    } else {
-      hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 2>), grid, dim3(fp8bq::kThreads), 0, st, c, b, d);
+    const dim3 grid(static_cast<unsigned>(s.slots) * static_cast<unsigned>(cache->kv_heads));
+    switch (s.rows) {
+      case 16: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 1>), grid, dim3(256), 0, st, c, b, d); break;
+      case 32: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 2>), grid, dim3(256), 0, st, c, b, d); break;
+      case 64: hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 2>), grid, dim3(128), 0, st, c, b, d); break;
+      default: hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 4>), grid, dim3(256), 0, st, c, b, d); break;
     }
     if (split) {
       const int64_t rows = q->tokens * q->q_heads;

@@ -21,7 +21,12 @@
 namespace fp8bq {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+
+// Memory that no kernel writes while it is read so (scalar loads).
+#define FP8BQ_CONSTANT __attribute__((address_space(4)))
 
 struct KvCache {
   uint8_t* k;      // e4m3 [pages, heads, S, D]
@@ -556,7 +561,8 @@ __device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int
       const int32_t local = (int32_t)(w - before) - (__shfl(sum, at) - __shfl(items, at));
       const int32_t rtile = local / k.splits;
       k.split = local - rtile * k.splits;
-      k.first = rtile * R;
+      // the last rows see the most keys: they go first
+      k.first = (__shfl(mine.rtiles, at) - 1 - rtile) * R;
       k.count = k.n * p.group;
       k.tile0 = tile0 + min((int64_t)k.split * chunk, (int64_t)tiles);
       k.tile1 = tile0 + min((int64_t)(k.split + 1) * chunk, (int64_t)tiles);
@@ -602,9 +608,9 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
   __shared__ float lds_m[4][R], lds_l[4][R];
   const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t col = lane & 15, grp = lane >> 4;
-  const int32_t h = blockIdx.y;
+  const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
   KvWork wk;
-  if (!kv_plan<R>(bt, p, c.log_s, blockIdx.x, wk)) return;
+  if (!kv_plan<R>(bt, p, c.log_s, w_item, wk)) return;
   const int32_t S = 1 << c.log_s;
   const int64_t cap = (int64_t)bt.max_pages << c.log_s;
 
@@ -805,7 +811,7 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
     }
     __syncthreads();
   }
-  const int64_t slot = (int64_t)h * p.slots + blockIdx.x;
+  const int64_t slot = (int64_t)h * p.slots + w_item;
   for (int32_t i = threadIdx.x; i < R * (D / 8); i += kThreads) {
     const int32_t rr = i / (D / 8), d = (i - rr * (D / 8)) * 8, r = wk.first + rr;
     if (r >= wk.count) continue;
@@ -838,9 +844,310 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
     }
     if (d == 0 && p.rows && wk.split == 0) {
       p.rows[row * ((int64_t)c.heads * p.group) + head] =
-          int2{(int)((blockIdx.x * R) + rr), wk.splits};
+          int2{w_item * R + rr, wk.splits};
     }
   }
+}
+
+// Many query rows: each of W waves holds 32 rows, and all of them share the
+// key tiles, which the workgroup stages in LDS as codes, two tiles deep: the
+// next tile's loads are in flight while the current one is computed.
+//
+// The products are the 32x32x16 ones, scores again transposed.  Key row m of a
+// 32-key product is token 16 ((m / 4) % 2) + 4 (m / 8) + m % 4, which leaves
+// lane half x with the 16 consecutive tokens 16 x .. 16 x + 15 of its query
+// row, the order in which V^T P^T takes them.  16-byte LDS chunks are
+// exchanged (XOR with the row) so that 8 neighbouring lanes, which read 8
+// rows at one column, fall on different banks.
+//
+// VALU work per score bounds this kernel (the exponential at a quarter rate,
+// and the widening of codes), so what can be is kept out of the inner loop:
+// k's scale and the softmax scale are one factor per 16 tokens inside the
+// fused multiply-add in front of the exponential; v's scale enters there too,
+// as its logarithm; sums and maxima are only rescaled when a row's maximum
+// has grown by more than 2^8.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCache c, KvBatch bt, KvQuery p) {
+  constexpr int R = 32 * W, kN = 64 * W;
+  constexpr int kC = D / 16;            // 16-byte chunks of a key row
+  constexpr int kM = D / 32;            // 32-channel tiles of the output
+  constexpr int kLoads = 4 * D / kN;    // chunks that a thread stages of k, and of v
+  constexpr int kBuf = 128 * D;         // bytes of a staged tile: k, then v
+  __shared__ __align__(16) uint8_t lds[2 * kBuf];
+  const int32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t col = lane & 31, half = lane >> 5;
+  const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
+  KvWork wk;
+  if (!kv_plan<R>(bt, p, c.log_s, w_item, wk)) return;
+  const int32_t log_s = c.log_s, S = 1 << log_s;
+  const int64_t cap = (int64_t)bt.max_pages << log_s;
+
+  const int32_t r_mine = wk.first + wave * 32 + col;
+  const bool live = r_mine < wk.count;
+  const int32_t tok_mine = live ? r_mine / p.group : 0;
+  const int64_t head = (int64_t)h * p.group + (live ? r_mine - tok_mine * p.group : 0);
+  const int64_t row = wk.row0 + tok_mine;
+  const int64_t row_hi = live ? min(wk.pos0 + tok_mine + 1, cap) : 0;
+  const int64_t row_lo = p.window > 0 ? max(wk.pos0 + tok_mine + 1 - p.window, (int64_t)0) : 0;
+  bf16x8 q[2 * kM];
+  {
+    const uint16_t* src = p.q + row * p.q_tok + head * p.q_head + 16 * half;
+    const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
+#pragma unroll
+    for (int s = 0; s < 2 * kM; ++s) {
+      u32x4 x = *(const u32x4*)(src + 32 * (s >> 1) + 8 * (s & 1));
+      x ^= u32x4{flip, flip, flip, flip};
+      if (!live) x = u32x4{0, 0, 0, 0};
+      q[s] = __builtin_bit_cast(bf16x8, x);
+    }
+  }
+  const float scale = fabsf(p.scale);
+  const int32_t tok_a = wk.first / p.group, tok_z = min(wk.first + R - 1, wk.count - 1) / p.group;
+  const int64_t see_hi = min(wk.pos0 + tok_z + 1, cap), all_hi = min(wk.pos0 + tok_a + 1, cap);
+  const int64_t see_lo = p.window > 0 ? max(wk.pos0 + tok_a + 1 - p.window, (int64_t)0) : 0;
+  const int64_t all_lo = p.window > 0 ? max(wk.pos0 + tok_z + 1 - p.window, (int64_t)0) : 0;
+  const int32_t tile0 = (int32_t)max((int64_t)wk.tile0, see_lo / kKeyTile);
+  const int32_t tile1 = (int32_t)min((int64_t)wk.tile1, (max(see_hi, (int64_t)0) + kKeyTile - 1) / kKeyTile);
+
+  f32x16 o[kM];
+#pragma unroll
+  for (int i = 0; i < kM; ++i) o[i] = f32x16{};
+  float m = -INFINITY, l = 0.0f;
+
+  // Pages of a tile's four runs of 16 tokens, the same in every lane; -1 where
+  // none of the tokens is seen or the table's entry is no page.
+  const FP8BQ_CONSTANT int32_t* table =
+      (const FP8BQ_CONSTANT int32_t*)(uintptr_t)(bt.table + (int64_t)wk.b * bt.stride);
+  struct Pages {
+    int32_t of[4];
+  };
+  auto pages = [&](int32_t tile) {
+    Pages x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t t0 = (int64_t)tile * kKeyTile + 16 * r;
+      int32_t pg = -1;
+      if (t0 < see_hi && t0 + 16 > see_lo) pg = table[t0 >> log_s];
+      pg = __builtin_amdgcn_readfirstlane(pg);
+      x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
+    }
+    return x;
+  };
+  auto pick = [](const Pages& x, int32_t r) {
+    const int32_t a = r & 1 ? x.of[1] : x.of[0], b = r & 1 ? x.of[3] : x.of[2];
+    return r & 2 ? b : a;
+  };
+  u32x4 kr[kLoads], vr[kLoads];
+  float ks[2], vs[2], ks_next[2], vs_next[2];
+  auto fetch = [&](int32_t tile, const Pages& x) {
+    const int32_t in_page = (tile * kKeyTile) & (S - 1);   // 0 unless a page is longer than a tile
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int32_t at = tid + i * kN, tok = at / kC, ch = at - tok * kC;
+      const int64_t kb = ((int64_t)max(pick(x, tok >> 4), 0) * c.heads + h) << log_s;
+      kr[i] = *(const u32x4*)(c.k + (kb + ((in_page + tok) & (S - 1))) * D + 16 * ch);
+      const int32_t dim = at >> 2, run = at & 3;
+      const int64_t vb = ((int64_t)max(pick(x, run), 0) * c.heads + h) * D + dim;
+      vr[i] = *(const u32x4*)(c.v + (vb << log_s) + ((in_page + 16 * run) & (S - 1)));
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t at = (int64_t)max(half ? x.of[2 * u + 1] : x.of[2 * u], 0) * c.heads + h;
+      ks_next[u] = c.ks[at];
+      vs_next[u] = c.vs[at];
+    }
+  };
+  auto bad = [](const Pages& x) { return (x.of[0] | x.of[1] | x.of[2] | x.of[3]) < 0; };
+  auto is_edge = [&](int32_t tile, const Pages& x) {
+    const int64_t t0 = (int64_t)tile * kKeyTile;
+    return bad(x) || t0 < all_lo || t0 + kKeyTile > all_hi;
+  };
+  // Row `row` of a staged tile whose rows are `chunks` 16-byte chunks long.
+  auto swizzle = [](int32_t row, int32_t ch, int32_t chunks) {
+    return (row * chunks + (ch ^ (chunks % 8 == 0 ? row & 7 : (row >> 1) & 3))) * 16;
+  };
+  auto put = [&](int32_t buf, int32_t tile, const Pages& x, bool edge) {
+    uint8_t* kl = lds + buf * kBuf;
+    uint8_t* vl = kl + 64 * D;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int32_t at = tid + i * kN, tok = at / kC, ch = at - tok * kC;
+      const int32_t lrow = (tok & 32) + 8 * ((tok >> 2) & 3) + 4 * ((tok >> 4) & 1) + (tok & 3);
+      *(u32x4*)(kl + swizzle(lrow, ch, kC)) = kr[i];
+      const int32_t dim = at >> 2, run = at & 3;
+      if (edge) {
+        // what nobody sees counts as code 0, whatever is there
+        const int64_t t0 = (int64_t)tile * kKeyTile + 16 * run;
+        const int32_t lo = (int32_t)min(max(see_lo - t0, (int64_t)0), (int64_t)16);
+        const int32_t hi = pick(x, run) >= 0 ? (int32_t)min(max(see_hi - t0, (int64_t)0), (int64_t)16) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) keep |= 4 * e + y >= lo && 4 * e + y < hi ? 0xFFu << (8 * y) : 0u;
+          vr[i][e] &= keep;
+        }
+      }
+      *(u32x4*)(vl + swizzle(dim, run, 4)) = vr[i];
+    }
+  };
+
+  auto compute = [&](int32_t buf, int32_t tile, const Pages& x, bool edge) {
+    const uint8_t* kl = lds + buf * kBuf;
+    const uint8_t* vl = kl + 64 * D;
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u] = f32x16{};
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        const u32x4 a = *(const u32x4*)(kl + swizzle(32 * u + col, 2 * i + half, kC));
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[0], a[1]), q[2 * i], s[u], 0, 0, 0);
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[2], a[3]), q[2 * i + 1], s[u], 0, 0, 0);
+      }
+    }
+    float f[2], lv[2], back[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
+      const float v = ok ? fmaxf(vs[u], 5.421010862427522e-20f) : 1.0f;   // at least 2^-64
+      f[u] = ok ? ks[u] * scale : 0.0f;
+      lv[u] = __builtin_amdgcn_logf(v);
+      back[u] = 1.0f / v;
+    }
+    if (edge) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t t0 = (int64_t)tile * kKeyTile + 32 * u + 16 * half;
+        const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
+        const int32_t lo = (int32_t)min(max(row_lo - t0, (int64_t)0), (int64_t)16);
+        const int32_t hi = ok ? (int32_t)min(max(row_hi - t0, (int64_t)0), (int64_t)16) : 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[u][e] = e >= lo && e < hi ? s[u][e] : -INFINITY;
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float t = s[u][0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) t = fmaxf(t, s[u][e]);
+      // -inf times a factor of 0 (a run of no page) is no maximum
+      top = fmaxf(top, t == -INFINITY ? -INFINITY : t * f[u]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__ballot(top > m + 8.0f) != 0) {
+      const float now = fmaxf(m, top);
+      const float g = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= g;
+#pragma unroll
+      for (int i = 0; i < kM; ++i) o[i] *= g;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    bf16x8 w[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float off = lv[u] - base;
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float z = __builtin_fmaf(s[u][e], f[u], off);
+        if (edge) z = s[u][e] == -INFINITY ? -INFINITY : z;
+        const float pe = __builtin_amdgcn_exp2f(z);
+        sum += pe;
+        w[u][e >> 3][e & 7] = (__bf16)pe;
+      }
+      l = __builtin_fmaf(sum, back[u], l);
+    }
+#pragma unroll
+    for (int i = 0; i < kM; ++i) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const u32x4 a = *(const u32x4*)(vl + swizzle(32 * i + col, 2 * u + half, 4));
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[0], a[1]), w[u][0], o[i], 0, 0, 0);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[2], a[3]), w[u][1], o[i], 0, 0, 0);
+      }
+    }
+  };
+
+  if (tile0 < tile1) {
+    Pages now = pages(tile0), next = pages(tile0 + 1 < tile1 ? tile0 + 1 : tile0);
+    fetch(tile0, now);
+    put(0, tile0, now, is_edge(tile0, now));
+    for (int32_t tile = tile0; tile < tile1; ++tile) {
+      const int32_t buf = (tile - tile0) & 1;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        ks[u] = ks_next[u];
+        vs[u] = vs_next[u];
+      }
+      const bool more = tile + 1 < tile1;
+      if (more) fetch(tile + 1, next);
+      const Pages after = pages(tile + 2 < tile1 ? tile + 2 : tile);
+      __syncthreads();   // the tile is staged, and the other buffer is read out
+      compute(buf, tile, now, is_edge(tile, now));
+      if (more) put(buf ^ 1, tile + 1, next, is_edge(tile + 1, next));
+      now = next;
+      next = after;
+    }
+  }
+
+  l += __shfl_xor(l, 32);
+  const int64_t slot = (int64_t)h * p.slots + w_item;
+  const int32_t rr = wave * 32 + col;
+  const int64_t all = (int64_t)c.heads * p.group;
+  if (wk.splits > 1) {
+    if (live) {
+      float* to = p.part + (slot * R + rr) * D + 4 * half;
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          *(f32x4*)(to + 32 * i + 8 * e) = f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+        }
+      }
+      if (half == 0) p.part_ml[slot * R + rr] = float2{m, l};
+    }
+  } else {
+    // Through LDS, so that a wave writes whole rows.
+    constexpr int kRow = 2 * D + 16;   // bytes, a chunk of padding
+    static_assert(8 * kRow * W <= 2 * kBuf, "a quarter of the wave's rows at a time");
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __syncthreads();
+    uint8_t* mine = lds + wave * 8 * kRow;
+#pragma unroll
+    for (int part = 0; part < 4; ++part) {
+      if ((col >> 3) == part) {
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bf16x4 y = {(__bf16)(o[i][4 * e] * inv), (__bf16)(o[i][4 * e + 1] * inv),
+                              (__bf16)(o[i][4 * e + 2] * inv), (__bf16)(o[i][4 * e + 3] * inv)};
+            *(bf16x4*)(mine + (col & 7) * kRow + 2 * (32 * i + 8 * e + 4 * half)) = y;
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8 * (D / 8) / 64; ++i) {
+        const int32_t at = lane + 64 * i, lr = at / (D / 8), ch = at - lr * (D / 8);
+        const int32_t r = wk.first + wave * 32 + part * 8 + lr;
+        if (r < wk.count) {
+          const int32_t tok = r / p.group;
+          const int64_t hd = (int64_t)h * p.group + (r - tok * p.group);
+          *(u32x4*)(p.out + (wk.row0 + tok) * p.o_tok + hd * p.o_head + 8 * ch) =
+              *(const u32x4*)(mine + lr * kRow + 16 * ch);
+        }
+      }
+      __syncthreads();
+    }
+    if (live && half == 0 && p.lse) {
+      p.lse[row * all + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    }
+  }
+  if (live && half == 0 && p.rows && wk.split == 0) p.rows[row * all + head] = int2{w_item * R + rr, wk.splits};
 }
 
 // Joins the partial sums of each query row whose keys were split: a wave per

@@ -97,8 +97,9 @@ def attention(cache, q, table, lens, starts, scale=None, window=0):
       scores: products of BF16 values are exact in fp32, sums of D terms and
         the two multiplications by scales err by (D + 4) e sum |q k| scale =: ds,
         the exponent's argument by another 2 e |s|;
-      weights: exp2 and its argument (3 + 2 |s log2 e|) e more, then u by the
-        rounding to BF16;
+      weights: exp2 and its argument (3 + 2 |s log2 e|) e more, another
+        4 |log2 v_scale| e where that scale enters as a logarithm (its own
+        rounding, the sum's and the product's), then u by the rounding to BF16;
       sums: N e each for numerator and denominator;
       output: u |out|.
     The rescaling of sums by exp2 at each new maximum adds at most 2 e per key
@@ -134,7 +135,8 @@ def attention(cache, q, table, lens, starts, scale=None, window=0):
                 z = w.sum(1, keepdim=True)
                 o, a = w @ v / z, w @ v.abs() / z
                 N = len(keys)
-                rel = 2 * (ds + (5 + 3 * (m - s).amax(1, keepdim=True)) * e + 2 * N * e)
+                lv = float(np.abs(np.log2(vs[pg, h].astype(np.float64))).max())
+                rel = 2 * (ds + (5 + 3 * (m - s).amax(1, keepdim=True) + 4 * lv) * e + 2 * N * e)
                 out[row, h * group:(h + 1) * group] = o
                 tol[row, h * group:(h + 1) * group] = u * o.abs() + (u * (1 + u) + rel) * a + 1e-30
                 lse[row, h * group:(h + 1) * group] = (m + z.log())[:, 0]
