@@ -102,8 +102,17 @@ KvShape kv_shape(int32_t kv_heads, int32_t dim, int32_t q_heads, int32_t count, 
   const int64_t per_seq = ceil_div(tokens * s.group, count);
   s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 ? 64 : 128));
   const int64_t base = tokens * s.group / s.rows + count;
-  s.target = base * kv_heads >= 4096 ? 0 : static_cast<int32_t>(ceil_div(1024, kv_heads));
-  s.min_tiles = 4;
+#ifndef KV_T
+#define KV_T 1024
+#endif
+#ifndef KV_B
+#define KV_B 4096
+#endif
+#ifndef KV_MIN
+#define KV_MIN 4
+#endif
+  s.target = base * kv_heads >= KV_B ? 0 : static_cast<int32_t>(ceil_div(KV_T, kv_heads));
+  s.min_tiles = KV_MIN;
   s.slots = static_cast<int32_t>(base + s.target);
   const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(kv_heads) * static_cast<size_t>(s.rows);
   s.ml_at = n * static_cast<size_t>(dim) * 4;
@@ -242,8 +251,13 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
     }
     if (split) {
       const int64_t rows = q->tokens * q->q_heads;
-      hipLaunchKernelGGL(fp8bq::kv_attend_join<D>, dim3(static_cast<unsigned>(ceil_div(rows, 4))),
-                         dim3(fp8bq::kThreads), 0, st, b, d, c.heads, s.rows);
+      if (rows <= 1024) {
+        hipLaunchKernelGGL((fp8bq::kv_attend_join<D, 8>), dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, b, d,
+                           c.heads, s.rows);
+      } else {
+        hipLaunchKernelGGL((fp8bq::kv_attend_join<D, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0,
+                           st, b, d, c.heads, s.rows);
+      }
     }
   });
   const hipError_t e = hipGetLastError();

@@ -473,21 +473,52 @@ struct KvQuery {
 };
 
 constexpr int kKeyTile = 64;
+#ifndef KV_NT
+#define KV_NT 1
+#endif
+#if KV_NT
+#define KVLOAD(p) __builtin_nontemporal_load(p)
+#else
+#define KVLOAD(p) (*(p))
+#endif
 
 // The work of one workgroup: a tile of query rows of a sequence and a range
 // of its key tiles.
 struct KvWork {
   int32_t b, n, row0;       // sequence, its query tokens, their first row
   int32_t first, count;     // first query row (token * group + head in group) of the tile; rows of the sequence
-  int64_t pos0;             // position of the sequence's first query token
+  int32_t pos0;             // position of the sequence's first query token
   int32_t tile0, tile1;     // key tiles
   int32_t splits, split;
 };
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+// Sum over lanes 0 .. i, for every lane i (data-parallel moves, no LDS).
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+  auto from = [](T x, auto ctrl, auto rows) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                                             decltype(rows)::value, 0xF, false));
+  };
+  using std::integral_constant;
+  v += from(v, integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // row_shr:1
+  v += from(v, integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  v += from(v, integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  v += from(v, integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  v += from(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // last lane of the row before
+  v += from(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // last lane of the first half
   return v;
+}
+
+__device__ __forceinline__ int32_t lane_of(int32_t v, int32_t lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Positions stay below 2^31 - 1024, so that a tile's end is in 32 bits.
+__device__ __forceinline__ int32_t kv_capacity(const KvBatch& bt, int32_t log_s) {
+  return (int32_t)min((int64_t)bt.max_pages << log_s, (int64_t)INT32_MAX - 1023);
+}
+
+// The first position that a query at pos - 1 sees.
+__device__ __forceinline__ int32_t kv_low(int32_t end, int32_t window) {
+  return window > 0 ? max(max(end, 0) - window, 0) : 0;
 }
 
 // Which work item w is.  Every wave reads the batch's lengths and lays the
@@ -500,15 +531,14 @@ template <int R>
 __device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int32_t log_s, int32_t w,
                                         KvWork& k) {
   const int32_t lane = threadIdx.x & 63;
-  const int64_t cap = (int64_t)bt.max_pages << log_s;
+  const int32_t cap = kv_capacity(bt, log_s);
   struct Seq {
-    int32_t row0, n, rtiles, tile0, tiles;
-    int64_t pos0;
+    int32_t row0, n, len, rtiles, tile0, tiles;
   };
   auto seq = [&](int32_t b) {
     Seq s{0, 0, 0, 0, 0, 0};
     if (b >= bt.count) return s;
-    const int64_t len = bt.lens[b];
+    s.len = max(bt.lens[b], 0);
     if (bt.starts) {
       s.row0 = kv_clamp(bt.starts[b], p.tokens);
       s.n = max(kv_clamp(bt.starts[b + 1], p.tokens) - s.row0, 0);
@@ -516,61 +546,89 @@ __device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int
       s.row0 = b;
       s.n = 1;
     }
-    s.pos0 = len - s.n;
-    s.rtiles = (int32_t)(((int64_t)s.n * p.group + R - 1) / R);
-    const int64_t hi = min(len, cap);
-    const int64_t lo = p.window > 0 ? max(s.pos0 + 1 - p.window, (int64_t)0) : 0;
+    s.rtiles = (int32_t)(((uint32_t)s.n * (uint32_t)p.group + R - 1) / R);   // at most 2^25 rows
+    const int32_t hi = min(s.len, cap), lo = kv_low(s.len - s.n + 1, p.window);
     if (s.n > 0 && hi > lo) {
-      s.tile0 = (int32_t)(lo / kKeyTile);
-      s.tiles = (int32_t)((hi + kKeyTile - 1) / kKeyTile) - s.tile0;
+      s.tile0 = lo / kKeyTile;
+      s.tiles = (hi + kKeyTile - 1) / kKeyTile - s.tile0;
     }
     return s;
   };
   Seq mine = seq(lane);
   int32_t chunk = INT32_MAX;
   if (p.target > 0) {
-    int64_t total = (int64_t)mine.rtiles * mine.tiles;
+    // fp32 is enough, with room for its rounding: the chunk may only be too
+    // long, never so short that there are more items than slots
+    float total = (float)mine.rtiles * (float)mine.tiles;
     for (int32_t b = 64; b < bt.count; b += 64) {
       const Seq s = seq(b + lane);
-      total += (int64_t)s.rtiles * s.tiles;
+      total += (float)s.rtiles * (float)s.tiles;
     }
-    total = wave_sum(total);
-    const int64_t per = (total + p.target - 1) / p.target;
-    chunk = (int32_t)min(max(per, (int64_t)p.min_tiles), (int64_t)INT32_MAX);
+    total = __int_as_float(lane_of(__float_as_int(wave_scan(total)), 63));
+    const float per = __builtin_ceilf(total * 1.0001f / (float)p.target);
+    chunk = max((int32_t)fminf(per, 1e9f), p.min_tiles);
   }
   int64_t before = 0;
   for (int32_t b0 = 0; b0 < bt.count; b0 += 64) {
     if (b0 > 0) mine = seq(b0 + lane);
     const int32_t splits = max(1, (int32_t)(((int64_t)mine.tiles + chunk - 1) / chunk));
     const int32_t items = (int32_t)min((int64_t)mine.rtiles * splits, (int64_t)1 << 24);
-    int32_t sum = items;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int32_t o = __shfl_up(sum, d);
-      if (lane >= d) sum += o;
-    }
+    const int32_t sum = wave_scan(items);
     const uint64_t past = __ballot(before + sum > w);
     if (past != 0) {
       const int32_t at = __ffsll((unsigned long long)past) - 1;
       k.b = b0 + at;
-      k.row0 = __shfl(mine.row0, at);
-      k.n = __shfl(mine.n, at);
-      k.pos0 = __shfl(mine.pos0, at);
-      k.splits = __shfl(splits, at);
-      const int32_t tile0 = __shfl(mine.tile0, at), tiles = __shfl(mine.tiles, at);
-      const int32_t local = (int32_t)(w - before) - (__shfl(sum, at) - __shfl(items, at));
+      k.row0 = lane_of(mine.row0, at);
+      k.n = lane_of(mine.n, at);
+      k.pos0 = lane_of(mine.len, at) - k.n;
+      k.splits = lane_of(splits, at);
+      const int32_t tile0 = lane_of(mine.tile0, at), tiles = lane_of(mine.tiles, at);
+      const int32_t local = (int32_t)(w - before) - (lane_of(sum, at) - lane_of(items, at));
       const int32_t rtile = local / k.splits;
       k.split = local - rtile * k.splits;
       // the last rows see the most keys: they go first
-      k.first = (__shfl(mine.rtiles, at) - 1 - rtile) * R;
+      k.first = (lane_of(mine.rtiles, at) - 1 - rtile) * R;
       k.count = k.n * p.group;
       k.tile0 = tile0 + min((int64_t)k.split * chunk, (int64_t)tiles);
       k.tile1 = tile0 + min((int64_t)(k.split + 1) * chunk, (int64_t)tiles);
       return true;
     }
-    before += __shfl(sum, 63);
+    before += lane_of(sum, 63);
   }
   return false;
+}
+
+// What the query rows of a work item see: some of them keys see_lo ..
+// see_hi - 1, all of them all_lo .. all_hi - 1; and the tiles to visit.
+struct KvSeen {
+  int32_t see_lo, see_hi, all_lo, all_hi, tile0, tile1;
+};
+
+template <int R>
+__device__ __forceinline__ KvSeen kv_seen(const KvWork& k, const KvQuery& p, int32_t cap) {
+  const int32_t first = k.pos0 + k.first / p.group + 1;
+  const int32_t last = k.pos0 + min(k.first + R - 1, k.count - 1) / p.group + 1;
+  KvSeen s;
+  s.see_hi = min(last, cap);
+  s.all_hi = min(first, cap);
+  s.see_lo = kv_low(first, p.window);
+  s.all_lo = kv_low(last, p.window);
+  s.tile0 = max(k.tile0, s.see_lo / kKeyTile);
+  s.tile1 = min(k.tile1, (max(s.see_hi, 0) + kKeyTile - 1) / kKeyTile);
+  return s;
+}
+
+// The bytes lo .. hi - 1 of 16, as a mask.
+__device__ __forceinline__ u32x4 kv_bytes(int32_t lo, int32_t hi) {
+  u32x4 keep;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) w |= 4 * e + y >= lo && 4 * e + y < hi ? 0xFFu << (8 * y) : 0u;
+    keep[e] = w;
+  }
+  return keep;
 }
 
 // Eight codes (two dwords) as BF16, exactly.
@@ -580,6 +638,21 @@ __device__ __forceinline__ bf16x8 kv_widen(uint32_t a, uint32_t b) {
   const bf16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
   const bf16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
   return bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
+}
+
+#ifdef KV_NOSB
+#define SB
+#else
+#define SB __builtin_amdgcn_sched_barrier(0)
+#endif
+#ifndef KV_LB
+#define KV_LB (NT == 1 ? 2 : 1)
+#endif
+// The largest part of D channels, in equal parts of whole 16s, within `most`.
+constexpr int kv_part(int d, int most) {
+  int parts = 1;
+  while (d / parts > most || d % (16 * parts) != 0) ++parts;
+  return d / parts;
 }
 
 // Few query rows: R = 16 NT rows of a sequence (tokens times the query heads
@@ -598,51 +671,50 @@ __device__ __forceinline__ bf16x8 kv_widen(uint32_t a, uint32_t b) {
 // fp32 sums); scales enter in fp32, k's with the score, v's with the weight,
 // which is then rounded to BF16 once (relative 2^-9, its sum is not).
 template <int D, int NT>
-__global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_attend_rows(KvCache c, KvBatch bt,
+__global__ __launch_bounds__(kThreads, KV_LB) void kv_attend_rows(KvCache c, KvBatch bt,
                                                                                          KvQuery p) {
   constexpr int R = 16 * NT;
   constexpr int kI = D / 64;    // 64-channel pieces
   constexpr int kDt = D / 16;   // 16-channel tiles of the output
-  constexpr int kPitch = D + 4;
-  __shared__ float lds_o[R * kPitch];
+#ifndef KV_AHEAD
+#define KV_AHEAD (D <= 128)
+#endif
+  constexpr bool kAhead = KV_AHEAD;
+  constexpr int kPart = kv_part(D, 2048 / R);   // channels that are joined at a time: 8 per thread at most
+  __shared__ __align__(16) float lds_o[4][R][kPart + 4];
   __shared__ float lds_m[4][R], lds_l[4][R];
   const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t col = lane & 15, grp = lane >> 4;
   const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
   KvWork wk;
   if (!kv_plan<R>(bt, p, c.log_s, w_item, wk)) return;
-  const int32_t S = 1 << c.log_s;
-  const int64_t cap = (int64_t)bt.max_pages << c.log_s;
+  const int32_t S = 1 << c.log_s, cap = kv_capacity(bt, c.log_s);
+  const KvSeen see = kv_seen<R>(wk, p, cap);
 
-  // This lane's query rows, and what the whole tile sees.
-  int64_t row_hi[NT], row_lo[NT];
+  int32_t row_hi[NT], row_lo[NT];
   bf16x8 q[NT][kI][2];
+  const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int32_t r = wk.first + nt * 16 + col;
     const bool live = r < wk.count;
     const int32_t tok = live ? r / p.group : 0;
     const int32_t g = live ? r - tok * p.group : 0;
-    const int64_t pos = wk.pos0 + tok;
-    row_hi[nt] = live ? min(pos + 1, cap) : 0;
-    row_lo[nt] = p.window > 0 ? max(pos + 1 - p.window, (int64_t)0) : 0;
-    const uint16_t* src = p.q + (wk.row0 + tok) * p.q_tok + ((int64_t)h * p.group + g) * p.q_head;
+    row_hi[nt] = live ? min(wk.pos0 + tok + 1, cap) : 0;
+    row_lo[nt] = kv_low(wk.pos0 + tok + 1, p.window);
+    const uint16_t* src = p.q + (wk.row0 + tok) * p.q_tok + ((int64_t)h * p.group + g) * p.q_head + 16 * grp;
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        q[nt][i][x] = *(const bf16x8*)(src + 64 * i + 16 * grp + 8 * x);
-        if (!live) q[nt][i][x] = bf16x8{};
+      for (int y = 0; y < 2; ++y) {
+        u32x4 x = *(const u32x4*)(src + 64 * i + 8 * y);
+        x ^= u32x4{flip, flip, flip, flip};
+        if (!live) x = u32x4{0, 0, 0, 0};
+        q[nt][i][y] = __builtin_bit_cast(bf16x8, x);
       }
     }
   }
-  const int32_t tok_a = wk.first / p.group, tok_z = min(wk.first + R - 1, wk.count - 1) / p.group;
-  const int64_t see_hi = min(wk.pos0 + tok_z + 1, cap), all_hi = min(wk.pos0 + tok_a + 1, cap);
-  const int64_t see_lo = p.window > 0 ? max(wk.pos0 + tok_a + 1 - p.window, (int64_t)0) : 0;
-  const int64_t all_lo = p.window > 0 ? max(wk.pos0 + tok_z + 1 - p.window, (int64_t)0) : 0;
-  int32_t tile0 = wk.tile0, tile1 = wk.tile1;
-  tile0 = (int32_t)max((int64_t)tile0, see_lo / kKeyTile);
-  tile1 = (int32_t)min((int64_t)tile1, (max(see_hi, (int64_t)0) + kKeyTile - 1) / kKeyTile);
+  const float scale = fabsf(p.scale);
 
   f32x4 o[NT][kDt];
   float m[NT], l[NT];
@@ -657,37 +729,45 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
   const int32_t* table = bt.table + (int64_t)wk.b * bt.stride;
   // Page of the 16 tokens from t0 on, -1 where none of them is seen or the
   // table's entry is no page.
-  auto page_of = [&](int64_t t0) {
+  auto page_of = [&](int32_t t0) {
     int32_t pg = -1;
-    if (t0 < see_hi && t0 + 16 > see_lo) pg = table[t0 >> c.log_s];
+    if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> c.log_s];
     return pg >= 0 && pg < c.pages ? pg : -1;
   };
   const int32_t k_run = col >> 2;
-  struct Tile {
-    u32x4 k[4][kI], v[kDt];
-    float ks, vs;
-    int32_t pv;
-    bool bad;
-  };
-  auto load = [&](int32_t tile, int32_t pk, int32_t pv, Tile& x) {
-    const int64_t tk = (int64_t)tile * kKeyTile + 16 * k_run, tv = (int64_t)tile * kKeyTile + 16 * grp;
+  const bool half_rows = S > kKeyTile;
+  // One tile's codes: the next tile's keys are loaded into the same registers
+  // as soon as the scores are done, its values after the weighted sum, so
+  // that half a tile at least is always in flight.
+  u32x4 xk[4][kI], xv[kDt];
+  float ks_next, vs_next;
+  auto load_k = [&](int32_t tile, int32_t pk, int32_t pv) {
+    const int32_t tk = tile * kKeyTile + 16 * k_run;
     const int64_t kblock = (int64_t)max(pk, 0) * c.heads + h, vblock = (int64_t)max(pv, 0) * c.heads + h;
     const uint8_t* kp = c.k + kblock * S * D + ((tk & (S - 1)) + (col & 3)) * D + 16 * grp;
-    const uint8_t* vp = c.v + vblock * S * D + (int64_t)col * S + (tv & (S - 1));
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
-      for (int i = 0; i < kI; ++i) x.k[t][i] = *(const u32x4*)(kp + t * 4 * D + 64 * i);
+      for (int i = 0; i < kI; ++i) xk[t][i] = KVLOAD((const u32x4*)(kp + t * 4 * D + 64 * i));
     }
-#pragma unroll
-    for (int i = 0; i < kDt; ++i) x.v[i] = *(const u32x4*)(vp + i * 16 * S);
-    x.ks = c.ks[vblock];
-    x.vs = c.vs[vblock];
-    x.pv = pv;
-    x.bad = __ballot(pv < 0) != 0;
+    ks_next = c.ks[vblock];
+    vs_next = c.vs[vblock];
   };
-  auto compute = [&](int32_t tile, Tile& x) {
-    const int64_t t0 = (int64_t)tile * kKeyTile;
+  auto load_v = [&](int32_t tile, int32_t pv) {
+    const int32_t tv = tile * kKeyTile + 16 * grp;
+    const int64_t vblock = (int64_t)max(pv, 0) * c.heads + h;
+    const uint8_t* vp = c.v + vblock * S * D + (int64_t)col * S + (tv & (S - 1));
+#pragma unroll
+    for (int i = 0; i < kDt; ++i) {
+      const u32x4* at = (const u32x4*)(vp + i * 16 * S);
+      xv[i] = half_rows ? *at : KVLOAD(at);
+    }
+  };
+  // Tile `tile`, whose values lie in pages pv, and the next one's loads.
+  auto compute = [&](int32_t tile, int32_t pv, bool more, int32_t pk_next, int32_t pv_next) {
+    const bool ok = pv >= 0;
+    const float f = ok ? ks_next * scale : 0.0f, vs = ok ? vs_next : 0.0f;
+    const int32_t t0 = tile * kKeyTile;
     f32x4 s[NT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -695,69 +775,61 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
       for (int nt = 0; nt < NT; ++nt) s[nt][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        const bf16x8 a = kv_widen(x.k[t][i][0], x.k[t][i][1]), b = kv_widen(x.k[t][i][2], x.k[t][i][3]);
+        const bf16x8 a = kv_widen(xk[t][i][0], xk[t][i][1]), b = kv_widen(xk[t][i][2], xk[t][i][3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[nt][i][0], s[nt][t], 0, 0, 0);
           s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, q[nt][i][1], s[nt][t], 0, 0, 0);
         }
       }
+      SB;
     }
-    const bool edge = x.bad || t0 < all_lo || t0 + kKeyTile > all_hi;
-    const int64_t run = t0 + 16 * grp;
-    float vs = x.vs;
-    const float ks = x.ks * p.scale;
+    if constexpr (kAhead) {
+      if (more) load_k(tile + 4, pk_next, pv_next);
+    } else {
+      __builtin_amdgcn_sched_barrier(0);   // not before the keys' registers are free
+      load_v(tile, pv);
+    }
+    const bool edge = __ballot(!ok) != 0 || t0 < see.all_lo || t0 + kKeyTile > see.all_hi;
     if (edge) {
       // What nobody sees counts as code 0 with weight 0, whatever is there.
-      const bool ok = x.pv >= 0;
-      if (!ok) vs = 0.0f;
-      const int32_t lo = (int32_t)min(max(see_lo - run, (int64_t)0), (int64_t)16);
-      const int32_t hi = ok ? (int32_t)min(max(see_hi - run, (int64_t)0), (int64_t)16) : 0;
-      u32x4 keep;
+      const int32_t run = t0 + 16 * grp;
+      const u32x4 keep = kv_bytes(see.see_lo - run, ok ? see.see_hi - run : 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t w = 0;
+      for (int i = 0; i < kDt; ++i) xv[i] &= keep;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          if (4 * e + y >= lo && 4 * e + y < hi) w |= 0xFFu << (8 * y);
-        }
-        keep[e] = w;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int32_t lo = row_lo[nt] - run, hi = ok ? row_hi[nt] - run : 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[nt][e >> 2][e & 3] = e >= lo && e < hi ? s[nt][e >> 2][e & 3] : -INFINITY;
       }
-#pragma unroll
-      for (int i = 0; i < kDt; ++i) x.v[i] &= keep;
     }
     bf16x8 w[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float top = -INFINITY;
-      float z[16];
+      float top = s[nt][0][0];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) z[4 * t + r] = s[nt][t][r] * ks;
-      }
-      if (edge) {
-        const int64_t lo = row_lo[nt] - run, hi = x.pv >= 0 ? row_hi[nt] - run : 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) z[e] = (e >= lo && e < hi) ? z[e] : -INFINITY;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, z[e]);
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[nt][e >> 2][e & 3]);
+      // -inf times a factor of 0 (a run of no page) is no maximum
+      top = top == -INFINITY ? -INFINITY : top * f;
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      if (__ballot(top > m[nt]) != 0) {
+      if (__ballot(top > m[nt] + 8.0f) != 0) {
         const float now = fmaxf(m[nt], top);
-        const float f = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
+        const float x = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
         m[nt] = now;
-        l[nt] *= f;
+        l[nt] *= x;
 #pragma unroll
-        for (int i = 0; i < kDt; ++i) o[nt][i] *= f;
+        for (int i = 0; i < kDt; ++i) o[nt][i] *= x;
       }
-      const float base = m[nt] == -INFINITY ? 0.0f : m[nt];
+      const float base = m[nt] == -INFINITY ? 0.0f : -m[nt];
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float pe = __builtin_amdgcn_exp2f(z[e] - base);
+        const float x = s[nt][e >> 2][e & 3];
+        float z = __builtin_fmaf(x, f, base);
+        if (edge) z = x == -INFINITY ? -INFINITY : z;
+        const float pe = __builtin_amdgcn_exp2f(z);
         sum += pe;
         w[nt][e >> 3][e & 7] = (__bf16)(pe * vs);
       }
@@ -765,19 +837,38 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
     }
 #pragma unroll
     for (int i = 0; i < kDt; ++i) {
-      const bf16x8 a = kv_widen(x.v[i][0], x.v[i][1]), b = kv_widen(x.v[i][2], x.v[i][3]);
+      const bf16x8 a = kv_widen(xv[i][0], xv[i][1]), b = kv_widen(xv[i][2], xv[i][3]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w[nt][0], o[nt][i], 0, 0, 0);
         o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, w[nt][1], o[nt][i], 0, 0, 0);
       }
+      if (i % 2 == 1) SB;
     }
   };
-  for (int32_t tile = tile0 + wave; tile < tile1; tile += 4) {
-    const int64_t t0 = (int64_t)tile * kKeyTile;
-    Tile x;
-    load(tile, page_of(t0 + 16 * k_run), page_of(t0 + 16 * grp), x);
-    compute(tile, x);
+  int32_t tile = see.tile0 + wave;
+  if (tile < see.tile1) {
+    auto page_at = [&](int32_t tl, int32_t run) { return page_of(min(tl, see.tile1 - 1) * kKeyTile + 16 * run); };
+    int32_t pv = page_at(tile, grp);
+    int32_t pk_next = page_at(tile, k_run), pv_next = pv;
+    load_k(tile, pk_next, pv);
+    if constexpr (kAhead) load_v(tile, pv);
+    pk_next = page_at(tile + 4, k_run);
+    pv_next = page_at(tile + 4, grp);
+    for (; tile < see.tile1; tile += 4) {
+      const bool more = tile + 4 < see.tile1;
+      const int32_t pk_after = page_at(tile + 8, k_run), pv_after = page_at(tile + 8, grp);
+      compute(tile, pv, more, pk_next, pv_next);
+      if constexpr (kAhead) {
+        if (more) load_v(tile + 4, pv_next);
+      } else {
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) load_k(tile + 4, pk_next, pv_next);
+      }
+      pv = pv_next;
+      pk_next = pk_after;
+      pv_next = pv_after;
+    }
   }
 
   // Join the four waves: common maximum, then their sums one after another.
@@ -798,38 +889,43 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
     for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][nt * 16 + col]);
     f[nt] = m[nt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[nt] - top);
   }
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < kDt; ++i) {
-          f32x4* at = (f32x4*)&lds_o[(nt * 16 + col) * kPitch + i * 16 + 4 * grp];
-          *at = w == 0 ? o[nt][i] * f[nt] : *at + o[nt][i] * f[nt];
-        }
-      }
-    }
-    __syncthreads();
-  }
+  // Of each thread: 8 channels of one row, in every part.
+  const int32_t rr = threadIdx.x / (kPart / 8), ch = (threadIdx.x % (kPart / 8)) * 8, r = wk.first + rr;
+  const bool mine = rr < R && r < wk.count;
+  const int32_t tok = mine ? r / p.group : 0, g = mine ? r - tok * p.group : 0;
+  const int64_t head = (int64_t)h * p.group + g, row = wk.row0 + tok, all = (int64_t)c.heads * p.group;
   const int64_t slot = (int64_t)h * p.slots + w_item;
-  for (int32_t i = threadIdx.x; i < R * (D / 8); i += kThreads) {
-    const int32_t rr = i / (D / 8), d = (i - rr * (D / 8)) * 8, r = wk.first + rr;
-    if (r >= wk.count) continue;
-    const int32_t tok = r / p.group, g = r - tok * p.group;
-    float top = -INFINITY, sum = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
+  if (mine) {
     for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][rr]);
     for (int w = 0; w < 4; ++w) {
       if (lds_m[w][rr] != -INFINITY) sum += lds_l[w][rr] * __builtin_amdgcn_exp2f(lds_m[w][rr] - top);
     }
-    const f32x4 a = *(const f32x4*)&lds_o[rr * kPitch + d], z = *(const f32x4*)&lds_o[rr * kPitch + d + 4];
-    const int64_t head = (int64_t)h * p.group + g, row = wk.row0 + tok;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int part = 0; part < D / kPart; ++part) {
+    if (part > 0) __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kPart / 16; ++i) {
+        *(f32x4*)&lds_o[wave][nt * 16 + col][i * 16 + 4 * grp] = o[nt][part * (kPart / 16) + i] * f[nt];
+      }
+    }
+    __syncthreads();
+    if (!mine) continue;
+    f32x4 a = *(const f32x4*)&lds_o[0][rr][ch], z = *(const f32x4*)&lds_o[0][rr][ch + 4];
+    for (int w = 1; w < 4; ++w) {
+      a += *(const f32x4*)&lds_o[w][rr][ch];
+      z += *(const f32x4*)&lds_o[w][rr][ch + 4];
+    }
+    const int32_t d = part * kPart + ch;
     if (wk.splits > 1) {
       f32x4* to = (f32x4*)(p.part + (slot * R + rr) * D + d);
       to[0] = a;
       to[1] = z;
-      if (d == 0) p.part_ml[slot * R + rr] = float2{top, sum};
     } else {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       bf16x8 y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -837,16 +933,15 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1) ? 2 : 1) void kv_at
         y[4 + e] = (__bf16)(z[e] * inv);
       }
       *(bf16x8*)(p.out + row * p.o_tok + head * p.o_head + d) = y;
-      if (d == 0 && p.lse) {
-        p.lse[row * ((int64_t)c.heads * p.group) + head] =
-            sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-      }
-    }
-    if (d == 0 && p.rows && wk.split == 0) {
-      p.rows[row * ((int64_t)c.heads * p.group) + head] =
-          int2{w_item * R + rr, wk.splits};
     }
   }
+  if (!mine || ch != 0) return;
+  if (wk.splits > 1) {
+    p.part_ml[slot * R + rr] = float2{top, sum};
+  } else if (p.lse) {
+    p.lse[row * all + head] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+  }
+  if (p.rows && wk.split == 0) p.rows[row * all + head] = int2{w_item * R + rr, wk.splits};
 }
 
 // Many query rows: each of W waves holds 32 rows, and all of them share the
@@ -879,16 +974,16 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
   KvWork wk;
   if (!kv_plan<R>(bt, p, c.log_s, w_item, wk)) return;
-  const int32_t log_s = c.log_s, S = 1 << log_s;
-  const int64_t cap = (int64_t)bt.max_pages << log_s;
+  const int32_t log_s = c.log_s, S = 1 << log_s, cap = kv_capacity(bt, log_s);
+  const KvSeen see = kv_seen<R>(wk, p, cap);
 
   const int32_t r_mine = wk.first + wave * 32 + col;
   const bool live = r_mine < wk.count;
   const int32_t tok_mine = live ? r_mine / p.group : 0;
   const int64_t head = (int64_t)h * p.group + (live ? r_mine - tok_mine * p.group : 0);
   const int64_t row = wk.row0 + tok_mine;
-  const int64_t row_hi = live ? min(wk.pos0 + tok_mine + 1, cap) : 0;
-  const int64_t row_lo = p.window > 0 ? max(wk.pos0 + tok_mine + 1 - p.window, (int64_t)0) : 0;
+  const int32_t row_hi = live ? min(wk.pos0 + tok_mine + 1, cap) : 0;
+  const int32_t row_lo = kv_low(wk.pos0 + tok_mine + 1, p.window);
   bf16x8 q[2 * kM];
   {
     const uint16_t* src = p.q + row * p.q_tok + head * p.q_head + 16 * half;
@@ -902,13 +997,6 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     }
   }
   const float scale = fabsf(p.scale);
-  const int32_t tok_a = wk.first / p.group, tok_z = min(wk.first + R - 1, wk.count - 1) / p.group;
-  const int64_t see_hi = min(wk.pos0 + tok_z + 1, cap), all_hi = min(wk.pos0 + tok_a + 1, cap);
-  const int64_t see_lo = p.window > 0 ? max(wk.pos0 + tok_a + 1 - p.window, (int64_t)0) : 0;
-  const int64_t all_lo = p.window > 0 ? max(wk.pos0 + tok_z + 1 - p.window, (int64_t)0) : 0;
-  const int32_t tile0 = (int32_t)max((int64_t)wk.tile0, see_lo / kKeyTile);
-  const int32_t tile1 = (int32_t)min((int64_t)wk.tile1, (max(see_hi, (int64_t)0) + kKeyTile - 1) / kKeyTile);
-
   f32x16 o[kM];
 #pragma unroll
   for (int i = 0; i < kM; ++i) o[i] = f32x16{};
@@ -925,9 +1013,9 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     Pages x;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int64_t t0 = (int64_t)tile * kKeyTile + 16 * r;
+      const int32_t t0 = tile * kKeyTile + 16 * r;
       int32_t pg = -1;
-      if (t0 < see_hi && t0 + 16 > see_lo) pg = table[t0 >> log_s];
+      if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> log_s];
       pg = __builtin_amdgcn_readfirstlane(pg);
       x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
     }
@@ -959,8 +1047,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   };
   auto bad = [](const Pages& x) { return (x.of[0] | x.of[1] | x.of[2] | x.of[3]) < 0; };
   auto is_edge = [&](int32_t tile, const Pages& x) {
-    const int64_t t0 = (int64_t)tile * kKeyTile;
-    return bad(x) || t0 < all_lo || t0 + kKeyTile > all_hi;
+    const int32_t t0 = tile * kKeyTile;
+    return bad(x) || t0 < see.all_lo || t0 + kKeyTile > see.all_hi;
   };
   // Row `row` of a staged tile whose rows are `chunks` 16-byte chunks long.
   auto swizzle = [](int32_t row, int32_t ch, int32_t chunks) {
@@ -977,16 +1065,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       const int32_t dim = at >> 2, run = at & 3;
       if (edge) {
         // what nobody sees counts as code 0, whatever is there
-        const int64_t t0 = (int64_t)tile * kKeyTile + 16 * run;
-        const int32_t lo = (int32_t)min(max(see_lo - t0, (int64_t)0), (int64_t)16);
-        const int32_t hi = pick(x, run) >= 0 ? (int32_t)min(max(see_hi - t0, (int64_t)0), (int64_t)16) : 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t keep = 0;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) keep |= 4 * e + y >= lo && 4 * e + y < hi ? 0xFFu << (8 * y) : 0u;
-          vr[i][e] &= keep;
-        }
+        const int32_t t0 = tile * kKeyTile + 16 * run;
+        vr[i] &= kv_bytes(see.see_lo - t0, pick(x, run) >= 0 ? see.see_hi - t0 : 0);
       }
       *(u32x4*)(vl + swizzle(dim, run, 4)) = vr[i];
     }
@@ -1018,10 +1098,9 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     if (edge) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int64_t t0 = (int64_t)tile * kKeyTile + 32 * u + 16 * half;
+        const int32_t t0 = tile * kKeyTile + 32 * u + 16 * half;
         const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
-        const int32_t lo = (int32_t)min(max(row_lo - t0, (int64_t)0), (int64_t)16);
-        const int32_t hi = ok ? (int32_t)min(max(row_hi - t0, (int64_t)0), (int64_t)16) : 0;
+        const int32_t lo = row_lo - t0, hi = ok ? row_hi - t0 : 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[u][e] = e >= lo && e < hi ? s[u][e] : -INFINITY;
       }
@@ -1071,20 +1150,20 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     }
   };
 
-  if (tile0 < tile1) {
-    Pages now = pages(tile0), next = pages(tile0 + 1 < tile1 ? tile0 + 1 : tile0);
-    fetch(tile0, now);
-    put(0, tile0, now, is_edge(tile0, now));
-    for (int32_t tile = tile0; tile < tile1; ++tile) {
-      const int32_t buf = (tile - tile0) & 1;
+  if (see.tile0 < see.tile1) {
+    Pages now = pages(see.tile0), next = pages(see.tile0 + 1 < see.tile1 ? see.tile0 + 1 : see.tile0);
+    fetch(see.tile0, now);
+    put(0, see.tile0, now, is_edge(see.tile0, now));
+    for (int32_t tile = see.tile0; tile < see.tile1; ++tile) {
+      const int32_t buf = (tile - see.tile0) & 1;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         ks[u] = ks_next[u];
         vs[u] = vs_next[u];
       }
-      const bool more = tile + 1 < tile1;
+      const bool more = tile + 1 < see.tile1;
       if (more) fetch(tile + 1, next);
-      const Pages after = pages(tile + 2 < tile1 ? tile + 2 : tile);
+      const Pages after = pages(tile + 2 < see.tile1 ? tile + 2 : tile);
       __syncthreads();   // the tile is staged, and the other buffer is read out
       compute(buf, tile, now, is_edge(tile, now));
       if (more) put(buf ^ 1, tile + 1, next, is_edge(tile + 1, next));
@@ -1150,14 +1229,19 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   if (live && half == 0 && p.rows && wk.split == 0) p.rows[row * all + head] = int2{w_item * R + rr, wk.splits};
 }
 
-// Joins the partial sums of each query row whose keys were split: a wave per
-// row, which finds them through `rows` (first slot times R plus row in tile,
-// and how many slots, one after another).
-template <int D>
-__global__ __launch_bounds__(kThreads) void kv_attend_join(KvBatch bt, KvQuery p, int32_t heads, int32_t R) {
+// Joins the partial sums of each query row whose keys were split, found
+// through `rows` (first slot times R plus row in tile, and how many slots, one
+// after another).  N waves share a row, each taking every Nth partial, all in
+// flight at once: with few rows of many splits, as one long sequence has, one
+// wave per row would add up its partials one round trip after another.
+template <int D, int N>
+__global__ __launch_bounds__(N == 1 ? 256 : 64 * N) void kv_attend_join(KvBatch bt, KvQuery p, int32_t heads,
+                                                                        int32_t R) {
   constexpr int kV = D / 64;
-  const int32_t lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ float acc_of[N][D], sum_of[N], top_of[N];
+  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t item = N == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  const int32_t part = N == 1 ? 0 : wave;
   const int32_t all = heads * p.group;
   if (item >= (int64_t)p.tokens * all) return;
   const int64_t row = item / all;
@@ -1169,20 +1253,53 @@ __global__ __launch_bounds__(kThreads) void kv_attend_join(KvBatch bt, KvQuery p
   if (at.y <= 1 || at.x < 0 || slot0 >= p.slots) return;
   const int32_t n = min(at.y, p.slots - slot0);
   const int64_t base = ((int64_t)(head / p.group) * p.slots + slot0) * R + rr;
-  float top = -INFINITY;
-  for (int32_t i = lane; i < n; i += 64) top = fmaxf(top, p.part_ml[base + (int64_t)i * R].x);
-  top = wave_max(top);
-  float sum = 0.0f, acc[kV] = {};
-  if (top != -INFINITY) {
-#pragma unroll 4
-    for (int32_t i = 0; i < n; ++i) {
-      const int64_t e = base + (int64_t)i * R;
-      const float2 ml = p.part_ml[e];
-      const float f = __builtin_amdgcn_exp2f(ml.x - top);
-      sum += ml.y * f;
+  float top = -INFINITY, sum = 0.0f, acc[kV] = {};
+  for (int32_t i0 = part; i0 < n; i0 += 8 * N) {
+    float2 ml[8];
+    float x[8][kV];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t e = base + (int64_t)min(i0 + j * N, n - 1) * R;
+      ml[j] = p.part_ml[e];
       const float* src = p.part + e * D + lane * kV;
 #pragma unroll
-      for (int x = 0; x < kV; ++x) acc[x] += src[x] * f;
+      for (int y = 0; y < kV; ++y) x[j][y] = src[y];
+    }
+    float now = top;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) now = fmaxf(now, ml[j].x);
+    if (now == -INFINITY) continue;
+    const float keep = __builtin_amdgcn_exp2f(top - now);
+    top = now;
+    sum *= keep;
+#pragma unroll
+    for (int y = 0; y < kV; ++y) acc[y] *= keep;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = i0 + j * N < n ? __builtin_amdgcn_exp2f(ml[j].x - now) : 0.0f;
+      sum += ml[j].y * f;
+#pragma unroll
+      for (int y = 0; y < kV; ++y) acc[y] += x[j][y] * f;
+    }
+  }
+  if constexpr (N > 1) {
+    if (lane == 0) {
+      top_of[wave] = top;
+      sum_of[wave] = sum;
+    }
+#pragma unroll
+    for (int y = 0; y < kV; ++y) acc_of[wave][lane * kV + y] = acc[y];
+    __syncthreads();
+    if (wave != 0) return;
+    for (int w = 0; w < N; ++w) top = fmaxf(top, top_of[w]);
+    sum = 0.0f;
+#pragma unroll
+    for (int y = 0; y < kV; ++y) acc[y] = 0.0f;
+    for (int w = 0; w < N; ++w) {
+      const float f = top_of[w] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top_of[w] - top);
+      sum += sum_of[w] * f;
+#pragma unroll
+      for (int y = 0; y < kV; ++y) acc[y] += acc_of[w][lane * kV + y] * f;
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

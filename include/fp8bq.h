@@ -396,7 +396,7 @@ typedef struct fp8bq_kv_cache {
  * These arrays live on the device and are not checked by the host.  The
  * kernels read and write nothing outside the buffers whatever they hold:
  * tokens whose page number is not in 0 .. num_pages - 1, or whose position is
- * negative or beyond max_pages pages, are neither stored nor seen, and
+ * negative, beyond max_pages pages or above 2^31 - 1024, are neither stored nor seen, and
  * query_start is clamped to 0 .. tokens.  Rows of no sequence are left as they
  * are.
  */
