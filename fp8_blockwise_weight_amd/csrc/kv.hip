@@ -90,8 +90,10 @@ void kv_for_dim(int32_t dim, F&& f) {
 struct KvShape {
   int32_t group;       // query heads per key/value head
   int32_t rows;        // query rows (tokens x heads of a group) of a workgroup
-  int32_t slots;       // workgroups per key/value head
+  int32_t grid;        // workgroups per key/value head
   int32_t target;      // of these, how many splitting the keys aims at; 0: no splits
+  int32_t slots;       // places for partial sums per key/value head
+  int32_t jump;
   int32_t min_tiles;
   size_t rows_at, ml_at, bytes;   // workspace: partial sums at 0, then these
 };
@@ -101,19 +103,20 @@ KvShape kv_shape(int32_t kv_heads, int32_t dim, int32_t q_heads, int32_t count, 
   s.group = q_heads / kv_heads;
   const int64_t per_seq = ceil_div(tokens * s.group, count);
   s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 ? 64 : 128));
-  const int64_t base = tokens * s.group / s.rows + count;
-#ifndef KV_T
-#define KV_T 1024
-#endif
-#ifndef KV_B
-#define KV_B 4096
-#endif
-#ifndef KV_MIN
-#define KV_MIN 4
-#endif
-  s.target = base * kv_heads >= KV_B ? 0 : static_cast<int32_t>(ceil_div(KV_T, kv_heads));
-  s.min_tiles = KV_MIN;
-  s.slots = static_cast<int32_t>(base + s.target);
+  const int resident = s.rows == 16 ? (dim == 64 ? 768 : 512) : (s.rows == 64 ? 1024 : (s.rows == 128 ? 512 : 256));
+  s.min_tiles = 4;
+  if (s.rows <= 32) {
+    s.target = static_cast<int32_t>(ceil_div(resident, kv_heads));
+    s.grid = s.target;
+    s.slots = 2 * s.target;
+    s.jump = s.target;
+  } else {
+    const int64_t base = tokens * s.group / s.rows + count;
+    s.target = base * kv_heads >= resident ? 0 : static_cast<int32_t>(ceil_div(resident, kv_heads));
+    s.grid = static_cast<int32_t>(base + s.target);
+    s.slots = s.grid;
+    s.jump = 0;
+  }
   const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(kv_heads) * static_cast<size_t>(s.rows);
   s.ml_at = n * static_cast<size_t>(dim) * 4;
   s.rows_at = s.ml_at + n * 8;
@@ -237,12 +240,13 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   d.window = q->window;
   d.slots = s.slots;
   d.target = s.target;
+  d.jump = s.jump;
   d.min_tiles = s.min_tiles;
   d.scale = q->scale * 1.4426950408889634f;
   hipStream_t st = static_cast<hipStream_t>(stream);
   kv_for_dim(cache->head_dim, [&](auto dim) {
     constexpr int D = decltype(dim)::value;
-    const dim3 grid(static_cast<unsigned>(s.slots) * static_cast<unsigned>(cache->kv_heads));
+    const dim3 grid(static_cast<unsigned>(s.grid) * static_cast<unsigned>(cache->kv_heads));
     switch (s.rows) {
       case 16: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 1>), grid, dim3(256), 0, st, c, b, d); break;
       case 32: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 2>), grid, dim3(256), 0, st, c, b, d); break;

@@ -466,22 +466,14 @@ struct KvQuery {
   int32_t tokens;
   int32_t group;
   int32_t window;      // 0: none
-  int32_t slots;       // work items per key/value head
-  int32_t target;      // items per head that splitting aims at; 0: no splits
+  int32_t slots;       // places for partial sums per key/value head
+  int32_t target;      // work items per head that splitting aims at; 0: no splits
+  int32_t jump;        // second and later slots of a row tile: first + jump + 1, ...
   int32_t min_tiles;   // least key tiles of a split
   float scale;         // of the scores, times log2(e)
 };
 
 constexpr int kKeyTile = 64;
-#ifndef KV_NT
-#define KV_NT 1
-#endif
-#if KV_NT
-#define KVLOAD(p) __builtin_nontemporal_load(p)
-#else
-#define KVLOAD(p) (*(p))
-#endif
-
 // The work of one workgroup: a tile of query rows of a sequence and a range
 // of its key tiles.
 struct KvWork {
@@ -489,15 +481,22 @@ struct KvWork {
   int32_t first, count;     // first query row (token * group + head in group) of the tile; rows of the sequence
   int32_t pos0;             // position of the sequence's first query token
   int32_t tile0, tile1;     // key tiles
-  int32_t splits, split;
+  int32_t parts, slot;      // how many work items share the row tile's keys, and where this one's sums go
+  bool begin;               // whether this one has the first of them
 };
 
 // Sum over lanes 0 .. i, for every lane i (data-parallel moves, no LDS).
 template <typename T>
 __device__ __forceinline__ T wave_scan(T v) {
   auto from = [](T x, auto ctrl, auto rows) {
-    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
-                                                             decltype(rows)::value, 0xF, false));
+    auto move = [](int y) {
+      return __builtin_amdgcn_update_dpp(0, y, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+    };
+    if constexpr (sizeof(T) == 4) {
+      return __builtin_bit_cast(T, move(__builtin_bit_cast(int, x)));
+    } else {
+      return (T)(((uint64_t)(uint32_t)move((int)(x >> 32)) << 32) | (uint32_t)move((int)x));
+    }
   };
   using std::integral_constant;
   v += from(v, integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // row_shr:1
@@ -510,6 +509,9 @@ __device__ __forceinline__ T wave_scan(T v) {
 }
 
 __device__ __forceinline__ int32_t lane_of(int32_t v, int32_t lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ int64_t lane_of(int64_t v, int32_t lane) {
+  return (int64_t)(((uint64_t)(uint32_t)lane_of((int32_t)(v >> 32), lane) << 32) | (uint32_t)lane_of((int32_t)v, lane));
+}
 
 // Positions stay below 2^31 - 1024, so that a tile's end is in 32 bits.
 __device__ __forceinline__ int32_t kv_capacity(const KvBatch& bt, int32_t log_s) {
@@ -521,47 +523,56 @@ __device__ __forceinline__ int32_t kv_low(int32_t end, int32_t window) {
   return window > 0 ? max(max(end, 0) - window, 0) : 0;
 }
 
-// Which work item w is.  Every wave reads the batch's lengths and lays the
-// items out by itself: sequence b has ceil(rows / R) row tiles of
-// ceil(key tiles / chunk) splits each, with one chunk for the whole batch
-// such that about `target` items come out of it.  The grid depends on the
-// number of sequences and query tokens alone, so a captured launch stays
-// right, and balanced, as the lengths grow.
+// A sequence of the call: its rows, and its key tiles as far as any of its
+// queries sees them.
+struct KvSeq {
+  int32_t row0, n, len, rtiles, tile0, tiles;
+};
+
 template <int R>
-__device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int32_t log_s, int32_t w,
-                                        KvWork& k) {
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvQuery& p, int32_t cap, int32_t b) {
+  KvSeq s{0, 0, 0, 0, 0, 0};
+  if (b >= bt.count) return s;
+  s.len = max(bt.lens[b], 0);
+  if (bt.starts) {
+    s.row0 = kv_clamp(bt.starts[b], p.tokens);
+    s.n = max(kv_clamp(bt.starts[b + 1], p.tokens) - s.row0, 0);
+  } else {
+    s.row0 = b;
+    s.n = 1;
+  }
+  s.rtiles = (int32_t)(((uint32_t)s.n * (uint32_t)p.group + R - 1) / R);   // at most 2^25 rows
+  const int32_t hi = min(s.len, cap), lo = kv_low(s.len - s.n + 1, p.window);
+  if (s.n > 0 && hi > lo) {
+    s.tile0 = lo / kKeyTile;
+    s.tiles = (hi + kKeyTile - 1) / kKeyTile - s.tile0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ KvSeq lane_of(const KvSeq& s, int32_t lane) {
+  return KvSeq{lane_of(s.row0, lane), lane_of(s.n, lane), lane_of(s.len, lane),
+               lane_of(s.rtiles, lane), lane_of(s.tile0, lane), lane_of(s.tiles, lane)};
+}
+
+// Every wave reads the batch's lengths and finds its work by itself, in one of
+// two ways.  Grids depend on the number of sequences and query tokens alone,
+// so a captured launch stays right, and balanced, as the lengths grow.
+//
+// kv_plan, for workgroups that do one item each: sequence b has
+// ceil(rows / R) row tiles of ceil(key tiles / chunk) splits each, with one
+// chunk for the whole batch such that about `target` items come out of it.
+template <int R>
+__device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int32_t cap, int32_t w, KvWork& k) {
   const int32_t lane = threadIdx.x & 63;
-  const int32_t cap = kv_capacity(bt, log_s);
-  struct Seq {
-    int32_t row0, n, len, rtiles, tile0, tiles;
-  };
-  auto seq = [&](int32_t b) {
-    Seq s{0, 0, 0, 0, 0, 0};
-    if (b >= bt.count) return s;
-    s.len = max(bt.lens[b], 0);
-    if (bt.starts) {
-      s.row0 = kv_clamp(bt.starts[b], p.tokens);
-      s.n = max(kv_clamp(bt.starts[b + 1], p.tokens) - s.row0, 0);
-    } else {
-      s.row0 = b;
-      s.n = 1;
-    }
-    s.rtiles = (int32_t)(((uint32_t)s.n * (uint32_t)p.group + R - 1) / R);   // at most 2^25 rows
-    const int32_t hi = min(s.len, cap), lo = kv_low(s.len - s.n + 1, p.window);
-    if (s.n > 0 && hi > lo) {
-      s.tile0 = lo / kKeyTile;
-      s.tiles = (hi + kKeyTile - 1) / kKeyTile - s.tile0;
-    }
-    return s;
-  };
-  Seq mine = seq(lane);
+  KvSeq mine = kv_seq<R>(bt, p, cap, lane);
   int32_t chunk = INT32_MAX;
   if (p.target > 0) {
     // fp32 is enough, with room for its rounding: the chunk may only be too
     // long, never so short that there are more items than slots
     float total = (float)mine.rtiles * (float)mine.tiles;
     for (int32_t b = 64; b < bt.count; b += 64) {
-      const Seq s = seq(b + lane);
+      const KvSeq s = kv_seq<R>(bt, p, cap, b + lane);
       total += (float)s.rtiles * (float)s.tiles;
     }
     total = __int_as_float(lane_of(__float_as_int(wave_scan(total)), 63));
@@ -570,33 +581,119 @@ __device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int
   }
   int64_t before = 0;
   for (int32_t b0 = 0; b0 < bt.count; b0 += 64) {
-    if (b0 > 0) mine = seq(b0 + lane);
+    if (b0 > 0) mine = kv_seq<R>(bt, p, cap, b0 + lane);
     const int32_t splits = max(1, (int32_t)(((int64_t)mine.tiles + chunk - 1) / chunk));
     const int32_t items = (int32_t)min((int64_t)mine.rtiles * splits, (int64_t)1 << 24);
     const int32_t sum = wave_scan(items);
     const uint64_t past = __ballot(before + sum > w);
     if (past != 0) {
       const int32_t at = __ffsll((unsigned long long)past) - 1;
-      k.b = b0 + at;
-      k.row0 = lane_of(mine.row0, at);
-      k.n = lane_of(mine.n, at);
-      k.pos0 = lane_of(mine.len, at) - k.n;
-      k.splits = lane_of(splits, at);
-      const int32_t tile0 = lane_of(mine.tile0, at), tiles = lane_of(mine.tiles, at);
+      const KvSeq s = lane_of(mine, at);
+      const int32_t of = lane_of(splits, at);
       const int32_t local = (int32_t)(w - before) - (lane_of(sum, at) - lane_of(items, at));
-      const int32_t rtile = local / k.splits;
-      k.split = local - rtile * k.splits;
+      const int32_t rtile = local / of, split = local - rtile * of;
+      k.b = b0 + at;
+      k.row0 = s.row0;
+      k.n = s.n;
+      k.pos0 = s.len - s.n;
+      k.parts = of;
+      k.begin = split == 0;
       // the last rows see the most keys: they go first
-      k.first = (lane_of(mine.rtiles, at) - 1 - rtile) * R;
-      k.count = k.n * p.group;
-      k.tile0 = tile0 + min((int64_t)k.split * chunk, (int64_t)tiles);
-      k.tile1 = tile0 + min((int64_t)(k.split + 1) * chunk, (int64_t)tiles);
+      k.first = (s.rtiles - 1 - rtile) * R;
+      k.count = s.n * p.group;
+      k.tile0 = s.tile0 + min((int64_t)split * chunk, (int64_t)s.tiles);
+      k.tile1 = s.tile0 + min((int64_t)(split + 1) * chunk, (int64_t)s.tiles);
+      k.slot = w;
       return true;
     }
     before += lane_of(sum, 63);
   }
   return false;
 }
+
+// KvShares, for a grid that the chip holds at once: the key tiles of all row
+// tiles, one after another, are cut into `target` equal shares.  A workgroup
+// goes through its share row tile by row tile; only the first and the last of
+// them can continue in a neighbour's.  Everyone ends at the same time whatever
+// the lengths are, and nothing is started twice.  The partial sums of a row
+// tile that begins in share i are slot i, those of it in a later share j slot
+// target + j.
+template <int R>
+struct KvShares {
+  const KvBatch& bt;
+  const KvQuery& p;
+  int32_t cap, index;
+  int64_t at, end, share;   // this share's tiles, counted over the whole batch
+  int32_t b, rtile, t;      // the next one's sequence, row tile and tile
+  KvSeq s;
+
+  static __device__ __forceinline__ int64_t weight(const KvSeq& s) {
+    return (int64_t)s.rtiles * max(s.tiles, 1);   // a row that sees nothing is written, too
+  }
+
+  __device__ __forceinline__ KvShares(const KvBatch& bt_, const KvQuery& p_, int32_t cap_, int32_t index_)
+      : bt(bt_), p(p_), cap(cap_), index(index_), at(0), end(0), share(1), b(0), rtile(0), t(0) {
+    const int32_t lane = threadIdx.x & 63;
+    KvSeq mine = kv_seq<R>(bt, p, cap, lane);
+    int64_t total = lane_of(wave_scan(weight(mine)), 63);
+    for (int32_t b0 = 64; b0 < bt.count; b0 += 64) {
+      total += lane_of(wave_scan(weight(kv_seq<R>(bt, p, cap, b0 + lane))), 63);
+    }
+    share = (int64_t)__builtin_ceil((double)total / (double)p.target);
+    if (share * p.target < total) ++share;
+    share = lane_of(max(share, (int64_t)p.min_tiles), 0);
+    at = index * share;
+    end = min(at + share, total);
+    if (at >= end) return;
+    int64_t before = 0;
+    for (int32_t b0 = 0; b0 < bt.count; b0 += 64) {
+      if (b0 > 0) mine = kv_seq<R>(bt, p, cap, b0 + lane);
+      const int64_t w = weight(mine), sum = wave_scan(w);
+      const uint64_t past = __ballot(before + sum > at);
+      if (past != 0) {
+        const int32_t which = __ffsll((unsigned long long)past) - 1;
+        s = lane_of(mine, which);
+        b = b0 + which;
+        const int64_t off = at - (before + lane_of(sum, which) - lane_of(w, which));
+        const int32_t tiles = max(s.tiles, 1);
+        rtile = off < tiles ? 0 : (int32_t)(off / tiles);
+        t = (int32_t)(off - (int64_t)rtile * tiles);
+        return;
+      }
+      before += lane_of(sum, 63);
+    }
+  }
+
+  __device__ __forceinline__ bool next(KvWork& k) {
+    if (at >= end) return false;
+    while (rtile >= s.rtiles) {
+      if (++b >= bt.count) return false;
+      rtile = 0;
+      s = kv_seq<R>(bt, p, cap, b);
+      s = lane_of(s, 0);
+    }
+    const int32_t tiles = max(s.tiles, 1);
+    const int32_t take = (int32_t)min((int64_t)(tiles - t), end - at);
+    k.b = b;
+    k.row0 = s.row0;
+    k.n = s.n;
+    k.pos0 = s.len - s.n;
+    k.first = rtile * R;
+    k.count = s.n * p.group;
+    k.tile0 = s.tile0 + t;
+    k.tile1 = s.tile0 + min(t + take, s.tiles);
+    k.begin = t == 0;
+    k.parts = 1;
+    if (t > 0 || t + take < tiles) {
+      k.parts = 1 + (int32_t)((at - t + tiles - 1) / share) - (int32_t)((at - t) / share);
+    }
+    k.slot = k.begin ? index : p.target + index;
+    at += take;
+    t = 0;
+    ++rtile;
+    return true;
+  }
+};
 
 // What the query rows of a work item see: some of them keys see_lo ..
 // see_hi - 1, all of them all_lo .. all_hi - 1; and the tiles to visit.
@@ -640,20 +737,16 @@ __device__ __forceinline__ bf16x8 kv_widen(uint32_t a, uint32_t b) {
   return bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
-#ifdef KV_NOSB
-#define SB
-#else
-#define SB __builtin_amdgcn_sched_barrier(0)
-#endif
-#ifndef KV_LB
-#define KV_LB (NT == 1 ? 2 : 1)
-#endif
 // The largest part of D channels, in equal parts of whole 16s, within `most`.
 constexpr int kv_part(int d, int most) {
   int parts = 1;
   while (d / parts > most || d % (16 * parts) != 0) ++parts;
   return d / parts;
 }
+
+// Waves of kv_attend_rows that a SIMD holds: what its registers allow without
+// spilling (a spill of four registers at D = 256 took a 91 us call to 107).
+constexpr int kv_rows_per_simd(int d, int nt) { return nt > 1 ? 1 : (d == 64 ? 4 : (d == 128 ? 3 : 2)); }
 
 // Few query rows: R = 16 NT rows of a sequence (tokens times the query heads
 // that share a key head) in each of four waves, which take every fourth key
@@ -671,277 +764,274 @@ constexpr int kv_part(int d, int most) {
 // fp32 sums); scales enter in fp32, k's with the score, v's with the weight,
 // which is then rounded to BF16 once (relative 2^-9, its sum is not).
 template <int D, int NT>
-__global__ __launch_bounds__(kThreads, KV_LB) void kv_attend_rows(KvCache c, KvBatch bt,
-                                                                                         KvQuery p) {
+__global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_rows(KvCache c, KvBatch bt, KvQuery p) {
   constexpr int R = 16 * NT;
   constexpr int kI = D / 64;    // 64-channel pieces
   constexpr int kDt = D / 16;   // 16-channel tiles of the output
-#ifndef KV_AHEAD
-#define KV_AHEAD (D <= 128)
-#endif
-  constexpr bool kAhead = KV_AHEAD;
   constexpr int kPart = kv_part(D, 2048 / R);   // channels that are joined at a time: 8 per thread at most
-  __shared__ __align__(16) float lds_o[4][R][kPart + 4];
+  // the queries, later the waves' sums
+  constexpr int kSums = 4 * R * (kPart + 4), kQueries = R * (D + 8) / 2;
+  __shared__ __align__(16) float lds[kSums > kQueries ? kSums : kQueries];
   __shared__ float lds_m[4][R], lds_l[4][R];
-  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t col = lane & 15, grp = lane >> 4;
   const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
-  KvWork wk;
-  if (!kv_plan<R>(bt, p, c.log_s, w_item, wk)) return;
   const int32_t S = 1 << c.log_s, cap = kv_capacity(bt, c.log_s);
-  const KvSeen see = kv_seen<R>(wk, p, cap);
-
-  int32_t row_hi[NT], row_lo[NT];
-  bf16x8 q[NT][kI][2];
-  const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int32_t r = wk.first + nt * 16 + col;
-    const bool live = r < wk.count;
-    const int32_t tok = live ? r / p.group : 0;
-    const int32_t g = live ? r - tok * p.group : 0;
-    row_hi[nt] = live ? min(wk.pos0 + tok + 1, cap) : 0;
-    row_lo[nt] = kv_low(wk.pos0 + tok + 1, p.window);
-    const uint16_t* src = p.q + (wk.row0 + tok) * p.q_tok + ((int64_t)h * p.group + g) * p.q_head + 16 * grp;
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        u32x4 x = *(const u32x4*)(src + 64 * i + 8 * y);
-        x ^= u32x4{flip, flip, flip, flip};
-        if (!live) x = u32x4{0, 0, 0, 0};
-        q[nt][i][y] = __builtin_bit_cast(bf16x8, x);
-      }
-    }
-  }
   const float scale = fabsf(p.scale);
-
-  f32x4 o[NT][kDt];
-  float m[NT], l[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = -INFINITY;
-    l[nt] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kDt; ++i) o[nt][i] = f32x4{0, 0, 0, 0};
-  }
-
-  const int32_t* table = bt.table + (int64_t)wk.b * bt.stride;
-  // Page of the 16 tokens from t0 on, -1 where none of them is seen or the
-  // table's entry is no page.
-  auto page_of = [&](int32_t t0) {
-    int32_t pg = -1;
-    if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> c.log_s];
-    return pg >= 0 && pg < c.pages ? pg : -1;
-  };
-  const int32_t k_run = col >> 2;
-  const bool half_rows = S > kKeyTile;
-  // One tile's codes: the next tile's keys are loaded into the same registers
-  // as soon as the scores are done, its values after the weighted sum, so
-  // that half a tile at least is always in flight.
-  u32x4 xk[4][kI], xv[kDt];
-  float ks_next, vs_next;
-  auto load_k = [&](int32_t tile, int32_t pk, int32_t pv) {
-    const int32_t tk = tile * kKeyTile + 16 * k_run;
-    const int64_t kblock = (int64_t)max(pk, 0) * c.heads + h, vblock = (int64_t)max(pv, 0) * c.heads + h;
-    const uint8_t* kp = c.k + kblock * S * D + ((tk & (S - 1)) + (col & 3)) * D + 16 * grp;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int i = 0; i < kI; ++i) xk[t][i] = KVLOAD((const u32x4*)(kp + t * 4 * D + 64 * i));
-    }
-    ks_next = c.ks[vblock];
-    vs_next = c.vs[vblock];
-  };
-  auto load_v = [&](int32_t tile, int32_t pv) {
-    const int32_t tv = tile * kKeyTile + 16 * grp;
-    const int64_t vblock = (int64_t)max(pv, 0) * c.heads + h;
-    const uint8_t* vp = c.v + vblock * S * D + (int64_t)col * S + (tv & (S - 1));
-#pragma unroll
-    for (int i = 0; i < kDt; ++i) {
-      const u32x4* at = (const u32x4*)(vp + i * 16 * S);
-      xv[i] = half_rows ? *at : KVLOAD(at);
-    }
-  };
-  // Tile `tile`, whose values lie in pages pv, and the next one's loads.
-  auto compute = [&](int32_t tile, int32_t pv, bool more, int32_t pk_next, int32_t pv_next) {
-    const bool ok = pv >= 0;
-    const float f = ok ? ks_next * scale : 0.0f, vs = ok ? vs_next : 0.0f;
-    const int32_t t0 = tile * kKeyTile;
-    f32x4 s[NT][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][t] = f32x4{0, 0, 0, 0};
+  const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
+  KvShares<R> shares(bt, p, cap, w_item);
+  KvWork wk;
+  while (shares.next(wk)) {
+    // Hidden from the compiler, which would keep what follows from it in
+    // registers across row tiles and spill others for that.
+    int32_t tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int32_t lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int32_t col = lane & 15, grp = lane >> 4, k_run = col >> 2;
+    const KvSeen see = kv_seen<R>(wk, p, cap);
+    const int32_t* table = bt.table + (int64_t)wk.b * bt.stride;
+    // Page of a run of 16 tokens, -1 where none of them is seen or the table's
+    // entry is no page.
+    auto page_at = [&](int32_t tile, int32_t run) {
+      const int32_t t0 = min(tile, see.tile1 - 1) * kKeyTile + 16 * run;
+      int32_t pg = -1;
+      if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> c.log_s];
+      return pg >= 0 && pg < c.pages ? pg : -1;
+    };
+    u32x4 xk[4][kI], xv[kDt];
+    float ks, vs;
+    auto load_k = [&](int32_t tile, int32_t pk, int32_t pv) {
+      const int32_t tk = tile * kKeyTile + 16 * k_run;
+      const int64_t kblock = (int64_t)max(pk, 0) * c.heads + h, vblock = (int64_t)max(pv, 0) * c.heads + h;
+      const uint8_t* kp = c.k + kblock * S * D + ((tk & (S - 1)) + (col & 3)) * D + 16 * grp;
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        const bf16x8 a = kv_widen(xk[t][i][0], xk[t][i][1]), b = kv_widen(xk[t][i][2], xk[t][i][3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[nt][i][0], s[nt][t], 0, 0, 0);
-          s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, q[nt][i][1], s[nt][t], 0, 0, 0);
-        }
+        for (int t = 0; t < 4; ++t) xk[t][i] = __builtin_nontemporal_load((const u32x4*)(kp + t * 4 * D + 64 * i));
       }
-      SB;
-    }
-    if constexpr (kAhead) {
-      if (more) load_k(tile + 4, pk_next, pv_next);
-    } else {
-      __builtin_amdgcn_sched_barrier(0);   // not before the keys' registers are free
-      load_v(tile, pv);
-    }
-    const bool edge = __ballot(!ok) != 0 || t0 < see.all_lo || t0 + kKeyTile > see.all_hi;
-    if (edge) {
-      // What nobody sees counts as code 0 with weight 0, whatever is there.
-      const int32_t run = t0 + 16 * grp;
-      const u32x4 keep = kv_bytes(see.see_lo - run, ok ? see.see_hi - run : 0);
+      ks = c.ks[vblock];
+      vs = c.vs[vblock];
+    };
+    // Not past the cache: a page row of v longer than a tile is read in pieces
+    // of half a cache line, whose other half the next tile's wave wants.
+    auto load_v = [&](int32_t tile, int32_t pv) {
+      const int32_t tv = tile * kKeyTile + 16 * grp;
+      const int64_t vblock = (int64_t)max(pv, 0) * c.heads + h;
+      const uint8_t* vp = c.v + vblock * S * D + (int64_t)col * S + (tv & (S - 1));
 #pragma unroll
-      for (int i = 0; i < kDt; ++i) xv[i] &= keep;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int32_t lo = row_lo[nt] - run, hi = ok ? row_hi[nt] - run : 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[nt][e >> 2][e & 3] = e >= lo && e < hi ? s[nt][e >> 2][e & 3] : -INFINITY;
+      for (int i = 0; i < kDt; ++i) {
+        xv[i] = *(const u32x4*)(vp + i * 16 * S);
       }
+    };
+
+    int32_t tile = see.tile0 + wave;
+    int32_t pk = -1, pv = -1, pk_next = -1, pv_next = -1;
+    if (tile < see.tile1) {
+      pk = page_at(tile, k_run);
+      pv = page_at(tile, grp);
+      load_k(tile, pk, pv);
+      pk_next = page_at(tile + 4, k_run);
+      pv_next = page_at(tile + 4, grp);
     }
-    bf16x8 w[NT][2];
+    // The queries in LDS, where all waves read them: row pitch 2 D + 16 bytes.
+    uint16_t* q_lds = (uint16_t*)lds;
+    for (int32_t i = tid; i < R * (D / 8); i += kThreads) {
+      const int32_t rr = i / (D / 8), ch = i - rr * (D / 8), r = wk.first + rr;
+      u32x4 x = {0, 0, 0, 0};
+      if (r < wk.count) {
+        const int32_t tok = r / p.group, g = r - tok * p.group;
+        x = *(const u32x4*)(p.q + (wk.row0 + tok) * p.q_tok + ((int64_t)h * p.group + g) * p.q_head + 8 * ch);
+        x ^= u32x4{flip, flip, flip, flip};
+      }
+      *(u32x4*)(q_lds + rr * (D + 8) + 8 * ch) = x;
+    }
+    f32x4 o[NT][kDt];
+    float m[NT], l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float top = s[nt][0][0];
+      m[nt] = -INFINITY;
+      l[nt] = 0.0f;
 #pragma unroll
-      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[nt][e >> 2][e & 3]);
-      // -inf times a factor of 0 (a run of no page) is no maximum
-      top = top == -INFINITY ? -INFINITY : top * f;
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__ballot(top > m[nt] + 8.0f) != 0) {
-        const float now = fmaxf(m[nt], top);
-        const float x = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
-        m[nt] = now;
-        l[nt] *= x;
-#pragma unroll
-        for (int i = 0; i < kDt; ++i) o[nt][i] *= x;
-      }
-      const float base = m[nt] == -INFINITY ? 0.0f : -m[nt];
-      float sum = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float x = s[nt][e >> 2][e & 3];
-        float z = __builtin_fmaf(x, f, base);
-        if (edge) z = x == -INFINITY ? -INFINITY : z;
-        const float pe = __builtin_amdgcn_exp2f(z);
-        sum += pe;
-        w[nt][e >> 3][e & 7] = (__bf16)(pe * vs);
-      }
-      l[nt] += sum;
+      for (int i = 0; i < kDt; ++i) o[nt][i] = f32x4{0, 0, 0, 0};
     }
-#pragma unroll
-    for (int i = 0; i < kDt; ++i) {
-      const bf16x8 a = kv_widen(xv[i][0], xv[i][1]), b = kv_widen(xv[i][2], xv[i][3]);
+    __syncthreads();
+
+    // One tile at a time: its values' loads are in flight during the softmax,
+    // the next one's keys when the others compute.  Two or three workgroups
+    // to a CU keep more than enough bytes in flight; loading further ahead
+    // measured no gain, and its registers cost a workgroup.
+    for (; tile < see.tile1; tile += 4) {
+      const int32_t pk_after = page_at(tile + 8, k_run), pv_after = page_at(tile + 8, grp);
+      const bool ok = pv >= 0;
+      const float f = ok ? ks * scale : 0.0f, vw = ok ? vs : 0.0f;
+      const int32_t t0 = tile * kKeyTile;
+      f32x4 s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w[nt][0], o[nt][i], 0, 0, 0);
-        o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, w[nt][1], o[nt][i], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[nt][t] = f32x4{0, 0, 0, 0};
       }
-      if (i % 2 == 1) SB;
-    }
-  };
-  int32_t tile = see.tile0 + wave;
-  if (tile < see.tile1) {
-    auto page_at = [&](int32_t tl, int32_t run) { return page_of(min(tl, see.tile1 - 1) * kKeyTile + 16 * run); };
-    int32_t pv = page_at(tile, grp);
-    int32_t pk_next = page_at(tile, k_run), pv_next = pv;
-    load_k(tile, pk_next, pv);
-    if constexpr (kAhead) load_v(tile, pv);
-    pk_next = page_at(tile + 4, k_run);
-    pv_next = page_at(tile + 4, grp);
-    for (; tile < see.tile1; tile += 4) {
-      const bool more = tile + 4 < see.tile1;
-      const int32_t pk_after = page_at(tile + 8, k_run), pv_after = page_at(tile + 8, grp);
-      compute(tile, pv, more, pk_next, pv_next);
-      if constexpr (kAhead) {
-        if (more) load_v(tile + 4, pv_next);
-      } else {
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) load_k(tile + 4, pk_next, pv_next);
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        bf16x8 q[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            q[nt][y] = *(const bf16x8*)(q_lds + (nt * 16 + col) * (D + 8) + 64 * i + 16 * grp + 8 * y);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bf16x8 a = kv_widen(xk[t][i][0], xk[t][i][1]), b = kv_widen(xk[t][i][2], xk[t][i][3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[nt][0], s[nt][t], 0, 0, 0);
+            s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, q[nt][1], s[nt][t], 0, 0, 0);
+          }
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);   // the values' registers are the keys'
+      load_v(tile, pv);
+      const bool edge = __ballot(!ok) != 0 || t0 < see.all_lo || t0 + kKeyTile > see.all_hi;
+      const int32_t run = t0 + 16 * grp;
+      if (edge) {
+        int32_t r = wk.first + col;
+        asm volatile("" : "+v"(r));   // few tiles are edges: no registers for this across the others
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt, r += 16) {
+          const int32_t last = wk.pos0 + r / p.group + 1;
+          const int32_t lo = kv_low(last, p.window) - run, hi = ok && r < wk.count ? min(last, cap) - run : 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[nt][e >> 2][e & 3] = e >= lo && e < hi ? s[nt][e >> 2][e & 3] : -INFINITY;
+        }
+      }
+      bf16x8 w[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float top = s[nt][0][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[nt][e >> 2][e & 3]);
+        // -inf times a factor of 0 (a run of no page) is no maximum
+        top = top == -INFINITY ? -INFINITY : top * f;
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // sums are rescaled only when a maximum has grown by more than 2^8
+        if (__ballot(top > m[nt] + 8.0f) != 0) {
+          const float now = fmaxf(m[nt], top);
+          const float x = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
+          m[nt] = now;
+          l[nt] *= x;
+#pragma unroll
+          for (int i = 0; i < kDt; ++i) o[nt][i] *= x;
+        }
+        const float base = m[nt] == -INFINITY ? 0.0f : -m[nt];
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = s[nt][e >> 2][e & 3];
+          float z = __builtin_fmaf(x, f, base);
+          if (edge) z = x == -INFINITY ? -INFINITY : z;
+          const float pe = __builtin_amdgcn_exp2f(z);
+          sum += pe;
+          w[nt][e >> 3][e & 7] = (__bf16)(pe * vw);
+        }
+        l[nt] += sum;
+      }
+      if (edge) {
+        // What nobody sees counts as code 0, whatever is there.
+        const u32x4 keep = kv_bytes(see.see_lo - run, ok ? see.see_hi - run : 0);
+#pragma unroll
+        for (int i = 0; i < kDt; ++i) xv[i] &= keep;
+      }
+#pragma unroll
+      for (int i = 0; i < kDt; ++i) {
+        const bf16x8 a = kv_widen(xv[i][0], xv[i][1]), b = kv_widen(xv[i][2], xv[i][3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w[nt][0], o[nt][i], 0, 0, 0);
+          o[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, w[nt][1], o[nt][i], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (tile + 4 < see.tile1) load_k(tile + 4, pk_next, pv_next);
       pv = pv_next;
       pk_next = pk_after;
       pv_next = pv_after;
     }
-  }
 
-  // Join the four waves: common maximum, then their sums one after another.
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    l[nt] += __shfl_xor(l[nt], 16);
-    l[nt] += __shfl_xor(l[nt], 32);
-    if (grp == 0) {
-      lds_m[wave][nt * 16 + col] = m[nt];
-      lds_l[wave][nt * 16 + col] = l[nt];
-    }
-  }
-  __syncthreads();
-  float f[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float top = -INFINITY;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][nt * 16 + col]);
-    f[nt] = m[nt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[nt] - top);
-  }
-  // Of each thread: 8 channels of one row, in every part.
-  const int32_t rr = threadIdx.x / (kPart / 8), ch = (threadIdx.x % (kPart / 8)) * 8, r = wk.first + rr;
-  const bool mine = rr < R && r < wk.count;
-  const int32_t tok = mine ? r / p.group : 0, g = mine ? r - tok * p.group : 0;
-  const int64_t head = (int64_t)h * p.group + g, row = wk.row0 + tok, all = (int64_t)c.heads * p.group;
-  const int64_t slot = (int64_t)h * p.slots + w_item;
-  float top = -INFINITY, sum = 0.0f;
-  if (mine) {
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][rr]);
-    for (int w = 0; w < 4; ++w) {
-      if (lds_m[w][rr] != -INFINITY) sum += lds_l[w][rr] * __builtin_amdgcn_exp2f(lds_m[w][rr] - top);
-    }
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int part = 0; part < D / kPart; ++part) {
-    if (part > 0) __syncthreads();
+    // Join the four waves: common maximum, then their sums one after another.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < kPart / 16; ++i) {
-        *(f32x4*)&lds_o[wave][nt * 16 + col][i * 16 + 4 * grp] = o[nt][part * (kPart / 16) + i] * f[nt];
+      l[nt] += __shfl_xor(l[nt], 16);
+      l[nt] += __shfl_xor(l[nt], 32);
+      if (grp == 0) {
+        lds_m[wave][nt * 16 + col] = m[nt];
+        lds_l[wave][nt * 16 + col] = l[nt];
       }
     }
     __syncthreads();
-    if (!mine) continue;
-    f32x4 a = *(const f32x4*)&lds_o[0][rr][ch], z = *(const f32x4*)&lds_o[0][rr][ch + 4];
-    for (int w = 1; w < 4; ++w) {
-      a += *(const f32x4*)&lds_o[w][rr][ch];
-      z += *(const f32x4*)&lds_o[w][rr][ch + 4];
-    }
-    const int32_t d = part * kPart + ch;
-    if (wk.splits > 1) {
-      f32x4* to = (f32x4*)(p.part + (slot * R + rr) * D + d);
-      to[0] = a;
-      to[1] = z;
-    } else {
-      bf16x8 y;
+    float f[NT];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = (__bf16)(a[e] * inv);
-        y[4 + e] = (__bf16)(z[e] * inv);
-      }
-      *(bf16x8*)(p.out + row * p.o_tok + head * p.o_head + d) = y;
+    for (int nt = 0; nt < NT; ++nt) {
+      float top = -INFINITY;
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][nt * 16 + col]);
+      f[nt] = m[nt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[nt] - top);
     }
+    // Of each thread: 8 channels of one row, in every part.
+    const int32_t rr = tid / (kPart / 8), ch = (tid % (kPart / 8)) * 8, r = wk.first + rr;
+    const bool mine = rr < R && r < wk.count;
+    const int32_t tok = mine ? r / p.group : 0, g = mine ? r - tok * p.group : 0;
+    const int64_t head = (int64_t)h * p.group + g, row = wk.row0 + tok, all = (int64_t)c.heads * p.group;
+    const int64_t slot = (int64_t)h * p.slots + wk.slot;
+    float top = -INFINITY, sum = 0.0f;
+    if (mine) {
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][rr]);
+      for (int w = 0; w < 4; ++w) {
+        if (lds_m[w][rr] != -INFINITY) sum += lds_l[w][rr] * __builtin_amdgcn_exp2f(lds_m[w][rr] - top);
+      }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int part = 0; part < D / kPart; ++part) {
+      if (part > 0) __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < kPart / 16; ++i) {
+          *(f32x4*)&lds[(wave * R + nt * 16 + col) * (kPart + 4) + i * 16 + 4 * grp] = o[nt][part * (kPart / 16) + i] * f[nt];
+        }
+      }
+      __syncthreads();
+      if (!mine) continue;
+      f32x4 a = *(const f32x4*)&lds[rr * (kPart + 4) + ch], z = *(const f32x4*)&lds[rr * (kPart + 4) + ch + 4];
+      for (int w = 1; w < 4; ++w) {
+        a += *(const f32x4*)&lds[(w * R + rr) * (kPart + 4) + ch];
+        z += *(const f32x4*)&lds[(w * R + rr) * (kPart + 4) + ch + 4];
+      }
+      const int32_t d = part * kPart + ch;
+      if (wk.parts > 1) {
+        f32x4* to = (f32x4*)(p.part + (slot * R + rr) * D + d);
+        to[0] = a;
+        to[1] = z;
+      } else {
+        bf16x8 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = (__bf16)(a[e] * inv);
+          y[4 + e] = (__bf16)(z[e] * inv);
+        }
+        *(bf16x8*)(p.out + row * p.o_tok + head * p.o_head + d) = y;
+      }
+    }
+    if (mine && ch == 0) {
+      if (wk.parts > 1) {
+        p.part_ml[slot * R + rr] = float2{top, sum};
+      } else if (p.lse) {
+        p.lse[row * all + head] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+      }
+      if (wk.begin) p.rows[row * all + head] = int2{wk.slot * R + rr, wk.parts};
+    }
+    __syncthreads();   // LDS is free for the next row tile
   }
-  if (!mine || ch != 0) return;
-  if (wk.splits > 1) {
-    p.part_ml[slot * R + rr] = float2{top, sum};
-  } else if (p.lse) {
-    p.lse[row * all + head] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-  }
-  if (p.rows && wk.split == 0) p.rows[row * all + head] = int2{w_item * R + rr, wk.splits};
 }
 
 // Many query rows: each of W waves holds 32 rows, and all of them share the
@@ -972,9 +1062,9 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   const int32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t col = lane & 31, half = lane >> 5;
   const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
-  KvWork wk;
-  if (!kv_plan<R>(bt, p, c.log_s, w_item, wk)) return;
   const int32_t log_s = c.log_s, S = 1 << log_s, cap = kv_capacity(bt, log_s);
+  KvWork wk;
+  if (!kv_plan<R>(bt, p, cap, w_item, wk)) return;
   const KvSeen see = kv_seen<R>(wk, p, cap);
 
   const int32_t r_mine = wk.first + wave * 32 + col;
@@ -1173,10 +1263,10 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   }
 
   l += __shfl_xor(l, 32);
-  const int64_t slot = (int64_t)h * p.slots + w_item;
+  const int64_t slot = (int64_t)h * p.slots + wk.slot;
   const int32_t rr = wave * 32 + col;
   const int64_t all = (int64_t)c.heads * p.group;
-  if (wk.splits > 1) {
+  if (wk.parts > 1) {
     if (live) {
       float* to = p.part + (slot * R + rr) * D + 4 * half;
 #pragma unroll
@@ -1226,12 +1316,12 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       p.lse[row * all + head] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
     }
   }
-  if (live && half == 0 && p.rows && wk.split == 0) p.rows[row * all + head] = int2{w_item * R + rr, wk.splits};
+  if (live && half == 0 && p.rows && wk.begin) p.rows[row * all + head] = int2{wk.slot * R + rr, wk.parts};
 }
 
 // Joins the partial sums of each query row whose keys were split, found
-// through `rows` (first slot times R plus row in tile, and how many slots, one
-// after another).  N waves share a row, each taking every Nth partial, all in
+// through `rows` (first slot times R plus row in tile, and how many slots; the
+// second is `jump` + 1 behind the first, the others follow it).  N waves share a row, each taking every Nth partial, all in
 // flight at once: with few rows of many splits, as one long sequence has, one
 // wave per row would add up its partials one round trip after another.
 template <int D, int N>
@@ -1251,7 +1341,7 @@ __global__ __launch_bounds__(N == 1 ? 256 : 64 * N) void kv_attend_join(KvBatch 
   const int2 at = p.rows[item];
   const int32_t slot0 = at.x / R, rr = at.x - slot0 * R;
   if (at.y <= 1 || at.x < 0 || slot0 >= p.slots) return;
-  const int32_t n = min(at.y, p.slots - slot0);
+  const int32_t n = min(at.y, max(p.slots - slot0 - p.jump, 1));
   const int64_t base = ((int64_t)(head / p.group) * p.slots + slot0) * R + rr;
   float top = -INFINITY, sum = 0.0f, acc[kV] = {};
   for (int32_t i0 = part; i0 < n; i0 += 8 * N) {
@@ -1259,7 +1349,8 @@ __global__ __launch_bounds__(N == 1 ? 256 : 64 * N) void kv_attend_join(KvBatch 
     float x[8][kV];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t e = base + (int64_t)min(i0 + j * N, n - 1) * R;
+      const int32_t i = min(i0 + j * N, n - 1);
+      const int64_t e = base + (int64_t)(i + (i > 0 ? p.jump : 0)) * R;
       ml[j] = p.part_ml[e];
       const float* src = p.part + e * D + lane * kV;
 #pragma unroll
