@@ -474,6 +474,8 @@ struct KvQuery {
 };
 
 constexpr int kKeyTile = 64;
+// Least factor of a score: a masked one, minus infinity, stays that.
+constexpr float kTiny = 1.17549435e-38f;
 // The work of one workgroup: a tile of query rows of a sequence and a range
 // of its key tiles.
 struct KvWork {
@@ -861,7 +863,7 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
     for (; tile < see.tile1; tile += 4) {
       const int32_t pk_after = page_at(tile + 8, k_run), pv_after = page_at(tile + 8, grp);
       const bool ok = pv >= 0;
-      const float f = ok ? ks * scale : 0.0f, vw = ok ? vs : 0.0f;
+      const float f = ok ? fmaxf(ks * scale, kTiny) : 1.0f, vw = ok ? vs : 0.0f;
       const int32_t t0 = tile * kKeyTile;
       f32x4 s[NT][4];
 #pragma unroll
@@ -910,8 +912,7 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
         float top = s[nt][0][0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[nt][e >> 2][e & 3]);
-        // -inf times a factor of 0 (a run of no page) is no maximum
-        top = top == -INFINITY ? -INFINITY : top * f;
+        top *= f;
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         // sums are rescaled only when a maximum has grown by more than 2^8
@@ -927,10 +928,7 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float x = s[nt][e >> 2][e & 3];
-          float z = __builtin_fmaf(x, f, base);
-          if (edge) z = x == -INFINITY ? -INFINITY : z;
-          const float pe = __builtin_amdgcn_exp2f(z);
+          const float pe = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 2][e & 3], f, base));
           sum += pe;
           w[nt][e >> 3][e & 7] = (__bf16)(pe * vw);
         }
@@ -1093,21 +1091,30 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   float m = -INFINITY, l = 0.0f;
 
   // Pages of a tile's four runs of 16 tokens, the same in every lane; -1 where
-  // none of the tokens is seen or the table's entry is no page.
+  // the table's entry is no page or none of the tokens is seen.  A page of 64
+  // tokens or more holds the whole tile.
   const FP8BQ_CONSTANT int32_t* table =
       (const FP8BQ_CONSTANT int32_t*)(uintptr_t)(bt.table + (int64_t)wk.b * bt.stride);
+  const bool one_page = log_s >= 6;
   struct Pages {
     int32_t of[4];
   };
   auto pages = [&](int32_t tile) {
     Pages x;
+    if (one_page) {
+      int32_t pg = __builtin_amdgcn_readfirstlane(table[(tile * kKeyTile) >> log_s]);
+      pg = pg >= 0 && pg < c.pages ? pg : -1;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int32_t t0 = tile * kKeyTile + 16 * r;
-      int32_t pg = -1;
-      if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> log_s];
-      pg = __builtin_amdgcn_readfirstlane(pg);
-      x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
+      for (int r = 0; r < 4; ++r) x.of[r] = pg;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int32_t t0 = tile * kKeyTile + 16 * r;
+        int32_t pg = -1;
+        if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> log_s];
+        pg = __builtin_amdgcn_readfirstlane(pg);
+        x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
+      }
     }
     return x;
   };
@@ -1115,24 +1122,58 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     const int32_t a = r & 1 ? x.of[1] : x.of[0], b = r & 1 ? x.of[3] : x.of[2];
     return r & 2 ? b : a;
   };
+
+  // Where a thread stages its chunks, and reads its operands: byte `at` of row
+  // `row`, whose 16-byte chunks are exchanged with the row.  What a constant
+  // adds to (32 rows, 8 or 4 chunks) leaves the exchange as it is.
+  auto swizzle = [](int32_t row, int32_t ch, int32_t chunks) {
+    return (row * chunks + (ch ^ (chunks % 8 == 0 ? row & 7 : (row >> 1) & 3))) * 16;
+  };
+  constexpr int kAts = kC % 8 == 0 ? 4 : 2;
+  int32_t k_put[kLoads], v_put[kLoads], k_at[kAts], v_at[2];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int32_t at = tid + i * kN, tok = at / kC;
+    k_put[i] = swizzle((tok & 32) + 8 * ((tok >> 2) & 3) + 4 * ((tok >> 4) & 1) + (tok & 3), at - tok * kC, kC);
+    v_put[i] = 64 * D + swizzle(at >> 2, at & 3, 4);
+  }
+#pragma unroll
+  for (int i = 0; i < kAts; ++i) k_at[i] = swizzle(col, 2 * i + half, kC);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) v_at[u] = 64 * D + swizzle(col, 2 * u + half, 4);
+  const int32_t v_off = ((tid >> 2) << log_s) + 16 * (tid & 3);
+
   u32x4 kr[kLoads], vr[kLoads];
   float ks[2], vs[2], ks_next[2], vs_next[2];
   auto fetch = [&](int32_t tile, const Pages& x) {
     const int32_t in_page = (tile * kKeyTile) & (S - 1);   // 0 unless a page is longer than a tile
+    if (one_page) {
+      const int64_t block = (int64_t)max(x.of[0], 0) * c.heads + h;
+      const uint8_t* kp = c.k + ((block << log_s) + in_page) * D;
+      const uint8_t* vp = c.v + ((block * D) << log_s) + in_page;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int32_t at = tid + i * kN, tok = at / kC, ch = at - tok * kC;
-      const int64_t kb = ((int64_t)max(pick(x, tok >> 4), 0) * c.heads + h) << log_s;
-      kr[i] = *(const u32x4*)(c.k + (kb + ((in_page + tok) & (S - 1))) * D + 16 * ch);
-      const int32_t dim = at >> 2, run = at & 3;
-      const int64_t vb = ((int64_t)max(pick(x, run), 0) * c.heads + h) * D + dim;
-      vr[i] = *(const u32x4*)(c.v + (vb << log_s) + ((in_page + 16 * run) & (S - 1)));
-    }
+      for (int i = 0; i < kLoads; ++i) {
+        kr[i] = *(const u32x4*)(kp + (uint32_t)(16 * tid + 16 * i * kN));
+        vr[i] = *(const u32x4*)(vp + (uint32_t)(v_off + ((i * kN / 4) << log_s)));
+      }
+      ks_next[0] = ks_next[1] = c.ks[block];
+      vs_next[0] = vs_next[1] = c.vs[block];
+    } else {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t at = (int64_t)max(half ? x.of[2 * u + 1] : x.of[2 * u], 0) * c.heads + h;
-      ks_next[u] = c.ks[at];
-      vs_next[u] = c.vs[at];
+      for (int i = 0; i < kLoads; ++i) {
+        const int32_t at = tid + i * kN, tok = at / kC, ch = at - tok * kC;
+        const int64_t kb = ((int64_t)max(pick(x, tok >> 4), 0) * c.heads + h) << log_s;
+        kr[i] = *(const u32x4*)(c.k + (kb + (tok & (S - 1))) * D + 16 * ch);
+        const int32_t dim = at >> 2, run = at & 3;
+        const int64_t vb = ((int64_t)max(pick(x, run), 0) * c.heads + h) * D + dim;
+        vr[i] = *(const u32x4*)(c.v + (vb << log_s) + ((16 * run) & (S - 1)));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t at = (int64_t)max(half ? x.of[2 * u + 1] : x.of[2 * u], 0) * c.heads + h;
+        ks_next[u] = c.ks[at];
+        vs_next[u] = c.vs[at];
+      }
     }
   };
   auto bad = [](const Pages& x) { return (x.of[0] | x.of[1] | x.of[2] | x.of[3]) < 0; };
@@ -1140,38 +1181,31 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     const int32_t t0 = tile * kKeyTile;
     return bad(x) || t0 < see.all_lo || t0 + kKeyTile > see.all_hi;
   };
-  // Row `row` of a staged tile whose rows are `chunks` 16-byte chunks long.
-  auto swizzle = [](int32_t row, int32_t ch, int32_t chunks) {
-    return (row * chunks + (ch ^ (chunks % 8 == 0 ? row & 7 : (row >> 1) & 3))) * 16;
-  };
-  auto put = [&](int32_t buf, int32_t tile, const Pages& x, bool edge) {
-    uint8_t* kl = lds + buf * kBuf;
-    uint8_t* vl = kl + 64 * D;
+  auto put = [&](uint8_t* to, int32_t tile, const Pages& x) {
+    if (is_edge(tile, x)) {
+      // what nobody sees counts as code 0, whatever is there
+      asm volatile("");   // a branch: not computed for the other tiles
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int32_t at = tid + i * kN, tok = at / kC, ch = at - tok * kC;
-      const int32_t lrow = (tok & 32) + 8 * ((tok >> 2) & 3) + 4 * ((tok >> 4) & 1) + (tok & 3);
-      *(u32x4*)(kl + swizzle(lrow, ch, kC)) = kr[i];
-      const int32_t dim = at >> 2, run = at & 3;
-      if (edge) {
-        // what nobody sees counts as code 0, whatever is there
-        const int32_t t0 = tile * kKeyTile + 16 * run;
+      for (int i = 0; i < kLoads; ++i) {
+        const int32_t run = (tid + i * kN) & 3, t0 = tile * kKeyTile + 16 * run;
         vr[i] &= kv_bytes(see.see_lo - t0, pick(x, run) >= 0 ? see.see_hi - t0 : 0);
       }
-      *(u32x4*)(vl + swizzle(dim, run, 4)) = vr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      *(u32x4*)(to + k_put[i]) = kr[i];
+      *(u32x4*)(to + v_put[i]) = vr[i];
     }
   };
 
-  auto compute = [&](int32_t buf, int32_t tile, const Pages& x, bool edge) {
-    const uint8_t* kl = lds + buf * kBuf;
-    const uint8_t* vl = kl + 64 * D;
+  auto compute = [&](const uint8_t* from, int32_t tile, const Pages& x) {
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       s[u] = f32x16{};
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
-        const u32x4 a = *(const u32x4*)(kl + swizzle(32 * u + col, 2 * i + half, kC));
+        const u32x4 a = *(const u32x4*)(from + k_at[i % kAts] + 32 * u * D + i / kAts * 32 * kAts);
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[0], a[1]), q[2 * i], s[u], 0, 0, 0);
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[2], a[3]), q[2 * i + 1], s[u], 0, 0, 0);
       }
@@ -1181,11 +1215,12 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     for (int u = 0; u < 2; ++u) {
       const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
       const float v = ok ? fmaxf(vs[u], 5.421010862427522e-20f) : 1.0f;   // at least 2^-64
-      f[u] = ok ? ks[u] * scale : 0.0f;
+      f[u] = ok ? fmaxf(ks[u] * scale, kTiny) : 1.0f;
       lv[u] = __builtin_amdgcn_logf(v);
-      back[u] = 1.0f / v;
+      back[u] = __builtin_amdgcn_rcpf(v);
     }
-    if (edge) {
+    if (is_edge(tile, x)) {
+      asm volatile("");
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int32_t t0 = tile * kKeyTile + 32 * u + 16 * half;
@@ -1201,8 +1236,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       float t = s[u][0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) t = fmaxf(t, s[u][e]);
-      // -inf times a factor of 0 (a run of no page) is no maximum
-      top = fmaxf(top, t == -INFINITY ? -INFINITY : t * f[u]);
+      top = fmaxf(top, t * f[u]);
     }
     top = fmaxf(top, __shfl_xor(top, 32));
     if (__ballot(top > m + 8.0f) != 0) {
@@ -1221,9 +1255,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        float z = __builtin_fmaf(s[u][e], f[u], off);
-        if (edge) z = s[u][e] == -INFINITY ? -INFINITY : z;
-        const float pe = __builtin_amdgcn_exp2f(z);
+        const float pe = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], f[u], off));
         sum += pe;
         w[u][e >> 3][e & 7] = (__bf16)pe;
       }
@@ -1233,7 +1265,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     for (int i = 0; i < kM; ++i) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const u32x4 a = *(const u32x4*)(vl + swizzle(32 * i + col, 2 * u + half, 4));
+        const u32x4 a = *(const u32x4*)(from + v_at[u] + 32 * i * 64);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[0], a[1]), w[u][0], o[i], 0, 0, 0);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[2], a[3]), w[u][1], o[i], 0, 0, 0);
       }
@@ -1241,11 +1273,13 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   };
 
   if (see.tile0 < see.tile1) {
-    Pages now = pages(see.tile0), next = pages(see.tile0 + 1 < see.tile1 ? see.tile0 + 1 : see.tile0);
-    fetch(see.tile0, now);
-    put(0, see.tile0, now, is_edge(see.tile0, now));
-    for (int32_t tile = see.tile0; tile < see.tile1; ++tile) {
-      const int32_t buf = (tile - see.tile0) & 1;
+    int32_t tile = see.tile0;
+    Pages now = pages(tile), next = pages(min(tile + 1, see.tile1 - 1));
+    fetch(tile, now);
+    put(lds, tile, now);
+    // One tile out of `from`, while the next one is on its way into `to`;
+    // false after the last one.
+    auto step = [&](const uint8_t* from, uint8_t* to) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         ks[u] = ks_next[u];
@@ -1253,12 +1287,16 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       }
       const bool more = tile + 1 < see.tile1;
       if (more) fetch(tile + 1, next);
-      const Pages after = pages(tile + 2 < see.tile1 ? tile + 2 : tile);
+      const Pages after = pages(min(tile + 2, see.tile1 - 1));
       __syncthreads();   // the tile is staged, and the other buffer is read out
-      compute(buf, tile, now, is_edge(tile, now));
-      if (more) put(buf ^ 1, tile + 1, next, is_edge(tile + 1, next));
+      compute(from, tile, now);
+      if (more) put(to, tile + 1, next);
       now = next;
       next = after;
+      ++tile;
+      return more;
+    };
+    while (step(lds, lds + kBuf) && step(lds + kBuf, lds)) {
     }
   }
 
