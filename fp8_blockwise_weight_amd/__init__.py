@@ -163,7 +163,7 @@ def load_library() -> ctypes.CDLL:
     lib.fp8bq_kv_append.restype = ctypes.c_int
     lib.fp8bq_kv_attention.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]
     lib.fp8bq_kv_attention.restype = ctypes.c_int
-    lib.fp8bq_kv_attention_workspace_bytes.argtypes = [c_i32, c_i32, c_i32, c_i32, c_i64]
+    lib.fp8bq_kv_attention_workspace_bytes.argtypes = [c_vp, c_vp, c_i32, c_i64]
     lib.fp8bq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.fp8bq_encode_e4m3.argtypes = [c_vp, c_vp, c_i64, c_vp]
     lib.fp8bq_encode_e4m3.restype = ctypes.c_int

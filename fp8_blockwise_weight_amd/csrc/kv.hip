@@ -85,6 +85,11 @@ void kv_for_dim(int32_t dim, F&& f) {
   }
 }
 
+// Sequences whose table has room for no more key tiles than this are done by
+// one workgroup for each row tile and head: a few more tiles to each wave
+// (about 1.5 us each) cost less than joining parts in a second launch.
+constexpr int64_t kKvWhole = 16;
+
 // How an attention call is cut up: from the shapes alone, so that the
 // workspace can be sized, and a launch captured, before any length is known.
 struct KvShape {
@@ -98,27 +103,29 @@ struct KvShape {
   size_t rows_at, ml_at, bytes;   // workspace: partial sums at 0, then these
 };
 
-KvShape kv_shape(int32_t kv_heads, int32_t dim, int32_t q_heads, int32_t count, int64_t tokens) {
+KvShape kv_shape(const fp8bq_kv_cache& c, const fp8bq_kv_batch& b, int32_t q_heads, int64_t tokens) {
   KvShape s;
-  s.group = q_heads / kv_heads;
-  const int64_t per_seq = ceil_div(tokens * s.group, count);
-  s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 ? 64 : 128));
-  const int resident = s.rows == 16 ? (dim == 64 ? 768 : 512) : (s.rows == 64 ? 1024 : (s.rows == 128 ? 512 : 256));
+  s.group = q_heads / c.kv_heads;
+  const int64_t per_seq = ceil_div(tokens * s.group, b.count);
+  s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 && c.head_dim <= 128 ? 64 : 128));
+  const int64_t base = tokens * s.group / s.rows + b.count;   // row tiles of all sequences, at most
+  const int resident =
+      s.rows == 16 ? (c.head_dim == 64 ? 768 : 512) : (s.rows == 64 ? 1024 : (s.rows == 128 ? 512 : 256));
+  const int64_t tiles = ceil_div(static_cast<int64_t>(b.max_pages) * c.page_size, 64);
   s.min_tiles = 4;
-  if (s.rows <= 32) {
-    s.target = static_cast<int32_t>(ceil_div(resident, kv_heads));
+  s.target = static_cast<int32_t>(ceil_div(resident, c.kv_heads));
+  if (s.rows <= 32 && tiles > kKvWhole) {
     s.grid = s.target;
     s.slots = 2 * s.target;
     s.jump = s.target;
   } else {
-    const int64_t base = tokens * s.group / s.rows + count;
-    s.target = base * kv_heads >= resident ? 0 : static_cast<int32_t>(ceil_div(resident, kv_heads));
+    if (s.rows <= 32 || base * c.kv_heads >= resident) s.target = 0;
     s.grid = static_cast<int32_t>(base + s.target);
     s.slots = s.grid;
     s.jump = 0;
   }
-  const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(kv_heads) * static_cast<size_t>(s.rows);
-  s.ml_at = n * static_cast<size_t>(dim) * 4;
+  const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(c.kv_heads) * static_cast<size_t>(s.rows);
+  s.ml_at = n * static_cast<size_t>(c.head_dim) * 4;
   s.rows_at = s.ml_at + n * 8;
   s.bytes = s.target == 0 ? 0 : s.rows_at + static_cast<size_t>(tokens) * static_cast<size_t>(q_heads) * 8;
   return s;
@@ -197,10 +204,14 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
   return e == hipSuccess ? FP8BQ_OK : hip_failed(e);
 }
 
-size_t fp8bq_kv_attention_workspace_bytes(int32_t kv_heads, int32_t head_dim, int32_t q_heads, int32_t count,
-                                          int64_t tokens) {
-  if (kv_heads < 1 || count < 1 || tokens < 1 || !kv_heads_ok(q_heads, kv_heads, count, tokens)) return 0;
-  return kv_shape(kv_heads, head_dim, q_heads, count, tokens).bytes;
+size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
+                                          int32_t q_heads, int64_t tokens) {
+  if (!cache || !batch || cache->kv_heads < 1 || kv_log2_page(cache->page_size) < 0 || cache->head_dim < 1 ||
+      batch->count < 1 || batch->max_pages < 0 || tokens < 1 ||
+      !kv_heads_ok(q_heads, cache->kv_heads, batch->count, tokens)) {
+    return 0;
+  }
+  return kv_shape(*cache, *batch, q_heads, tokens).bytes;
 }
 
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, const fp8bq_kv_query* q,
@@ -214,7 +225,7 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
       !kv_rows_ok(q->out, q->out_token_stride, q->out_head_stride) || !kv_aligned(q->lse, 4)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
-  const KvShape s = kv_shape(cache->kv_heads, cache->head_dim, q->q_heads, batch->count, q->tokens);
+  const KvShape s = kv_shape(*cache, *batch, q->q_heads, q->tokens);
   if (s.bytes > 0 && (workspace == nullptr || workspace_bytes < s.bytes || !kv_aligned(workspace, 16))) {
     return FP8BQ_ERR_WORKSPACE;
   }

@@ -619,34 +619,40 @@ __device__ __forceinline__ bool kv_plan(const KvBatch& bt, const KvQuery& p, int
 // them can continue in a neighbour's.  Everyone ends at the same time whatever
 // the lengths are, and nothing is started twice.  The partial sums of a row
 // tile that begins in share i are slot i, those of it in a later share j slot
-// target + j.
+// target + j.  With a target of 0 (short tables) every workgroup has one whole
+// row tile.
 template <int R>
 struct KvShares {
   const KvBatch& bt;
   const KvQuery& p;
   int32_t cap, index;
-  int64_t at, end, share;   // this share's tiles, counted over the whole batch
+  int64_t at, end, share;   // this share's tiles (row tiles: target 0), counted over the whole batch
   int32_t b, rtile, t;      // the next one's sequence, row tile and tile
   KvSeq s;
 
-  static __device__ __forceinline__ int64_t weight(const KvSeq& s) {
-    return (int64_t)s.rtiles * max(s.tiles, 1);   // a row that sees nothing is written, too
-  }
+  // Units of a row tile: one that sees nothing is written, too.
+  __device__ __forceinline__ int32_t units(const KvSeq& s) const { return p.target == 0 ? 1 : max(s.tiles, 1); }
+  __device__ __forceinline__ int64_t weight(const KvSeq& s) const { return (int64_t)s.rtiles * units(s); }
 
   __device__ __forceinline__ KvShares(const KvBatch& bt_, const KvQuery& p_, int32_t cap_, int32_t index_)
       : bt(bt_), p(p_), cap(cap_), index(index_), at(0), end(0), share(1), b(0), rtile(0), t(0) {
     const int32_t lane = threadIdx.x & 63;
     KvSeq mine = kv_seq<R>(bt, p, cap, lane);
-    int64_t total = lane_of(wave_scan(weight(mine)), 63);
-    for (int32_t b0 = 64; b0 < bt.count; b0 += 64) {
-      total += lane_of(wave_scan(weight(kv_seq<R>(bt, p, cap, b0 + lane))), 63);
+    if (p.target == 0) {
+      at = index;
+      end = at + 1;
+    } else {
+      int64_t total = lane_of(wave_scan(weight(mine)), 63);
+      for (int32_t b0 = 64; b0 < bt.count; b0 += 64) {
+        total += lane_of(wave_scan(weight(kv_seq<R>(bt, p, cap, b0 + lane))), 63);
+      }
+      share = (int64_t)__builtin_ceil((double)total / (double)p.target);
+      if (share * p.target < total) ++share;
+      share = lane_of(max(share, (int64_t)p.min_tiles), 0);
+      at = index * share;
+      end = min(at + share, total);
+      if (at >= end) return;
     }
-    share = (int64_t)__builtin_ceil((double)total / (double)p.target);
-    if (share * p.target < total) ++share;
-    share = lane_of(max(share, (int64_t)p.min_tiles), 0);
-    at = index * share;
-    end = min(at + share, total);
-    if (at >= end) return;
     int64_t before = 0;
     for (int32_t b0 = 0; b0 < bt.count; b0 += 64) {
       if (b0 > 0) mine = kv_seq<R>(bt, p, cap, b0 + lane);
@@ -657,13 +663,14 @@ struct KvShares {
         s = lane_of(mine, which);
         b = b0 + which;
         const int64_t off = at - (before + lane_of(sum, which) - lane_of(w, which));
-        const int32_t tiles = max(s.tiles, 1);
+        const int32_t tiles = units(s);
         rtile = off < tiles ? 0 : (int32_t)(off / tiles);
         t = (int32_t)(off - (int64_t)rtile * tiles);
         return;
       }
       before += lane_of(sum, 63);
     }
+    end = at;   // beyond the last one
   }
 
   __device__ __forceinline__ bool next(KvWork& k) {
@@ -674,7 +681,7 @@ struct KvShares {
       s = kv_seq<R>(bt, p, cap, b);
       s = lane_of(s, 0);
     }
-    const int32_t tiles = max(s.tiles, 1);
+    const int32_t tiles = units(s);
     const int32_t take = (int32_t)min((int64_t)(tiles - t), end - at);
     k.b = b;
     k.row0 = s.row0;
@@ -683,7 +690,7 @@ struct KvShares {
     k.first = rtile * R;
     k.count = s.n * p.group;
     k.tile0 = s.tile0 + t;
-    k.tile1 = s.tile0 + min(t + take, s.tiles);
+    k.tile1 = s.tile0 + (p.target == 0 ? s.tiles : min(t + take, s.tiles));
     k.begin = t == 0;
     k.parts = 1;
     if (t > 0 || t + take < tiles) {
@@ -1026,7 +1033,7 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
       } else if (p.lse) {
         p.lse[row * all + head] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
       }
-      if (wk.begin) p.rows[row * all + head] = int2{wk.slot * R + rr, wk.parts};
+      if (wk.begin && p.rows) p.rows[row * all + head] = int2{wk.slot * R + rr, wk.parts};
     }
     __syncthreads();   // LDS is free for the next row tile
   }

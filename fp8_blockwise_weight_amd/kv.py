@@ -145,14 +145,20 @@ def _writable(x, stride_t, stride_h, what):
         raise ValueError(f"{what}'s rows must not overlap")
 
 
-def _launch(cache, call):
-    """``call(stream)`` with the cache's device current."""
+def _run(cache, f, *args):
+    """``f(*args, stream)`` on the current stream of the cache's device.
+
+    The stream's handle is taken from torch's own lookup: building a Stream
+    object around it took 2.8 us of a 12.5 us call.
+    """
     import torch
 
-    if torch.cuda.current_device() == cache._index:
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(cache._index):
-        return call(torch.cuda.current_stream().cuda_stream)
+    index = cache._index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        return f(*args, stream)
+    with torch.cuda.device(index):
+        return f(*args, stream)
 
 
 def kv_append(cache, k, v, block_table, seq_lens, query_start=None, *, q=None, q_out=None, cos=None,
@@ -213,15 +219,18 @@ def kv_append(cache, k, v, block_table, seq_lens, query_start=None, *, q=None, q
         return q_out
     packed = _TOKENS.pack(kp, vp, qp, op, cp, sp, kt, kh, vt, vh, qt, qh, ot, oh, tokens, positions,
                           q_heads, rot, int(bool(interleaved)), 0)
-    f = load_library().fp8bq_kv_append
-    _check("fp8bq_kv_append", _launch(cache, lambda stream: f(cache._packed, batch, packed, stream)))
+    status = _run(cache, load_library().fp8bq_kv_append, cache._packed, batch, packed)
+    if status:
+        _check("fp8bq_kv_append", status)
     return q_out
 
 
-def kv_attention_workspace_bytes(cache, q_heads, sequences, tokens):
-    """Bytes of ``kv_attention``'s workspace: by shapes alone."""
-    return int(load_library().fp8bq_kv_attention_workspace_bytes(cache.kv_heads, cache.head_dim, q_heads,
-                                                                  sequences, tokens))
+def kv_attention_workspace_bytes(cache, q, block_table):
+    """Bytes of ``kv_attention``'s workspace for these tensors: by their shapes
+    alone."""
+    n, width = block_table.shape
+    batch = _BATCH.pack(0, 0, 0, width, n, width)
+    return int(load_library().fp8bq_kv_attention_workspace_bytes(cache._packed, batch, q.shape[1], q.shape[0]))
 
 
 def kv_attention(cache, q, block_table, seq_lens, query_start=None, *, scale=None, window=0, out=None,
@@ -271,7 +280,7 @@ def kv_attention(cache, q, block_table, seq_lens, query_start=None, *, scale=Non
         lp = lse.data_ptr()
     if tokens > 0 and n > 0:
         lib = load_library()
-        need = lib.fp8bq_kv_attention_workspace_bytes(heads, dim, q_heads, n, tokens)
+        need = lib.fp8bq_kv_attention_workspace_bytes(cache._packed, batch, q_heads, tokens)
         wp = size = 0
         if workspace is not None:
             if workspace.get_device() != index or not workspace.is_contiguous():
@@ -281,7 +290,7 @@ def kv_attention(cache, q, block_table, seq_lens, query_start=None, *, scale=Non
             workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
             wp, size = workspace.data_ptr(), need
         packed = _QUERY.pack(qp, op, lp, qt, qh, ot, oh, tokens, q_heads, window, scale, 0)
-        f = lib.fp8bq_kv_attention
-        _check("fp8bq_kv_attention",
-               _launch(cache, lambda stream: f(cache._packed, batch, packed, wp, size, stream)))
+        status = _run(cache, lib.fp8bq_kv_attention, cache._packed, batch, packed, wp, size)
+        if status:
+            _check("fp8bq_kv_attention", status)
     return (out, lse) if return_lse else out

@@ -468,10 +468,11 @@ typedef struct fp8bq_kv_query {
   int32_t reserved;   /* ignored */
 } fp8bq_kv_query;
 
-/* Device workspace bytes of fp8bq_kv_attention (0: none).  They depend on the
- * shapes alone, not on any length. */
-size_t fp8bq_kv_attention_workspace_bytes(int32_t kv_heads, int32_t head_dim, int32_t q_heads,
-                                          int32_t count, int64_t tokens);
+/* Device workspace bytes of fp8bq_kv_attention (0: none).  Of the structs only
+ * page_size, kv_heads, head_dim, count and max_pages are read: the size depends
+ * on the shapes alone, not on any length. */
+size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
+                                          int32_t q_heads, int64_t tokens);
 
 /*
  * Attention over the cache: for the query at position p of its sequence,

@@ -24,7 +24,7 @@ def cache(k=K, v=V, ks=KS, vs=VS, pages=100, size=64, heads=8, dim=128):
     return kv._CACHE.pack(k, v, ks, vs, pages, size, heads, dim, 0)
 
 
-def batch(table=TB, lens=LN, starts=ST, stride=16, count=4, width=16):
+def batch(table=TB, lens=LN, starts=ST, stride=40, count=4, width=40):
     return kv._BATCH.pack(table, lens, starts, stride, count, width)
 
 
@@ -41,7 +41,7 @@ BAD_CACHES = [dict(k=0), dict(v=0), dict(ks=0), dict(vs=0), dict(k=K + 8), dict(
               dict(pages=0), dict(pages=1 << 31), dict(size=8), dict(size=48), dict(size=512), dict(heads=0),
               dict(heads=-1), dict(heads=1 << 16), dict(dim=0), dict(dim=96), dict(dim=320), dict(v=K + 16),
               dict(ks=K + 64), dict(vs=KS + 4)]
-BAD_BATCHES = [dict(table=0), dict(lens=0), dict(stride=15), dict(width=-1), dict(count=-1), dict(count=1 << 21),
+BAD_BATCHES = [dict(table=0), dict(lens=0), dict(stride=39), dict(width=-1), dict(count=-1), dict(count=1 << 21),
                dict(table=TB + 2), dict(lens=LN + 1), dict(starts=ST + 2), dict(starts=0)]
 
 
@@ -92,7 +92,7 @@ def test_null_structs_and_workspace():
     assert lib.fp8bq_kv_attention(None, batch(), query(), WS, 1 << 40, None) == INVALID
     assert lib.fp8bq_kv_attention(cache(), None, query(), WS, 1 << 40, None) == INVALID
     assert lib.fp8bq_kv_attention(cache(), batch(), None, WS, 1 << 40, None) == INVALID
-    need = lib.fp8bq_kv_attention_workspace_bytes(8, 128, 32, 4, 9)
+    need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
     assert need > 0
     assert lib.fp8bq_kv_attention(cache(), batch(), query(), None, need, None) == WORKSPACE
     assert lib.fp8bq_kv_attention(cache(), batch(), query(), WS, need - 1, None) == WORKSPACE
@@ -109,10 +109,14 @@ def test_nothing_to_do_touches_no_device():
 
 def test_workspace_depends_on_shapes_alone():
     f = fq.load_library().fp8bq_kv_attention_workspace_bytes
-    for bad in ((0, 128, 32, 1, 1), (8, 128, 12, 1, 1), (8, 128, 32, 0, 1), (8, 128, 32, 1, 0), (8, 128, 32, 1, 1 << 40)):
-        assert f(*bad) == 0
-    assert f(8, 128, 32, 1, 1) < 1 << 28
-    assert f(1, 64, 1, 1, 1) > 0
+    none = dict(table=0, lens=0, starts=0)
+    for c, b, heads, tokens in ((dict(heads=0), {}, 32, 9), (dict(size=24), {}, 32, 9), ({}, dict(count=0), 32, 9),
+                                ({}, {}, 12, 9), ({}, {}, 32, 0), ({}, {}, 32, 1 << 40), ({}, dict(width=-1), 32, 9)):
+        assert f(cache(**c), batch(**none, **b), heads, tokens) == 0
+    assert f(None, batch(), 32, 9) == 0 and f(cache(), None, 32, 9) == 0
+    assert 0 < f(cache(k=0, v=0, ks=0, vs=0), batch(**none, width=10000, stride=10000, count=1), 32, 1) < 1 << 28
+    assert f(cache(), batch(**none, width=16, count=9), 32, 9) == 0          # short tables: no splits
+    assert f(cache(), batch(**none, width=17, stride=17, count=9), 32, 9) > 0
 
 
 def test_struct_sizes():

@@ -201,21 +201,25 @@ def test_append_leaves_out_what_has_no_place(gpu_lib, single):
 # -------------------------------------------------------------- attention
 
 def check_attention(fq, cache, q, table, lens, starts, one, **kw):
+    """Against the definition with a table just as wide as the sequences and
+    with room for long ones (keys then split over workgroups), each twice."""
     out, lse, tol, tol_lse = ref.attention(host(cache), q, table, lens, starts, **kw)
-    dq = q.to(DEV)
-    got, got_lse = fq.kv_attention(cache, dq, i32(table), i32(lens), None if one else i32(starts), return_lse=True, **kw)
-    again = fq.kv_attention(cache, dq, i32(table), i32(lens), None if one else i32(starts), **kw)
-    torch.cuda.synchronize()
-    assert torch.equal(got.view(torch.int16), again.view(torch.int16))
-    got, got_lse = got.cpu().double(), got_lse.cpu().double()
     rows = [r for b in range(len(lens)) for r in range(starts[b], starts[b + 1])]
-    off = (got[rows] - out[rows]).abs()
-    assert not torch.isnan(off).any()
-    assert (off <= tol[rows]).all(), float((off / tol[rows]).max())
     empty = torch.isinf(lse[rows])
-    assert torch.equal(empty, torch.isinf(got_lse[rows])) and (got_lse[rows][empty] < 0).all()
-    off = (got_lse[rows] - lse[rows])[~empty].abs()
-    assert (off <= tol_lse[rows][~empty]).all()
+    dq, st = q.to(DEV), None if one else i32(starts)
+    for room in (0, 20 * 64 // cache.page_size):
+        wide = i32([list(r) + [-1] * room for r in table])
+        got, got_lse = fq.kv_attention(cache, dq, wide, i32(lens), st, return_lse=True, **kw)
+        again = fq.kv_attention(cache, dq, wide, i32(lens), st, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+        got, got_lse = got.cpu().double(), got_lse.cpu().double()
+        off = (got[rows] - out[rows]).abs()
+        assert not torch.isnan(off).any()
+        assert (off <= tol[rows]).all(), (room, float((off / tol[rows]).max()))
+        assert torch.equal(empty, torch.isinf(got_lse[rows])) and (got_lse[rows][empty] < 0).all()
+        off = (got_lse[rows] - lse[rows])[~empty].abs()
+        assert (off <= tol_lse[rows][~empty]).all(), room
     return got
 
 
@@ -457,7 +461,7 @@ def test_captured_step_follows_the_lengths(gpu_lib):
     fq, g = gpu_lib, torch.Generator().manual_seed(15)
     dim, page, heads, group, B, width = 128, 16, 2, 4, 5, 8
     cos, sin = (torch.from_numpy(x).to(DEV) for x in rotation(width * page, 128))
-    table = i32(tables(g, [width] * B, width, B * width))
+    table = i32([r + [-1] * 80 for r in tables(g, [width] * B, width, B * width)])   # room: keys are split
     sets = []
     for i in range(2):
         cache, eager = (fq.KvCache.empty(B * width, heads, dim, page, device=DEV) for _ in range(2))
@@ -466,7 +470,7 @@ def test_captured_step_follows_the_lengths(gpu_lib):
         q, k, v = qkv[:, :heads * group], qkv[:, heads * group:heads * (group + 1)], qkv[:, heads * (group + 1):]
         turned = torch.empty((B, heads * group, dim), dtype=torch.bfloat16, device=DEV)
         out = torch.empty_like(turned)
-        ws = torch.empty(max(16, fq.kv_attention_workspace_bytes(cache, heads * group, B, B)), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(max(16, fq.kv_attention_workspace_bytes(cache, turned, table)), dtype=torch.uint8, device=DEV)
         stream = torch.cuda.Stream()
 
         def step(c, o):
@@ -555,7 +559,7 @@ def test_refusals(gpu_lib):
         with pytest.raises((ValueError, TypeError)):
             call()
     with pytest.raises(fq.Fp8bqError, match="workspace"):
-        at(workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+        at(tb=i32([[0, 1] + [-1] * 80]), workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
     empty = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device=DEV)
     assert at(q=empty, st=i32([0, 0])).shape == (0, 4, 64)
     assert ap(k=empty[:, :2], v=empty[:, :2], st=i32([0, 0])) is None
