@@ -22,7 +22,7 @@ bool kv_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 // Grids and in-kernel row numbers stay in 32 bits.
 constexpr int64_t kKvMaxRows = int64_t{1} << 25;   // query tokens x query heads
 constexpr int32_t kKvMaxBatch = 1 << 20;
-constexpr int64_t kKvMaxBlocks = int64_t{1} << 22;  // sequences x key/value heads
+constexpr int64_t kKvMaxBlocks = int64_t{1} << 21;  // sequences x key/value heads
 
 bool kv_cache_ok(const fp8bq_kv_cache* c) {
   if (c == nullptr || kv_log2_page(c->page_size) < 0) return false;
@@ -132,7 +132,7 @@ KvShape kv_shape(const fp8bq_kv_cache& c, const fp8bq_kv_batch& b, int32_t q_hea
 }
 
 // A grid of `slots` workgroups per head stays below 2^32 work-items for
-// count * kv_heads <= 2^22 (slots <= rows / 16 + count + 1024 / kv_heads + 1).
+// count * kv_heads <= 2^21 (slots <= rows / 16 + count + 1024 / kv_heads + 1).
 bool kv_heads_ok(int32_t q_heads, int32_t kv_heads, int32_t count, int64_t tokens) {
   return q_heads >= 1 && q_heads % kv_heads == 0 && tokens <= kKvMaxRows / q_heads &&
          static_cast<int64_t>(count) * kv_heads <= kKvMaxBlocks;
@@ -195,8 +195,7 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
                          dim3(fp8bq::kThreads), 0, st, c, b, d);
     } else {
       const int64_t slots = (t->tokens >> c.log_s) + 2 * static_cast<int64_t>(batch->count);
-      hipLaunchKernelGGL(fp8bq::kv_append_pages<D>,
-                         dim3(static_cast<unsigned>(slots), static_cast<unsigned>(cache->kv_heads)),
+      hipLaunchKernelGGL(fp8bq::kv_append_pages<D>, dim3(static_cast<unsigned>(slots * cache->kv_heads)),
                          dim3(fp8bq::kThreads), 0, st, c, b, d);
     }
   });

@@ -251,9 +251,42 @@ __device__ __forceinline__ void unit_channels(int32_t u, int32_t half, int32_t i
   b = split ? half + 8 * u : 16 * u + 8;
 }
 
-// Rotates the 16 values of unit u (read as two 16-byte words) in place.
-__device__ __forceinline__ void unit_rotate(u32x4 lo, u32x4 hi, const float* cs, const float* sn, bool turn,
-                                            int32_t interleaved, float* x) {
+// The bytes lo .. hi - 1 of 16, as a mask.
+__device__ __forceinline__ u32x4 kv_bytes(int32_t lo, int32_t hi) {
+  u32x4 keep;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) w |= 4 * e + y >= lo && 4 * e + y < hi ? 0xFFu << (8 * y) : 0u;
+    keep[e] = w;
+  }
+  return keep;
+}
+
+// cos and sin of a unit's 8 pairs.
+struct KvTurn {
+  f32x4 cs[2], sn[2];
+  bool turn;
+};
+
+__device__ __forceinline__ KvTurn kv_turn(const KvTokens& t, int64_t pos, int32_t u) {
+  KvTurn w;
+  w.turn = 8 * u < t.half;
+  if (w.turn) {
+    const f32x4* cp = (const f32x4*)(t.cos + pos * t.half + 8 * u);
+    const f32x4* sp = (const f32x4*)(t.sin + pos * t.half + 8 * u);
+    w.cs[0] = cp[0];
+    w.cs[1] = cp[1];
+    w.sn[0] = sp[0];
+    w.sn[1] = sp[1];
+  }
+  return w;
+}
+
+// The 16 values of a unit (read as two 16-byte words), rotated.
+__device__ __forceinline__ void unit_rotate(u32x4 lo, u32x4 hi, const KvTurn& w, int32_t interleaved, float (&x)[16]) {
+  float y[16];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = bf_lo(lo[i]);
@@ -261,21 +294,30 @@ __device__ __forceinline__ void unit_rotate(u32x4 lo, u32x4 hi, const float* cs,
     x[8 + 2 * i] = bf_lo(hi[i]);
     x[8 + 2 * i + 1] = bf_hi(hi[i]);
   }
-  if (!turn) return;
-  if (interleaved) {
+  if (!w.turn) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = a * cs[i] - b * sn[i];
-      x[2 * i + 1] = b * cs[i] + a * sn[i];
-    }
-  } else {
+  for (int i = 0; i < 8; ++i) {
+    const float cs = w.cs[i >> 2][i & 3], sn = w.sn[i >> 2][i & 3];
+    const float a = interleaved ? x[2 * (i & 3) + 8 * (i >> 2)] : x[i];
+    const float b = interleaved ? x[2 * (i & 3) + 1 + 8 * (i >> 2)] : x[8 + i];
+    y[i] = a * cs - b * sn;
+    y[8 + i] = b * cs + a * sn;
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[i], b = x[8 + i];
-      x[i] = a * cs[i] - b * sn[i];
-      x[8 + i] = b * cs[i] + a * sn[i];
-    }
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = interleaved ? y[i] : y[2 * i];
+    x[2 * i + 1] = interleaved ? y[8 + i] : y[2 * i + 1];
+  }
+}
+
+// 16 tokens of two channels of v as codes: two 16-byte words.
+__device__ __forceinline__ void run_codes(const uint32_t (&pairs)[16], float r, u32x4 (&out)[2]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    out[0][x] = cvt4(clamp448(bf_lo(pairs[4 * x]) * r), clamp448(bf_lo(pairs[4 * x + 1]) * r),
+                     clamp448(bf_lo(pairs[4 * x + 2]) * r), clamp448(bf_lo(pairs[4 * x + 3]) * r));
+    out[1][x] = cvt4(clamp448(bf_hi(pairs[4 * x]) * r), clamp448(bf_hi(pairs[4 * x + 1]) * r),
+                     clamp448(bf_hi(pairs[4 * x + 2]) * r), clamp448(bf_hi(pairs[4 * x + 3]) * r));
   }
 }
 
@@ -284,14 +326,27 @@ __device__ __forceinline__ void unit_rotate(u32x4 lo, u32x4 hi, const float* cs,
 // workgroup touches it, so there are no atomics and the result does not
 // depend on any order.  Slot w of the grid belongs to the sequence with
 // floor(starts[b] / S) + 2 b <= w, which leaves every sequence at least as
-// many slots as its tokens can span pages.
+// many slots as its tokens can span pages.  Heads run fastest over the grid:
+// the workgroups that share the rows of a projection's output run together.
+//
+// Streaming work, bound by HBM: a thread holds its part of a page in registers
+// between the maximum and the codes, so that each input is read once (pages of
+// more than kHoldK * 256 units are read a second time, out of the caches); it
+// takes 16 channels of a token of k, with the rotation's row, which the
+// group's queries share, and 16 tokens of two channels of v, whose codes are
+// two 16-byte stores.  Rows of k and q pass the caches by (91 -> 83 us for
+// 17,633 tokens of 32 + 8 + 8 heads of 128: 4.9 TB/s, as a large copy); codes,
+// whose stores are parts of cache lines, do not (107 us).  A workgroup for k
+// and one for v of their own measured slower (105 us).
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv_append_pages(KvCache c, KvBatch bt, KvTokens t) {
+__global__ __launch_bounds__(kThreads, 3) void kv_append_pages(KvCache c, KvBatch bt, KvTokens t) {
   constexpr int kU = D / 16;
+  constexpr int kHoldK = 2, kHoldV = 1;
+  constexpr int kQ = 2;   // queries loaded at a time
   __shared__ float red[8];
-  const int32_t tid = threadIdx.x, h = blockIdx.y;
+  const int32_t tid = threadIdx.x;
+  const int32_t w = blockIdx.x / c.heads, h = blockIdx.x - w * c.heads;
   const int32_t S = 1 << c.log_s;
-  const int64_t w = blockIdx.x;
   auto first_slot = [&](int32_t b) {
     return (int64_t)(kv_clamp(bt.starts[b], t.tokens) >> c.log_s) + 2 * (int64_t)b;
   };
@@ -312,143 +367,189 @@ __global__ __launch_bounds__(kThreads) void kv_append_pages(KvCache c, KvBatch b
   const int32_t held = (int32_t)(lo - (j << c.log_s));   // earlier tokens in the page
   const int32_t count = (int32_t)(hi - lo);
   const int64_t row = row0 + (lo - start);               // input row of the first token
+  const int64_t block = (int64_t)max(page, 0) * c.heads + h;
+  const float k_was = held && stored ? c.ks[block] : 0.0f, v_was = held && stored ? c.vs[block] : 0.0f;
 
-  auto unit = [&](const uint16_t* base, int64_t pos, int32_t u, float* x) {
-    int32_t ca, cb;
-    unit_channels(u, t.half, t.interleaved, ca, cb);
-    const u32x4 a = *(const u32x4*)(base + ca), z = *(const u32x4*)(base + cb);
-    const bool turn = 8 * u < t.half;
-    float cs[8], sn[8];
-    if (turn) {
-      const f32x4* cp = (const f32x4*)(t.cos + pos * t.half + 8 * u);
-      const f32x4* sp = (const f32x4*)(t.sin + pos * t.half + 8 * u);
-      *(f32x4*)cs = cp[0];
-      *(f32x4*)(cs + 4) = cp[1];
-      *(f32x4*)sn = sp[0];
-      *(f32x4*)(sn + 4) = sp[1];
-    }
-    unit_rotate(a, z, cs, sn, turn, t.interleaved, x);
-  };
-
-  if (stored) {
-    float ka = 0.0f, va = 0.0f;
-    for (int32_t i = tid; i < count * kU; i += kThreads) {
-      const int32_t tok = i / kU, u = i - tok * kU;
-      float x[16];
-      unit(t.k + (row + tok) * t.k_tok + h * t.k_head, lo + tok, u, x);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) ka = fmaxf(ka, fabsf(x[e]));
-      const u32x4* vp = (const u32x4*)(t.v + (row + tok) * t.v_tok + h * t.v_head + 16 * u);
-      const uint32_t m = halves_max(pk_max_u16(fold_abs(vp[0]), fold_abs(vp[1])));
-      va = fmaxf(va, __uint_as_float(m << 16));
-    }
-    ka = wave_max(ka);
-    va = wave_max(va);
-    if ((tid & 63) == 0) {
-      red[tid >> 6] = ka;
-      red[4 + (tid >> 6)] = va;
-    }
-    const int64_t block = (int64_t)page * c.heads + h;
-    const float k_was = held ? c.ks[block] : 0.0f, v_was = held ? c.vs[block] : 0.0f;
-    __syncthreads();
-    ka = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    va = fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7]));
-    const float k_fit = kv_fit_scale(ka), v_fit = kv_fit_scale(va);
-    const float k_s = held ? fmaxf(k_was, k_fit) : k_fit, v_s = held ? fmaxf(v_was, v_fit) : v_fit;
-    const float kr = kv_inverse(k_s), vr = kv_inverse(v_s);
-    if (tid == 0) {
-      c.ks[block] = k_s;
-      c.vs[block] = v_s;
-    }
-    uint8_t* kb = c.k + block * S * D;
-    uint8_t* vb = c.v + block * S * D;
-    if (held > 0 && k_s > k_was) {
-      const float ratio = k_was * kr;
-      for (int32_t i = tid; i < held * kU; i += kThreads) {
-        u32x4* at = (u32x4*)kb + i;
-        u32x4 x = *at;
-        for (int e = 0; e < 4; ++e) x[e] = kv_recode4(x[e], ratio);
-        *at = x;
-      }
-    }
-    for (int32_t i = tid; i < count * kU; i += kThreads) {
-      const int32_t tok = i / kU, u = i - tok * kU;
-      float x[16];
-      unit(t.k + (row + tok) * t.k_tok + h * t.k_head, lo + tok, u, x);
-      int32_t ca, cb;
-      unit_channels(u, t.half, t.interleaved, ca, cb);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = clamp448(x[e] * kr);
-      uint8_t* to = kb + (held + tok) * D;
-      *(u32x2*)(to + ca) = u32x2{cvt4(x[0], x[1], x[2], x[3]), cvt4(x[4], x[5], x[6], x[7])};
-      *(u32x2*)(to + cb) = u32x2{cvt4(x[8], x[9], x[10], x[11]), cvt4(x[12], x[13], x[14], x[15])};
-    }
-    // v: a thread owns 16 tokens of two channels, reads a row of channel
-    // pairs per wave and writes 16 bytes of each channel; runs that only
-    // partly hold new tokens are read, merged and written back.
-    const bool grown = held > 0 && v_s > v_was;
-    const float v_ratio = v_was * vr;
-    const int32_t r0 = grown ? 0 : held >> 4, r1 = (held + count + 15) >> 4;
-    for (int32_t i = tid; i < (r1 - r0) * (D / 2); i += kThreads) {
-      const int32_t r = r0 + i / (D / 2), p = i % (D / 2);
-      const int32_t a = 16 * r - held;                    // new token of the run's first byte
-      u32x4* at[2] = {(u32x4*)(vb + (2 * p) * S) + r, (u32x4*)(vb + (2 * p + 1) * S) + r};
-      const uint16_t* src = t.v + row * t.v_tok + h * t.v_head + 2 * p;
-      const bool whole = a >= 0 && a + 16 <= count;
-      u32x4 out[2];
-      uint32_t pairs[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        pairs[e] = 0;
-        if (a + e >= 0 && a + e < count) pairs[e] = *(const uint32_t*)(src + (int64_t)(a + e) * t.v_tok);
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        out[0][x] = cvt4(clamp448(bf_lo(pairs[4 * x]) * vr), clamp448(bf_lo(pairs[4 * x + 1]) * vr),
-                         clamp448(bf_lo(pairs[4 * x + 2]) * vr), clamp448(bf_lo(pairs[4 * x + 3]) * vr));
-        out[1][x] = cvt4(clamp448(bf_hi(pairs[4 * x]) * vr), clamp448(bf_hi(pairs[4 * x + 1]) * vr),
-                         clamp448(bf_hi(pairs[4 * x + 2]) * vr), clamp448(bf_hi(pairs[4 * x + 3]) * vr));
-      }
-      if (!whole) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const u32x4 was = *at[y];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t again = grown ? kv_recode4(was[x], v_ratio) : was[x];
-            uint32_t m_new = 0, m_old = 0;   // bytes of new tokens, of earlier ones
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int32_t tok = a + 4 * x + e;
-              if (tok < 0) m_old |= 0xFFu << (8 * e);
-              else if (tok < count) m_new |= 0xFFu << (8 * e);
-            }
-            out[y][x] = (out[y][x] & m_new) | (again & m_old) | (was[x] & ~(m_new | m_old));
-          }
-        }
-      }
-      *at[0] = out[0];
-      *at[1] = out[1];
-    }
-  }
-  if (t.q == nullptr) return;
-  for (int32_t i = tid; i < count * kU; i += kThreads) {
+  // Unit i of the page's new tokens: of k, and of the queries of the group,
+  // which are done with it.
+  auto rotate_k = [&](int32_t i, float (&x)[16], bool queries) {
     const int32_t tok = i / kU, u = i - tok * kU;
     int32_t ca, cb;
     unit_channels(u, t.half, t.interleaved, ca, cb);
-    for (int32_t g = 0; g < t.group; ++g) {
-      const int64_t head = (int64_t)h * t.group + g;
-      float x[16];
-      unit(t.q + (row + tok) * t.q_tok + head * t.q_head, lo + tok, u, x);
-      uint16_t* to = t.q_out + (row + tok) * t.o_tok + head * t.o_head;
-      bf16x8 y, z;
+    const KvTurn turn = kv_turn(t, lo + tok, u);
+    const uint16_t* kp = t.k + (row + tok) * t.k_tok + h * t.k_head;
+    const u32x4 ka = __builtin_nontemporal_load((const u32x4*)(kp + ca)), kz = __builtin_nontemporal_load((const u32x4*)(kp + cb));
+    if (queries) {
+      const uint16_t* qp = t.q + (row + tok) * t.q_tok + (int64_t)h * t.group * t.q_head;
+      uint16_t* to = t.q_out + (row + tok) * t.o_tok + (int64_t)h * t.group * t.o_head;
+      for (int32_t g0 = 0; g0 < t.group; g0 += kQ) {
+        u32x4 qa[kQ], qz[kQ];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = (__bf16)x[e];
-        z[e] = (__bf16)x[8 + e];
+        for (int g = 0; g < kQ; ++g) {
+          const int64_t at = min(g0 + g, t.group - 1) * t.q_head;
+          qa[g] = __builtin_nontemporal_load((const u32x4*)(qp + at + ca));
+          qz[g] = __builtin_nontemporal_load((const u32x4*)(qp + at + cb));
+        }
+#pragma unroll
+        for (int g = 0; g < kQ; ++g) {
+          if (g0 + g >= t.group) continue;
+          float y[16];
+          unit_rotate(qa[g], qz[g], turn, t.interleaved, y);
+          bf16x8 ya, yz;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ya[e] = (__bf16)y[e];
+            yz[e] = (__bf16)y[8 + e];
+          }
+          __builtin_nontemporal_store(__builtin_bit_cast(u32x4, ya), (u32x4*)(to + (g0 + g) * t.o_head + ca));
+          __builtin_nontemporal_store(__builtin_bit_cast(u32x4, yz), (u32x4*)(to + (g0 + g) * t.o_head + cb));
+        }
       }
-      *(bf16x8*)(to + ca) = y;
-      *(bf16x8*)(to + cb) = z;
+    }
+    unit_rotate(ka, kz, turn, t.interleaved, x);
+  };
+  // 16 tokens of the channels 2 p, 2 p + 1 of v, zeros for those that are not new.
+  const int32_t r0 = held >> 4, runs = ((held + count + 15) >> 4) - r0;
+  auto pairs_v = [&](int32_t i, uint32_t (&pairs)[16]) {
+    const int32_t a = 16 * (r0 + i / (D / 2)) - held, p = i % (D / 2);
+    const uint16_t* src = t.v + row * t.v_tok + h * t.v_head + 2 * p;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      pairs[e] = a + e >= 0 && a + e < count ? *(const uint32_t*)(src + (int64_t)(a + e) * t.v_tok) : 0u;
+    }
+  };
+
+  float kx[kHoldK][16];
+  uint32_t vx[kHoldV][16];
+  float ka = 0.0f;
+  uint32_t va = 0;
+  const bool queries = t.q != nullptr;
+#pragma unroll
+  for (int y = 0; y < kHoldK; ++y) {
+    const int32_t i = tid + y * kThreads;
+    if (i < count * kU) {
+      rotate_k(i, kx[y], queries);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ka = fmaxf(ka, fabsf(kx[y][e]));
+    }
+  }
+  for (int32_t i = tid + kHoldK * kThreads; i < count * kU; i += kThreads) {
+    float x[16];
+    rotate_k(i, x, queries);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ka = fmaxf(ka, fabsf(x[e]));
+  }
+#pragma unroll
+  for (int y = 0; y < kHoldV; ++y) {
+    const int32_t i = tid + y * kThreads;
+    if (stored && i < runs * (D / 2)) {
+      pairs_v(i, vx[y]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) vx[y][e] = 0;
+    }
+  }
+  if (!stored) return;
+#pragma unroll
+  for (int y = 0; y < kHoldV; ++y) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) va = pk_max_u16(va, vx[y][e] & 0x7FFF7FFFu);
+  }
+  for (int32_t i = tid + kHoldV * kThreads; i < runs * (D / 2); i += kThreads) {
+    uint32_t x[16];
+    pairs_v(i, x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) va = pk_max_u16(va, x[e] & 0x7FFF7FFFu);
+  }
+  ka = wave_max(ka);
+  const float vm = wave_max(__uint_as_float(halves_max(va) << 16));
+  if ((tid & 63) == 0) {
+    red[tid >> 6] = ka;
+    red[4 + (tid >> 6)] = vm;
+  }
+  __syncthreads();
+  const float k_fit = kv_fit_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+  const float v_fit = kv_fit_scale(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
+  const float k_s = held ? fmaxf(k_was, k_fit) : k_fit, v_s = held ? fmaxf(v_was, v_fit) : v_fit;
+  const float kr = kv_inverse(k_s), vr = kv_inverse(v_s);
+  if (tid == 0) {
+    c.ks[block] = k_s;
+    c.vs[block] = v_s;
+  }
+  uint8_t* kb = c.k + block * S * D;
+  uint8_t* vb = c.v + block * S * D;
+
+  auto store_k = [&](int32_t i, const float (&x)[16]) {
+    const int32_t tok = i / kU, u = i - tok * kU;
+    int32_t ca, cb;
+    unit_channels(u, t.half, t.interleaved, ca, cb);
+    float y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = clamp448(x[e] * kr);
+    uint8_t* to = kb + (held + tok) * D;
+    *(u32x2*)(to + ca) = u32x2{cvt4(y[0], y[1], y[2], y[3]), cvt4(y[4], y[5], y[6], y[7])};
+    *(u32x2*)(to + cb) = u32x2{cvt4(y[8], y[9], y[10], y[11]), cvt4(y[12], y[13], y[14], y[15])};
+  };
+  const bool v_grown = held > 0 && v_s > v_was;
+  const float v_ratio = v_was * vr;
+  // Runs that hold only some new tokens are read, merged and written back.
+  auto store_v = [&](int32_t i, const uint32_t (&pairs)[16]) {
+    const int32_t r = r0 + i / (D / 2), p = i % (D / 2), a = 16 * r - held;
+    u32x4 out[2];
+    run_codes(pairs, vr, out);
+    u32x4* at[2] = {(u32x4*)(vb + (2 * p) * S) + r, (u32x4*)(vb + (2 * p + 1) * S) + r};
+    if (a < 0 || a + 16 > count) {
+      const u32x4 is_new = kv_bytes(-a, count - a), before = kv_bytes(0, -a);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const u32x4 was = *at[y];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t again = v_grown ? kv_recode4(was[x], v_ratio) : was[x];
+          out[y][x] = (out[y][x] & is_new[x]) | (again & before[x]) | (was[x] & ~(is_new[x] | before[x]));
+        }
+      }
+    }
+    *at[0] = out[0];
+    *at[1] = out[1];
+  };
+#pragma unroll
+  for (int y = 0; y < kHoldK; ++y) {
+    const int32_t i = tid + y * kThreads;
+    if (i < count * kU) store_k(i, kx[y]);
+  }
+#pragma unroll
+  for (int y = 0; y < kHoldV; ++y) {
+    const int32_t i = tid + y * kThreads;
+    if (i < runs * (D / 2)) store_v(i, vx[y]);
+  }
+  for (int32_t i = tid + kHoldK * kThreads; i < count * kU; i += kThreads) {
+    float x[16];
+    rotate_k(i, x, false);
+    store_k(i, x);
+  }
+  for (int32_t i = tid + kHoldV * kThreads; i < runs * (D / 2); i += kThreads) {
+    uint32_t x[16];
+    pairs_v(i, x);
+    store_v(i, x);
+  }
+  // Growth takes the earlier tokens along; those in the first new run of v
+  // have gone with it.
+  if (held > 0 && k_s > k_was) {
+    const float ratio = k_was * kr;
+    for (int32_t i = tid; i < held * kU; i += kThreads) {
+      u32x4* at = (u32x4*)kb + i;
+      u32x4 x = *at;
+      for (int e = 0; e < 4; ++e) x[e] = kv_recode4(x[e], ratio);
+      *at = x;
+    }
+  }
+  if (v_grown) {
+    for (int32_t i = tid; i < r0 * D; i += kThreads) {
+      u32x4* at = (u32x4*)(vb + (i % D) * S) + i / D;
+      u32x4 x = *at;
+      for (int e = 0; e < 4; ++e) x[e] = kv_recode4(x[e], v_ratio);
+      *at = x;
     }
   }
 }
@@ -722,19 +823,6 @@ __device__ __forceinline__ KvSeen kv_seen(const KvWork& k, const KvQuery& p, int
   s.tile0 = max(k.tile0, s.see_lo / kKeyTile);
   s.tile1 = min(k.tile1, (max(s.see_hi, 0) + kKeyTile - 1) / kKeyTile);
   return s;
-}
-
-// The bytes lo .. hi - 1 of 16, as a mask.
-__device__ __forceinline__ u32x4 kv_bytes(int32_t lo, int32_t hi) {
-  u32x4 keep;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) w |= 4 * e + y >= lo && 4 * e + y < hi ? 0xFFu << (8 * y) : 0u;
-    keep[e] = w;
-  }
-  return keep;
 }
 
 // Eight codes (two dwords) as BF16, exactly.

@@ -405,7 +405,7 @@ typedef struct fp8bq_kv_batch {
   const int32_t* seq_lens;     /* [count] */
   const int32_t* query_start;  /* [count + 1], or NULL */
   int64_t table_stride;        /* elements, >= max_pages */
-  int32_t count;               /* sequences, 0 .. 2^20; count * kv_heads <= 2^22 */
+  int32_t count;               /* sequences, 0 .. 2^20; count * kv_heads <= 2^21 */
   int32_t max_pages;           /* columns of the table */
 } fp8bq_kv_batch;
 
