@@ -260,7 +260,9 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
     switch (s.rows) {
       case 16: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 1>), grid, dim3(256), 0, st, c, b, d); break;
       case 32: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 2>), grid, dim3(256), 0, st, c, b, d); break;
-      case 64: hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 2>), grid, dim3(128), 0, st, c, b, d); break;
+      case 64:
+        if constexpr (D <= 128) hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 2>), grid, dim3(128), 0, st, c, b, d);
+        break;
       default: hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 4>), grid, dim3(256), 0, st, c, b, d); break;
     }
     if (split) {

@@ -1135,8 +1135,9 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
 // 32-key product is token 16 ((m / 4) % 2) + 4 (m / 8) + m % 4, which leaves
 // lane half x with the 16 consecutive tokens 16 x .. 16 x + 15 of its query
 // row, the order in which V^T P^T takes them.  16-byte LDS chunks are
-// exchanged (XOR with the row) so that 8 neighbouring lanes, which read 8
-// rows at one column, fall on different banks.
+// exchanged (XOR with the row) so that neighbouring lanes, which read rows at
+// one column, fall on different banks: with row / 2 for rows of 128 bytes and
+// row / 4 for rows of 64, conflicts went from 37% of LDS's cycles to none.
 //
 // VALU work per score bounds this kernel (the exponential at a quarter rate,
 // and the widening of codes), so what can be is kept out of the inner loop:
@@ -1144,6 +1145,12 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
 // fused multiply-add in front of the exponential; v's scale enters there too,
 // as its logarithm; sums and maxima are only rescaled when a row's maximum
 // has grown by more than 2^8.
+// The larger of a lane's value and that of its counterpart in the other half.
+__device__ __forceinline__ float half_max(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCache c, KvBatch bt, KvQuery p) {
   constexpr int R = 32 * W, kN = 64 * W;
@@ -1151,7 +1158,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   constexpr int kM = D / 32;            // 32-channel tiles of the output
   constexpr int kLoads = 4 * D / kN;    // chunks that a thread stages of k, and of v
   constexpr int kBuf = 128 * D;         // bytes of a staged tile: k, then v
-  __shared__ __align__(16) uint8_t lds[2 * kBuf];
+  constexpr int kBufs = D <= 128 && W == 4 ? 3 : 2;
+  __shared__ __align__(16) uint8_t lds[kBufs * kBuf];
   const int32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t col = lane & 31, half = lane >> 5;
   const int32_t w_item = blockIdx.x / c.heads, h = blockIdx.x - w_item * c.heads;
@@ -1222,16 +1230,10 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   // `row`, whose 16-byte chunks are exchanged with the row.  What a constant
   // adds to (32 rows, 8 or 4 chunks) leaves the exchange as it is.
   auto swizzle = [](int32_t row, int32_t ch, int32_t chunks) {
-    return (row * chunks + (ch ^ (chunks % 8 == 0 ? row & 7 : (row >> 1) & 3))) * 16;
+    return (row * chunks + (ch ^ (chunks % 8 == 0 ? (row >> 1) & 7 : (row >> 2) & 3))) * 16;
   };
   constexpr int kAts = kC % 8 == 0 ? 4 : 2;
-  int32_t k_put[kLoads], v_put[kLoads], k_at[kAts], v_at[2];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int32_t at = tid + i * kN, tok = at / kC;
-    k_put[i] = swizzle((tok & 32) + 8 * ((tok >> 2) & 3) + 4 * ((tok >> 4) & 1) + (tok & 3), at - tok * kC, kC);
-    v_put[i] = 64 * D + swizzle(at >> 2, at & 3, 4);
-  }
+  int32_t k_at[kAts], v_at[2];
 #pragma unroll
   for (int i = 0; i < kAts; ++i) k_at[i] = swizzle(col, 2 * i + half, kC);
 #pragma unroll
@@ -1239,8 +1241,10 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   const int32_t v_off = ((tid >> 2) << log_s) + 16 * (tid & 3);
 
   u32x4 kr[kLoads], vr[kLoads];
-  float ks[2], vs[2], ks_next[2], vs_next[2];
-  auto fetch = [&](int32_t tile, const Pages& x) {
+  struct Scales {
+    float k[2], v[2];
+  };
+  auto fetch = [&](int32_t tile, const Pages& x, Scales& sc) {
     const int32_t in_page = (tile * kKeyTile) & (S - 1);   // 0 unless a page is longer than a tile
     if (one_page) {
       const int64_t block = (int64_t)max(x.of[0], 0) * c.heads + h;
@@ -1251,8 +1255,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
         kr[i] = *(const u32x4*)(kp + (uint32_t)(16 * tid + 16 * i * kN));
         vr[i] = *(const u32x4*)(vp + (uint32_t)(v_off + ((i * kN / 4) << log_s)));
       }
-      ks_next[0] = ks_next[1] = c.ks[block];
-      vs_next[0] = vs_next[1] = c.vs[block];
+      sc.k[0] = sc.k[1] = c.ks[block];
+      sc.v[0] = sc.v[1] = c.vs[block];
     } else {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -1266,8 +1270,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t at = (int64_t)max(half ? x.of[2 * u + 1] : x.of[2 * u], 0) * c.heads + h;
-        ks_next[u] = c.ks[at];
-        vs_next[u] = c.vs[at];
+        sc.k[u] = c.ks[at];
+        sc.v[u] = c.vs[at];
       }
     }
   };
@@ -1286,15 +1290,20 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
         vr[i] &= kv_bytes(see.see_lo - t0, pick(x, run) >= 0 ? see.see_hi - t0 : 0);
       }
     }
+    int32_t first = tid;
+    if constexpr (kLoads > 2) asm volatile("" : "+v"(first));   // computed here, not kept in registers
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      *(u32x4*)(to + k_put[i]) = kr[i];
-      *(u32x4*)(to + v_put[i]) = vr[i];
+      const int32_t at = first + i * kN, tok = at / kC;
+      const int32_t lrow = (tok & 32) + 8 * ((tok >> 2) & 3) + 4 * ((tok >> 4) & 1) + (tok & 3);
+      *(u32x4*)(to + swizzle(lrow, at - tok * kC, kC)) = kr[i];
+      *(u32x4*)(to + 64 * D + swizzle(at >> 2, at & 3, 4)) = vr[i];
     }
   };
 
-  auto compute = [&](const uint8_t* from, int32_t tile, const Pages& x) {
+  auto compute = [&](const uint8_t* from, int32_t tile, const Pages& x, const Scales& sc, auto&& between) {
     f32x16 s[2];
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       s[u] = f32x16{};
@@ -1305,12 +1314,14 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[2], a[3]), q[2 * i + 1], s[u], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
+    between();
     float f[2], lv[2], back[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
-      const float v = ok ? fmaxf(vs[u], 5.421010862427522e-20f) : 1.0f;   // at least 2^-64
-      f[u] = ok ? fmaxf(ks[u] * scale, kTiny) : 1.0f;
+      const float v = ok ? fmaxf(sc.v[u], 5.421010862427522e-20f) : 1.0f;   // at least 2^-64
+      f[u] = ok ? fmaxf(sc.k[u] * scale, kTiny) : 1.0f;
       lv[u] = __builtin_amdgcn_logf(v);
       back[u] = __builtin_amdgcn_rcpf(v);
     }
@@ -1333,7 +1344,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       for (int e = 1; e < 16; ++e) t = fmaxf(t, s[u][e]);
       top = fmaxf(top, t * f[u]);
     }
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = half_max(top);
     if (__ballot(top > m + 8.0f) != 0) {
       const float now = fmaxf(m, top);
       const float g = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
@@ -1356,6 +1367,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       }
       l = __builtin_fmaf(sum, back[u], l);
     }
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < kM; ++i) {
 #pragma unroll
@@ -1365,33 +1377,50 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv_widen(a[2], a[3]), w[u][1], o[i], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   if (see.tile0 < see.tile1) {
+    // Tiles go round through the buffers; all but one of those hold tiles that
+    // are staged or computed, the last is being filled.
+    constexpr int kAhead = kBufs - 1;
+    const int32_t last = see.tile1 - 1;
     int32_t tile = see.tile0;
-    Pages now = pages(tile), next = pages(min(tile + 1, see.tile1 - 1));
-    fetch(tile, now);
-    put(lds, tile, now);
-    // One tile out of `from`, while the next one is on its way into `to`;
-    // false after the last one.
-    auto step = [&](const uint8_t* from, uint8_t* to) {
+    Pages pg[kBufs];
+    Scales sc[kBufs];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        ks[u] = ks_next[u];
-        vs[u] = vs_next[u];
+    for (int i = 0; i < kBufs; ++i) pg[i] = pages(min(tile + i, last));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (tile + i <= last) {
+        fetch(tile + i, pg[i], sc[i]);
+        put(lds + i * kBuf, tile + i, pg[i]);
       }
-      const bool more = tile + 1 < see.tile1;
-      if (more) fetch(tile + 1, next);
-      const Pages after = pages(min(tile + 2, see.tile1 - 1));
-      __syncthreads();   // the tile is staged, and the other buffer is read out
-      compute(from, tile, now);
-      if (more) put(to, tile + 1, next);
-      now = next;
-      next = after;
-      ++tile;
-      return more;
+    }
+    if constexpr (kBufs == 3) __syncthreads();
+    auto step = [&](auto which) {
+      constexpr int kNow = decltype(which)::value, kNext = (kNow + kAhead) % kBufs;
+      const bool more = tile + kAhead <= last;
+      if (more) fetch(tile + kAhead, pg[kNext], sc[kNext]);
+      // Whoever passes a tile's barrier has done with the buffer that is
+      // filled next.  With three buffers what is read was written before the
+      // barrier of a tile ago, and the barrier can stand between the products,
+      // where nobody waits for it long (prompts 317 -> 310 us).
+      if constexpr (kBufs == 2) __syncthreads();
+      compute(lds + kNow * kBuf, tile, pg[kNow], sc[kNow], [&] {
+        if constexpr (kBufs == 3) __syncthreads();
+      });
+      if (more) put(lds + kNext * kBuf, tile + kAhead, pg[kNext]);
+      pg[kNow] = pages(min(tile + kBufs, last));
+      return ++tile <= last;
     };
-    while (step(lds, lds + kBuf) && step(lds + kBuf, lds)) {
+    using std::integral_constant;
+    if constexpr (kBufs == 3) {
+      while (step(integral_constant<int, 0>{}) && step(integral_constant<int, 1>{}) && step(integral_constant<int, 2>{})) {
+      }
+    } else {
+      while (step(integral_constant<int, 0>{}) && step(integral_constant<int, 1>{})) {
+      }
     }
   }
 
