@@ -22,6 +22,7 @@ bool kv_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 // Grids and in-kernel row numbers stay in 32 bits.
 constexpr int64_t kKvMaxRows = int64_t{1} << 25;   // query tokens x query heads
 constexpr int32_t kKvMaxBatch = 1 << 20;
+constexpr int64_t kKvMaxStride = int64_t{1} << 36;   // elements; extents stay in 64 bits
 constexpr int64_t kKvMaxBlocks = int64_t{1} << 21;  // sequences x key/value heads
 
 bool kv_cache_ok(const fp8bq_kv_cache* c) {
@@ -55,7 +56,21 @@ bool kv_batch_ok(const fp8bq_kv_batch* b, int64_t tokens) {
 
 // Rows of 16-byte words: base and strides.
 bool kv_rows_ok(const void* p, int64_t tok, int64_t head) {
-  return p != nullptr && kv_aligned(p, 16) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0;
+  return p != nullptr && kv_aligned(p, 16) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0 &&
+         tok < kKvMaxStride && head < kKvMaxStride;
+}
+
+// Bytes from the first to the last of such rows.
+uint64_t kv_extent(int64_t tokens, int64_t tok, int64_t heads, int64_t head, int32_t dim) {
+  return 2 * static_cast<uint64_t>((tokens - 1) * tok + (heads - 1) * head + dim);
+}
+
+// Whether a buffer that is written lies apart from all of the cache.
+bool kv_apart(const fp8bq_kv_cache& c, const void* p, uint64_t bytes) {
+  const uint64_t blocks = static_cast<uint64_t>(c.num_pages) * static_cast<uint64_t>(c.kv_heads);
+  const uint64_t codes = blocks * static_cast<uint64_t>(c.page_size) * static_cast<uint64_t>(c.head_dim);
+  return !overlap(p, bytes, c.k, codes) && !overlap(p, bytes, c.v, codes) &&
+         !overlap(p, bytes, c.k_scale, 4 * blocks) && !overlap(p, bytes, c.v_scale, 4 * blocks);
 }
 
 fp8bq::KvCache kv_device(const fp8bq_kv_cache& c) {
@@ -158,6 +173,13 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
                !kv_rows_ok(t->q_out, t->q_out_token_stride, t->q_out_head_stride))) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
+  const int32_t dim = cache->head_dim;
+  if (!kv_apart(*cache, t->k, kv_extent(t->tokens, t->k_token_stride, cache->kv_heads, t->k_head_stride, dim)) ||
+      !kv_apart(*cache, t->v, kv_extent(t->tokens, t->v_token_stride, cache->kv_heads, t->v_head_stride, dim)) ||
+      (t->q && !kv_apart(*cache, t->q_out,
+                         kv_extent(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, dim)))) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
   if (t->rot_dim > 0 && (!t->cos || !t->sin || !kv_aligned(t->cos, 16) || !kv_aligned(t->sin, 16) ||
                          t->positions < 0)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
@@ -216,9 +238,11 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, const fp8bq_kv_query* q,
                        void* workspace, size_t workspace_bytes, void* stream) {
   if (!kv_cache_ok(cache) || q == nullptr || !kv_batch_ok(batch, q->tokens)) return FP8BQ_ERR_INVALID_ARGUMENT;
-  if (!kv_heads_ok(q->q_heads, cache->kv_heads, batch->count, q->tokens) || q->window < 0 || !(q->scale - q->scale == 0.0f)) {
+  if (!kv_heads_ok(q->q_heads, cache->kv_heads, batch->count, q->tokens) || q->window < 0) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
+  const float scale = q->scale * 1.4426950408889634f;   // for exp2
+  if (!(scale - scale == 0.0f)) return FP8BQ_ERR_INVALID_ARGUMENT;
   if (batch->count == 0 || q->tokens == 0) return FP8BQ_OK;
   if (!kv_rows_ok(q->q, q->q_token_stride, q->q_head_stride) ||
       !kv_rows_ok(q->out, q->out_token_stride, q->out_head_stride) || !kv_aligned(q->lse, 4)) {
@@ -227,6 +251,14 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   const KvShape s = kv_shape(*cache, *batch, q->q_heads, q->tokens);
   if (s.bytes > 0 && (workspace == nullptr || workspace_bytes < s.bytes || !kv_aligned(workspace, 16))) {
     return FP8BQ_ERR_WORKSPACE;
+  }
+  const uint64_t out_bytes =
+      kv_extent(q->tokens, q->out_token_stride, q->q_heads, q->out_head_stride, cache->head_dim);
+  const uint64_t lse_bytes = q->lse ? 4 * static_cast<uint64_t>(q->tokens) * static_cast<uint64_t>(q->q_heads) : 0;
+  if (!kv_apart(*cache, q->out, out_bytes) || !kv_apart(*cache, q->lse, lse_bytes) ||
+      !kv_apart(*cache, workspace, s.bytes) || overlap(q->out, out_bytes, q->lse, lse_bytes) ||
+      overlap(q->out, out_bytes, workspace, s.bytes) || overlap(q->lse, lse_bytes, workspace, s.bytes)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   const int rc = device_check();
   if (rc != FP8BQ_OK) return rc;
@@ -252,7 +284,7 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   d.target = s.target;
   d.jump = s.jump;
   d.min_tiles = s.min_tiles;
-  d.scale = q->scale * 1.4426950408889634f;
+  d.scale = scale;
   hipStream_t st = static_cast<hipStream_t>(stream);
   kv_for_dim(cache->head_dim, [&](auto dim) {
     constexpr int D = decltype(dim)::value;

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_step(KvCache c, KvBatch bt
   const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (item >= (int64_t)bt.count * c.heads) return;
   const int32_t b = (int32_t)(item / c.heads), h = (int32_t)(item - (int64_t)b * c.heads);
-  const int32_t pos = bt.lens[b] - 1;
+  const int32_t pos = max(bt.lens[b], 0) - 1;
   if (pos < 0 || (t.half > 0 && pos >= t.positions)) return;
   const int32_t S = 1 << c.log_s, slot = pos & (S - 1), j = pos >> c.log_s;
   const int32_t page = j < bt.max_pages ? bt.table[(int64_t)b * bt.stride + j] : -1;

@@ -260,7 +260,7 @@ def kv_attention(cache, q, block_table, seq_lens, query_start=None, *, scale=Non
     if tokens * q_heads > MAX_ROWS:
         raise ValueError(f"at most {MAX_ROWS} rows (tokens x heads) per call")
     scale = dim ** -0.5 if scale is None else float(scale)
-    if scale - scale != 0.0 or abs(scale) > 3e38:
+    if scale - scale != 0.0 or abs(scale) > 2e38:
         raise ValueError(f"scale must be a finite float32, got {scale}")
     if not 0 <= window <= 0x7FFFFFFF:
         raise ValueError(f"window must be 0 (none) or a positive number of tokens, got {window}")

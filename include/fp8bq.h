@@ -445,7 +445,8 @@ typedef struct fp8bq_kv_tokens {
  * A power of two, unlike the amax / 448 of weights, lets a page's scale grow
  * without rounding the earlier codes again (other than below e4m3's smallest
  * normal value).  Slots behind the new tokens keep their bytes.  Values must
- * be finite: a block with others gets unspecified codes.  A page may belong to
+ * be finite: a block with others gets unspecified codes.  The inputs and q_out
+ * lie apart from the cache (checked), q_out apart from k and v (not checked).  A page may belong to
  * several sequences as long as no more than one of them stores into it in a
  * call.  fp8bq_dequantize decodes a page's block.
  * No workspace; one launch; may be captured in a graph.
@@ -464,7 +465,7 @@ typedef struct fp8bq_kv_query {
   int64_t tokens;     /* tokens * q_heads <= 2^25 */
   int32_t q_heads;    /* a multiple of kv_heads; query head i reads key head i / (q_heads / kv_heads) */
   int32_t window;     /* a query sees its own position and the window - 1 before it; 0: all */
-  float scale;        /* of the scores, finite */
+  float scale;        /* of the scores; finite, and its product with log2(e) too */
   int32_t reserved;   /* ignored */
 } fp8bq_kv_query;
 
@@ -490,7 +491,10 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  *                    may overlap (other streams, graphs) need one each
  * The launch depends on the shapes alone: captured in a graph, it follows
  * block_table, seq_lens and query_start as they change between replays.
- * Results do not depend on timing.  Returns an fp8bq_status.
+ * out, lse and the workspace lie apart from each other and from the cache
+ * (checked).  v_scale below 2^-64 counts as 2^-64 where a sequence has more
+ * than 32 query rows per key/value head on average.  Results do not depend on
+ * timing.  Returns an fp8bq_status.
  */
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
                        const fp8bq_kv_query* query, void* workspace, size_t workspace_bytes,

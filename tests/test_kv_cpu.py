@@ -67,7 +67,8 @@ def test_bad_batch(bad):
     dict(strides=(1020, 128, 1024, 128, 4096, 128, 4096, 128)), dict(strides=(1024, 132, 1024, 128, 4096, 128, 4096, 128)),
     dict(strides=(1024, 128, 1024, 128, 4096, 128, -4096, 128)), dict(tokens=-1), dict(q_heads=0), dict(q_heads=12),
     dict(rot=-16), dict(rot=24), dict(rot=144), dict(cos=0), dict(sin=0), dict(cos=CO + 4), dict(positions=-1),
-    dict(tokens=1 << 25),
+    dict(tokens=1 << 25), dict(k=K + 4096), dict(v=V + 4096), dict(q_out=K - 4096), dict(q_out=VS),
+    dict(strides=(1 << 36, 128, 1024, 128, 4096, 128, 4096, 128)),
 ])
 def test_bad_tokens(bad):
     assert fq.load_library().fp8bq_kv_append(cache(), batch(), tokens(**bad), None) == INVALID
@@ -78,6 +79,8 @@ def test_bad_tokens(bad):
     dict(q=0), dict(out=0), dict(q=A + 8), dict(out=B + 2), dict(lse=2), dict(strides=(4100, 128, 4096, 128)),
     dict(strides=(4096, 128, 4096, -128)), dict(tokens=-1), dict(tokens=1 << 25), dict(q_heads=0), dict(q_heads=-8),
     dict(q_heads=20), dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")),
+    dict(scale=3e38), dict(out=K + 64), dict(out=V - 128), dict(lse=KS), dict(out=B, lse=B + 64), dict(out=WS), dict(lse=WS),
+    dict(strides=(4096, 128, 4096, 1 << 36)),
 ])
 def test_bad_query(bad):
     assert fq.load_library().fp8bq_kv_attention(cache(), batch(), query(**bad), WS, 1 << 40, None) == INVALID

@@ -240,6 +240,18 @@ ATTENTION = [
     (128, 64, 1, 8, [200, 131], [150, 131], 0),         # prompts
     (128, 64, 2, 2, [330], [257], 64),
     (64, 64, 1, 1, [400], [400], 0),
+    # 33 to 64 query rows a sequence: tiles of two waves
+    (128, 64, 2, 8, [200, 71, 130], [5, 6, 4], 0),
+    (128, 16, 1, 5, [333], [9], 50),
+    (64, 256, 2, 3, [300, 17], [13, 12], 0),
+    (64, 32, 1, 50, [65], [1], 0),
+    # tiles of four waves at every kind of page and width
+    (128, 16, 1, 4, [190], [90], 0),
+    (128, 256, 1, 4, [390], [65], 0),
+    (64, 16, 2, 2, [130, 64], [70, 64], 20),
+    (192, 128, 1, 3, [260], [50], 0),
+    (256, 32, 1, 2, [170], [77], 0),
+    (256, 64, 1, 1, [129], [129], 0),
 ]
 
 
@@ -255,6 +267,32 @@ def test_attention_within_its_roundings(gpu_lib, dim, page, heads, group, lens, 
     table = tables(g, [-(-x // page) for x in lens], width, pages)
     q = torch.randn((starts[-1], heads * group, dim), generator=g).to(torch.bfloat16)
     check_attention(fq, cache, q, table, lens, starts, one, window=window)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 3.0])
+@pytest.mark.parametrize("new", [None, [3, 2], [9, 8], [40, 31]])
+def test_attention_with_other_scales(gpu_lib, scale, new):
+    """Negative, zero, tiny and large factors of the scores in every kernel."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(21)
+    lens, starts = [150, 77], starts_of(new or [1, 1])
+    cache = random_cache(fq, g, 7, 1, 32, 64)
+    q = (0.1 * torch.randn((starts[-1], 5, 64), generator=g)).to(torch.bfloat16)
+    check_attention(fq, cache, q, [[0, 1, 2, 3, 4], [5, 6, 0, -1, -1]], lens, starts, new is None, scale=scale)
+
+
+def test_attention_without_splits_over_many_row_tiles(gpu_lib):
+    """Enough row tiles to fill the chip: keys are not split, and no workspace
+    is taken; the first sequences share their pages."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(22)
+    n, heads, group, new = 64, 8, 8, 9
+    lens = [9 + (11 * b) % 80 for b in range(n)]
+    cache = random_cache(fq, g, 2 * n, heads, 64, 64)
+    table = [[2 * b, 2 * b + 1] for b in range(n)]
+    table[1] = table[0]
+    starts = starts_of([new] * n)
+    q = torch.randn((n * new, heads * group, 64), generator=g).to(torch.bfloat16)
+    assert fq.kv_attention_workspace_bytes(cache, q.to(DEV), i32(table)) == 0
+    check_attention(fq, cache, q, table, lens, starts, False)
 
 
 @pytest.mark.parametrize("length", [5000, 20001])
@@ -505,6 +543,43 @@ def test_captured_step_follows_the_lengths(gpu_lib):
             same_cache(cache, host(eager))
             lens += 3
         torch.cuda.synchronize()
+
+
+def test_graphs_that_share_a_workspace_in_turn(gpu_lib):
+    """Nothing is kept in the workspace from one call for the next: two graphs
+    of different shapes replayed in turn over one, with other bytes in it
+    before each; and a graph whose call takes its own."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(17)
+    cache = random_cache(fq, g, 60, 2, 64, 128)
+    table = i32([list(range(30)), list(range(30, 60))])
+    lens = i32([1900, 1500])
+    calls = []
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    for heads, new, own in ((8, None, False), (4, [6, 3], False), (16, [90, 33], False), (8, None, True)):
+        starts = None if new is None else i32(starts_of(new))
+        q = torch.randn((2 if new is None else sum(new), heads, 128), generator=g).to(torch.bfloat16).to(DEV)
+        out = torch.zeros_like(q)
+        need = fq.kv_attention_workspace_bytes(cache, q, table)
+        assert 0 < need <= ws.numel()
+
+        def call(q=q, starts=starts, out=out, own=own):
+            fq.kv_attention(cache, q, table, lens, starts, out=out, workspace=None if own else ws)
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        calls.append((graph, q, starts, out))
+    for i in range(4):
+        lens.copy_(i32([1900 - 301 * i, 1500 - 377 * i]))
+        for graph, q, starts, out in calls:
+            ws.fill_(255 if i % 2 else 0x3C)
+            out.zero_()
+            graph.replay()
+            want = fq.kv_attention(cache, q, table, lens, starts)
+            torch.cuda.synchronize()
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
 
 
 def test_side_stream(gpu_lib):
