@@ -577,6 +577,9 @@ struct KvQuery {
 constexpr int kKeyTile = 64;
 // Least factor of a score: a masked one, minus infinity, stays that.
 constexpr float kTiny = 1.17549435e-38f;
+// Least scale of v, 2^-64: its logarithm is taken, and weights times it stay
+// normal numbers.
+constexpr float kLeastVScale = 5.421010862427522e-20f;
 // The work of one workgroup: a tile of query rows of a sequence and a range
 // of its key tiles.
 struct KvWork {
@@ -958,7 +961,7 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
     for (; tile < see.tile1; tile += 4) {
       const int32_t pk_after = page_at(tile + 8, k_run), pv_after = page_at(tile + 8, grp);
       const bool ok = pv >= 0;
-      const float f = ok ? fmaxf(ks * scale, kTiny) : 1.0f, vw = ok ? vs : 0.0f;
+      const float f = ok ? fmaxf(ks * scale, kTiny) : 1.0f, vw = ok ? fmaxf(vs, kLeastVScale) : 0.0f;
       const int32_t t0 = tile * kKeyTile;
       f32x4 s[NT][4];
 #pragma unroll
@@ -1320,7 +1323,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
-      const float v = ok ? fmaxf(sc.v[u], 5.421010862427522e-20f) : 1.0f;   // at least 2^-64
+      const float v = ok ? fmaxf(sc.v[u], kLeastVScale) : 1.0f;
       f[u] = ok ? fmaxf(sc.k[u] * scale, kTiny) : 1.0f;
       lv[u] = __builtin_amdgcn_logf(v);
       back[u] = __builtin_amdgcn_rcpf(v);

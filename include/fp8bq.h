@@ -492,8 +492,7 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  * The launch depends on the shapes alone: captured in a graph, it follows
  * block_table, seq_lens and query_start as they change between replays.
  * out, lse and the workspace lie apart from each other and from the cache
- * (checked).  v_scale below 2^-64 counts as 2^-64 where a sequence has more
- * than 32 query rows per key/value head on average.  Results do not depend on
+ * (checked).  A v_scale below 2^-64 counts as 2^-64.  Results do not depend on
  * timing.  Returns an fp8bq_status.
  */
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
