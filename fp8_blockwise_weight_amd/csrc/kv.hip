@@ -293,9 +293,20 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
       case 16: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 1>), grid, dim3(256), 0, st, c, b, d); break;
       case 32: hipLaunchKernelGGL((fp8bq::kv_attend_rows<D, 2>), grid, dim3(256), 0, st, c, b, d); break;
       case 64:
-        if constexpr (D <= 128) hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 2>), grid, dim3(128), 0, st, c, b, d);
+        if constexpr (D <= 128) {
+          if (c.log_s >= 6) {
+            hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 2, true>), grid, dim3(128), 0, st, c, b, d);
+          } else {
+            hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 2, false>), grid, dim3(128), 0, st, c, b, d);
+          }
+        }
         break;
-      default: hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 4>), grid, dim3(256), 0, st, c, b, d); break;
+      default:
+        if (c.log_s >= 6) {
+          hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 4, true>), grid, dim3(256), 0, st, c, b, d);
+        } else {
+          hipLaunchKernelGGL((fp8bq::kv_attend_tiles<D, 4, false>), grid, dim3(256), 0, st, c, b, d);
+        }
     }
     if (split) {
       const int64_t rows = q->tokens * q->q_heads;

@@ -1154,7 +1154,7 @@ __device__ __forceinline__ float half_max(float v) {
   return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 }
 
-template <int D, int W>
+template <int D, int W, bool kOne>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCache c, KvBatch bt, KvQuery p) {
   constexpr int R = 32 * W, kN = 64 * W;
   constexpr int kC = D / 16;            // 16-byte chunks of a key row
@@ -1198,34 +1198,28 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 
   // Pages of a tile's four runs of 16 tokens, the same in every lane; -1 where
   // the table's entry is no page or none of the tokens is seen.  A page of 64
-  // tokens or more holds the whole tile.
+  // tokens or more (kOne) holds the whole tile.
   const FP8BQ_CONSTANT int32_t* table =
       (const FP8BQ_CONSTANT int32_t*)(uintptr_t)(bt.table + (int64_t)wk.b * bt.stride);
-  const bool one_page = log_s >= 6;
+  constexpr int kRuns = kOne ? 1 : 4;
   struct Pages {
-    int32_t of[4];
+    int32_t of[kRuns];
   };
   auto pages = [&](int32_t tile) {
     Pages x;
-    if (one_page) {
-      int32_t pg = __builtin_amdgcn_readfirstlane(table[(tile * kKeyTile) >> log_s]);
-      pg = pg >= 0 && pg < c.pages ? pg : -1;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x.of[r] = pg;
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int32_t t0 = tile * kKeyTile + 16 * r;
-        int32_t pg = -1;
-        if (t0 < see.see_hi && t0 + 16 > see.see_lo) pg = table[t0 >> log_s];
-        pg = __builtin_amdgcn_readfirstlane(pg);
-        x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
-      }
+    for (int r = 0; r < kRuns; ++r) {
+      const int32_t t0 = tile * kKeyTile + 16 * r;
+      int32_t pg = -1;
+      if (kOne || (t0 < see.see_hi && t0 + 16 > see.see_lo)) pg = table[t0 >> log_s];
+      pg = __builtin_amdgcn_readfirstlane(pg);
+      x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
     }
     return x;
   };
   auto pick = [](const Pages& x, int32_t r) {
-    const int32_t a = r & 1 ? x.of[1] : x.of[0], b = r & 1 ? x.of[3] : x.of[2];
+    if constexpr (kOne) return x.of[0];
+    const int32_t a = r & 1 ? x.of[1 % kRuns] : x.of[0], b = r & 1 ? x.of[3 % kRuns] : x.of[2 % kRuns];
     return r & 2 ? b : a;
   };
 
@@ -1245,21 +1239,21 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 
   u32x4 kr[kLoads], vr[kLoads];
   struct Scales {
-    float k[2], v[2];
+    float k[2], v[2];   // of the lane's two runs (kOne: the same for all)
   };
   auto fetch = [&](int32_t tile, const Pages& x, Scales& sc) {
-    const int32_t in_page = (tile * kKeyTile) & (S - 1);   // 0 unless a page is longer than a tile
-    if (one_page) {
-      const int64_t block = (int64_t)max(x.of[0], 0) * c.heads + h;
-      const uint8_t* kp = c.k + ((block << log_s) + in_page) * D;
-      const uint8_t* vp = c.v + ((block * D) << log_s) + in_page;
+    if constexpr (kOne) {
+      const int32_t in_page = (tile * kKeyTile) & (S - 1);   // 0 unless a page is longer than a tile
+      const int64_t block = (int64_t)max(x.of[0], 0) * c.heads + h, at = block * (D << log_s);
+      const uint8_t* kp = c.k + (at + in_page * D);
+      const uint8_t* vp = c.v + (at + in_page);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         kr[i] = *(const u32x4*)(kp + (uint32_t)(16 * tid + 16 * i * kN));
         vr[i] = *(const u32x4*)(vp + (uint32_t)(v_off + ((i * kN / 4) << log_s)));
       }
-      sc.k[0] = sc.k[1] = c.ks[block];
-      sc.v[0] = sc.v[1] = c.vs[block];
+      sc.k[0] = sc.k[1] = ((const FP8BQ_CONSTANT float*)(uintptr_t)c.ks)[block];
+      sc.v[0] = sc.v[1] = ((const FP8BQ_CONSTANT float*)(uintptr_t)c.vs)[block];
     } else {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -1272,13 +1266,18 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int64_t at = (int64_t)max(half ? x.of[2 * u + 1] : x.of[2 * u], 0) * c.heads + h;
+        const int64_t at = (int64_t)max(pick(x, 2 * u + half), 0) * c.heads + h;
         sc.k[u] = c.ks[at];
         sc.v[u] = c.vs[at];
       }
     }
   };
-  auto bad = [](const Pages& x) { return (x.of[0] | x.of[1] | x.of[2] | x.of[3]) < 0; };
+  auto bad = [](const Pages& x) {
+    int32_t any = x.of[0];
+#pragma unroll
+    for (int r = 1; r < kRuns; ++r) any |= x.of[r];
+    return any < 0;
+  };
   auto is_edge = [&](int32_t tile, const Pages& x) {
     const int32_t t0 = tile * kKeyTile;
     return bad(x) || t0 < see.all_lo || t0 + kKeyTile > see.all_hi;
@@ -1322,7 +1321,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
     float f[2], lv[2], back[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
+      const bool ok = pick(x, 2 * u + half) >= 0;
       const float v = ok ? fmaxf(sc.v[u], kLeastVScale) : 1.0f;
       f[u] = ok ? fmaxf(sc.k[u] * scale, kTiny) : 1.0f;
       lv[u] = __builtin_amdgcn_logf(v);
@@ -1333,7 +1332,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int32_t t0 = tile * kKeyTile + 32 * u + 16 * half;
-        const bool ok = (half ? x.of[2 * u + 1] : x.of[2 * u]) >= 0;
+        const bool ok = pick(x, 2 * u + half) >= 0;
         const int32_t lo = row_lo - t0, hi = ok ? row_hi - t0 : 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[u][e] = e >= lo && e < hi ? s[u][e] : -INFINITY;
