@@ -862,7 +862,13 @@ constexpr int kv_rows_per_simd(int d, int nt) { return nt > 1 ? 1 : (d == 64 ? 4
 //
 // Codes are widened to BF16 exactly and multiplied there (BF16 products with
 // fp32 sums); scales enter in fp32, k's with the score, v's with the weight,
-// which is then rounded to BF16 once (relative 2^-9, its sum is not).
+// which is then rounded to BF16 once (relative 2^-8 at most, its sum is not).
+//
+// Bound by HBM.  One token each of 128 sequences of up to 16384, 32 heads over
+// 8 of 128: 351 us, 6.2 TB/s; one sequence of 131071: 44 us, 6.2 TB/s, and 5
+// for the join; 48 sequences under a window of 4096, heads of 256: 83 us, 4.6 TB/s,
+// where 256 registers leave two waves per SIMD.  Reads pass the caches by
+// (NT hints: 61 -> 57 us for the one sequence), as each byte is read once.
 template <int D, int NT>
 __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_rows(KvCache c, KvBatch bt, KvQuery p) {
   constexpr int R = 16 * NT;
@@ -1130,9 +1136,20 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
   }
 }
 
+// The larger of a lane's value and that of its counterpart in the other half.
+__device__ __forceinline__ float half_max(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+
 // Many query rows: each of W waves holds 32 rows, and all of them share the
-// key tiles, which the workgroup stages in LDS as codes, two tiles deep: the
-// next tile's loads are in flight while the current one is computed.
+// key tiles, which the workgroup stages in LDS as codes, as they lie in the
+// cache: staged as BF16 they would be widened once and not W times, but LDS's
+// traffic doubles (prompts below 318 -> 332 us).  The loads of the next tile
+// are under way in registers while the current one is computed.  Four waves
+// have three buffers, so that one barrier a tile, between the two products,
+// is enough; two waves have two, for the sake of four workgroups per CU
+// (36 rows a sequence, 32 sequences of up to 8192: 52 us against 68).
 //
 // The products are the 32x32x16 ones, scores again transposed.  Key row m of a
 // 32-key product is token 16 ((m / 4) % 2) + 4 (m / 8) + m % 4, which leaves
@@ -1147,13 +1164,14 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
 // k's scale and the softmax scale are one factor per 16 tokens inside the
 // fused multiply-add in front of the exponential; v's scale enters there too,
 // as its logarithm; sums and maxima are only rescaled when a row's maximum
-// has grown by more than 2^8.
-// The larger of a lane's value and that of its counterpart in the other half.
-__device__ __forceinline__ float half_max(float v) {
-  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-}
-
+// has grown by more than 2^8; and a page that holds a whole tile (kOne) makes
+// its addresses and scales uniform (307 -> 294 us).
+//
+// Two prompts of 4096, 32 heads over 8 of 128: 294 us, 934 TFLOP/s of the
+// 1360 of a large matrix product; 500 tokens over 32768: 293 us with the join.
+// Matrix units busy 40% of the cycles, VALU issue 64%, waits 21% of a wave's
+// time; without any exponential and widening it would be 285 us of the 311
+// that it then took.  64 rows a wave, to widen half as often, spills (586 us).
 template <int D, int W, bool kOne>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCache c, KvBatch bt, KvQuery p) {
   constexpr int R = 32 * W, kN = 64 * W;
@@ -1407,7 +1425,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
       // Whoever passes a tile's barrier has done with the buffer that is
       // filled next.  With three buffers what is read was written before the
       // barrier of a tile ago, and the barrier can stand between the products,
-      // where nobody waits for it long (prompts 317 -> 310 us).
+      // where nobody waits for it long (prompts, when it was put there: 317 -> 310 us).
       if constexpr (kBufs == 2) __syncthreads();
       compute(lds + kNow * kBuf, tile, pg[kNow], sc[kNow], [&] {
         if constexpr (kBufs == 3) __syncthreads();
@@ -1488,6 +1506,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 // second is `jump` + 1 behind the first, the others follow it).  N waves share a row, each taking every Nth partial, all in
 // flight at once: with few rows of many splits, as one long sequence has, one
 // wave per row would add up its partials one round trip after another.
+// Latency alone: 5 us for 32 rows of some 60 partials, 8 for 4608 rows.
 template <int D, int N>
 __global__ __launch_bounds__(N == 1 ? 256 : 64 * N) void kv_attend_join(KvBatch bt, KvQuery p, int32_t heads,
                                                                         int32_t R) {
