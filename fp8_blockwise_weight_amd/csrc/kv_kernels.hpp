@@ -75,10 +75,10 @@ __device__ __forceinline__ float kv_fit_scale(float amax) {
   return __uint_as_float(((bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0)) << 23);
 }
 
-// 1 / s of a power of two (exact).
-__device__ __forceinline__ float kv_inverse(float s) {
-  return __uint_as_float((254u << 23) - __float_as_uint(s));
-}
+// 1 / s, rounded to fp32: exact for the powers of two that appends make.  A
+// page that something else has filled can have another scale, which stays
+// while it is large enough; a change of exponent would not be its inverse.
+__device__ __forceinline__ float kv_inverse(float s) { return 1.0f / s; }
 
 __device__ __forceinline__ int32_t kv_clamp(int32_t v, int32_t hi) {
   return v < 0 ? 0 : (v > hi ? hi : v);
@@ -857,7 +857,8 @@ constexpr int kv_rows_per_simd(int d, int nt) { return nt > 1 ? 1 : (d == 64 ? 4
 // 16 (m / 4) + 4 t + m % 4, so that lane group g (16 lanes) ends up with the
 // 16 consecutive tokens 16 g .. 16 g + 15 of its query row: one page, one pair
 // of scales, and exactly the operand order of O^T = V^T P^T, whose lanes read
-// 16 tokens of a channel in one load.  Nothing goes through LDS, and softmax
+// 16 tokens of a channel in one load.  No key or value goes through LDS, which
+// holds the queries and, at the end, the sums of the four waves; softmax
 // needs one exchange across the four lane groups per tile.
 //
 // Codes are widened to BF16 exactly and multiplied there (BF16 products with

@@ -396,8 +396,8 @@ typedef struct fp8bq_kv_cache {
  * These arrays live on the device and are not checked by the host.  The
  * kernels read and write nothing outside the buffers whatever they hold:
  * tokens whose page number is not in 0 .. num_pages - 1, or whose position is
- * negative, beyond max_pages pages or above 2^31 - 1024, are neither stored nor seen, and
- * query_start is clamped to 0 .. tokens.  Rows of no sequence are left as they
+ * negative, beyond max_pages pages or above 2^31 - 1024, are neither stored nor
+ * seen, and query_start is clamped to 0 .. tokens.  Rows of no sequence are left as they
  * are.
  */
 typedef struct fp8bq_kv_batch {
@@ -440,15 +440,19 @@ typedef struct fp8bq_kv_tokens {
  *             over the call's tokens in the page
  *   scale'  = max(scale, fit) if the page holds earlier tokens of the sequence
  *             (slots before the first new one), fit if it does not
- *   earlier codes c become e4m3fn(c * scale / scale'), new ones
- *             e4m3fn(clamp(x / scale', -448, 448)), nearest, ties to even
+ *   earlier codes c become e4m3fn(c * (scale * r)) where the scale grows, new
+ *             ones e4m3fn(clamp(x * r, -448, 448)), nearest, ties to even, with
+ *             r = 1 / scale' (fp32; exact unless something else than an append
+ *             has left a scale that is no power of two)
  * A power of two, unlike the amax / 448 of weights, lets a page's scale grow
  * without rounding the earlier codes again (other than below e4m3's smallest
  * normal value).  Slots behind the new tokens keep their bytes.  Values must
  * be finite: a block with others gets unspecified codes.  The inputs and q_out
- * lie apart from the cache (checked), q_out apart from k and v (not checked).  A page may belong to
- * several sequences as long as no more than one of them stores into it in a
- * call.  fp8bq_dequantize decodes a page's block.
+ * lie apart from the cache (checked), q_out apart from k and v (not checked).
+ * A page may belong to several sequences, but a call stores into it for one of
+ * them, and in one place of its table, only.  Tokens at negative positions and
+ * at positions without a row of cos and sin leave their row of q_out as it was.
+ * fp8bq_dequantize decodes a page's block.
  * No workspace; one launch; may be captured in a graph.
  * Returns an fp8bq_status.
  */
@@ -492,8 +496,8 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  * The launch depends on the shapes alone: captured in a graph, it follows
  * block_table, seq_lens and query_start as they change between replays.
  * out, lse and the workspace lie apart from each other and from the cache
- * (checked).  A v_scale below 2^-64 counts as 2^-64.  Results do not depend on
- * timing.  Returns an fp8bq_status.
+ * (checked).  A v_scale below 2^-64 counts as 2^-64, and above 2^64 the fp32
+ * sums may overflow.  Results do not depend on timing.  Returns an fp8bq_status.
  */
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
                        const fp8bq_kv_query* query, void* workspace, size_t workspace_bytes,

@@ -169,6 +169,31 @@ def test_power_of_two_growth_rounds_once(gpu_lib):
     same_cache(one, host(all_))
 
 
+@pytest.mark.parametrize("new", [None, 1, 3])
+@pytest.mark.parametrize("loud", [True, False])
+def test_append_to_pages_whose_scale_is_no_power_of_two(gpu_lib, new, loud):
+    """Pages that something else has filled: the scale stays where the new
+    tokens fit, and gives way to a power of two where they do not."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(11)
+    heads, size, dim, held, n = 3, 64, 128, 21, new or 1
+    cache = random_cache(fq, g, 1, heads, size, dim, pow2=False)
+    want = host(cache)
+    k, v = (torch.randn((n, heads, dim), generator=g).to(torch.bfloat16) * (64.0 if loud else 0.0625) for _ in range(2))
+    one = np.float32(1)
+    for x, codes, scale, turned in ((k, want[0], want[2], False), (v, want[1], want[3], True)):
+        for h in range(heads):
+            at = codes[0, h].T if turned else codes[0, h]
+            x32, was = x[:, h].float().numpy(), scale[0, h]
+            s = np.float32(max(ref.fit(np.abs(x32).max()), was))
+            assert (s > was) == loud
+            if loud:
+                at[:held] = ref.encode((ref.decode(at[:held]).astype(np.float32) * (was * (one / s))).astype(np.float64))
+            at[held:held + n] = ref.encode((x32 * (one / s)).astype(np.float64))
+            scale[0, h] = s
+    fq.kv_append(cache, k.to(DEV), v.to(DEV), i32([[0]]), i32([held + n]), None if new is None else i32([0, n]))
+    same_cache(cache, want)
+
+
 @pytest.mark.parametrize("single", [True, False])
 def test_append_leaves_out_what_has_no_place(gpu_lib, single):
     """Pages that are none, positions beyond the table, beyond the rotation's
