@@ -779,11 +779,15 @@ struct KvShares {
 
   __device__ __forceinline__ bool next(KvWork& k) {
     if (at >= end) return false;
+    // the next sequence that has rows, 64 at a time
     while (rtile >= s.rtiles) {
       if (++b >= bt.count) return false;
+      const KvSeq mine = kv_seq<R>(bt, p, cap, b + (threadIdx.x & 63));
+      const uint64_t has = __ballot(mine.rtiles > 0);
+      const int32_t which = has != 0 ? __ffsll((unsigned long long)has) - 1 : 63;
+      s = lane_of(mine, which);
+      b += which;
       rtile = 0;
-      s = kv_seq<R>(bt, p, cap, b);
-      s = lane_of(s, 0);
     }
     const int32_t tiles = units(s);
     const int32_t take = (int32_t)min((int64_t)(tiles - t), end - at);

@@ -349,6 +349,21 @@ def test_attention_of_many_sequences(gpu_lib):
     check_attention(fq, cache, q, table, lens, starts, False)
 
 
+@pytest.mark.parametrize("new", [1, 5, 12, 40])
+def test_attention_with_few_sequences_awake(gpu_lib, new):
+    """Long runs of sequences without query tokens, which hold some all the
+    same, before, between and behind the others."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(new)
+    n, awake = 300, {70: 700, 71: 333, 139: 90, 267: 1200}
+    lens = [awake.get(b, 16 * (b % 3)) for b in range(n)]
+    counts = [-(-x // 16) for x in lens]
+    cache = random_cache(fq, g, sum(counts) + 1, 1, 16, 128)
+    table = tables(g, counts, max(counts), cache.num_pages)
+    starts = starts_of([new if b in awake else 0 for b in range(n)])
+    q = torch.randn((starts[-1], 3, 128), generator=g).to(torch.bfloat16)
+    check_attention(fq, cache, q, table, lens, starts, False)
+
+
 @pytest.mark.parametrize("one", [True, False])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_what_no_query_sees_has_no_effect(gpu_lib, one, dim):
