@@ -60,6 +60,12 @@ bool kv_rows_ok(const void* p, int64_t tok, int64_t head) {
          tok < kKvMaxStride && head < kKvMaxStride;
 }
 
+// Whether such rows share no elements, as those must that are written.
+bool kv_distinct(int64_t tokens, int64_t tok, int64_t heads, int64_t head, int32_t dim) {
+  if ((heads > 1 && head < dim) || (tokens > 1 && tok < dim)) return false;
+  return heads == 1 || tokens == 1 || tok >= (heads - 1) * head + dim || head >= (tokens - 1) * tok + dim;
+}
+
 // Bytes from the first to the last of such rows.
 uint64_t kv_extent(int64_t tokens, int64_t tok, int64_t heads, int64_t head, int32_t dim) {
   return 2 * static_cast<uint64_t>((tokens - 1) * tok + (heads - 1) * head + dim);
@@ -184,7 +190,8 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   if (t->q && (!kv_rows_ok(t->q, t->q_token_stride, t->q_head_stride) ||
-               !kv_rows_ok(t->q_out, t->q_out_token_stride, t->q_out_head_stride))) {
+               !kv_rows_ok(t->q_out, t->q_out_token_stride, t->q_out_head_stride) ||
+               !kv_distinct(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, cache->head_dim))) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   const int32_t dim = cache->head_dim;
@@ -259,7 +266,8 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   if (!(scale - scale == 0.0f)) return FP8BQ_ERR_INVALID_ARGUMENT;
   if (batch->count == 0 || q->tokens == 0) return FP8BQ_OK;
   if (!kv_rows_ok(q->q, q->q_token_stride, q->q_head_stride) ||
-      !kv_rows_ok(q->out, q->out_token_stride, q->out_head_stride) || !kv_aligned(q->lse, 4)) {
+      !kv_rows_ok(q->out, q->out_token_stride, q->out_head_stride) || !kv_aligned(q->lse, 4) ||
+      !kv_distinct(q->tokens, q->out_token_stride, q->q_heads, q->out_head_stride, cache->head_dim)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   const KvShape s = kv_shape(*cache, *batch, q->q_heads, q->tokens);

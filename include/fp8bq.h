@@ -410,7 +410,8 @@ typedef struct fp8bq_kv_batch {
 } fp8bq_kv_batch;
 
 /* New tokens.  Rows are BF16, head_dim contiguous values each, 16-byte
- * aligned; strides are in elements and multiples of 8. */
+ * aligned; strides are in elements, multiples of 8 and below 2^36.  Rows that
+ * are written (q_out, an attention's out) share no elements (checked). */
 typedef struct fp8bq_kv_tokens {
   const void* k;      /* [tokens, kv_heads, head_dim] */
   const void* v;      /* [tokens, kv_heads, head_dim] */

@@ -87,6 +87,17 @@ def test_bad_query(bad):
 
 
 @no_gpu
+@pytest.mark.parametrize("token,head", [(0, 128), (4096, 0), (4096, 120), (128, 128), (2048, 128),
+                                         (120, 4096), (128, 1024)])
+def test_written_rows_that_overlap(token, head):
+    lib = fq.load_library()
+    bad = tokens(strides=(1024, 128, 1024, 128, 4096, 128, token, head))
+    assert lib.fp8bq_kv_append(cache(), batch(), bad, None) == INVALID
+    bad = query(strides=(4096, 128, token, head))
+    assert lib.fp8bq_kv_attention(cache(), batch(), bad, WS, 1 << 40, None) == INVALID
+
+
+@no_gpu
 def test_null_structs_and_workspace():
     lib = fq.load_library()
     assert lib.fp8bq_kv_append(None, batch(), tokens(), None) == INVALID
