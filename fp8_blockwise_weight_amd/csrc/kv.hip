@@ -71,6 +71,37 @@ uint64_t kv_extent(int64_t tokens, int64_t tok, int64_t heads, int64_t head, int
   return 2 * static_cast<uint64_t>((tokens - 1) * tok + (heads - 1) * head + dim);
 }
 
+// BF16 rows [tokens, heads, dim] of a call.
+struct KvRows {
+  const void* p;
+  int64_t tok, heads, head;
+};
+
+// Whether rows share no element with others: by their extents, or interleaved
+// with them token by token or head by head, as slices of one tensor are.
+bool kv_rows_apart(const KvRows& a, const KvRows& b, int64_t tokens, int32_t dim) {
+  if (!overlap(a.p, kv_extent(tokens, a.tok, a.heads, a.head, dim), b.p,
+               kv_extent(tokens, b.tok, b.heads, b.head, dim))) {
+    return true;
+  }
+  const int64_t off = (static_cast<int64_t>(reinterpret_cast<intptr_t>(b.p)) -
+                       static_cast<int64_t>(reinterpret_cast<intptr_t>(a.p))) / 2;
+  // pieces of `in_a` and `in_b` elements, the next ones `out` further on
+  auto beside = [&](int64_t out, int64_t in_a, int64_t in_b) {
+    if (out <= 0) return false;
+    const int64_t d = (off % out + out) % out;
+    return d >= in_a && d + in_b <= out;
+  };
+  return (a.tok == b.tok && beside(a.tok, (a.heads - 1) * a.head + dim, (b.heads - 1) * b.head + dim)) ||
+         (a.head == b.head && beside(a.head, (tokens - 1) * a.tok + dim, (tokens - 1) * b.tok + dim));
+}
+
+// Whether output rows are their input's own, or apart from them.
+bool kv_rows_same_or_apart(const KvRows& out, const KvRows& in, int64_t tokens, int32_t dim) {
+  const bool same = out.p == in.p && (tokens == 1 || out.tok == in.tok) && (in.heads == 1 || out.head == in.head);
+  return same || kv_rows_apart(out, in, tokens, dim);
+}
+
 // Whether a buffer that is written lies apart from all of the cache.
 bool kv_apart(const fp8bq_kv_cache& c, const void* p, uint64_t bytes) {
   const uint64_t blocks = static_cast<uint64_t>(c.num_pages) * static_cast<uint64_t>(c.kv_heads);
@@ -201,6 +232,14 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
                          kv_extent(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, dim)))) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
+  if (t->q) {
+    const KvRows out{t->q_out, t->q_out_token_stride, t->q_heads, t->q_out_head_stride};
+    if (!kv_rows_same_or_apart(out, KvRows{t->q, t->q_token_stride, t->q_heads, t->q_head_stride}, t->tokens, dim) ||
+        !kv_rows_apart(out, KvRows{t->k, t->k_token_stride, cache->kv_heads, t->k_head_stride}, t->tokens, dim) ||
+        !kv_rows_apart(out, KvRows{t->v, t->v_token_stride, cache->kv_heads, t->v_head_stride}, t->tokens, dim)) {
+      return FP8BQ_ERR_INVALID_ARGUMENT;
+    }
+  }
   if (t->rot_dim > 0 && (!t->cos || !t->sin || !kv_aligned(t->cos, 16) || !kv_aligned(t->sin, 16) ||
                          t->positions < 0)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
@@ -268,6 +307,11 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   if (!kv_rows_ok(q->q, q->q_token_stride, q->q_head_stride) ||
       !kv_rows_ok(q->out, q->out_token_stride, q->out_head_stride) || !kv_aligned(q->lse, 4) ||
       !kv_distinct(q->tokens, q->out_token_stride, q->q_heads, q->out_head_stride, cache->head_dim)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (!kv_rows_same_or_apart(KvRows{q->out, q->out_token_stride, q->q_heads, q->out_head_stride},
+                             KvRows{q->q, q->q_token_stride, q->q_heads, q->q_head_stride}, q->tokens,
+                             cache->head_dim)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   const KvShape s = kv_shape(*cache, *batch, q->q_heads, q->tokens);

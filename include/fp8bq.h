@@ -449,7 +449,8 @@ typedef struct fp8bq_kv_tokens {
  * without rounding the earlier codes again (other than below e4m3's smallest
  * normal value).  Slots behind the new tokens keep their bytes.  Values must
  * be finite: a block with others gets unspecified codes.  The inputs and q_out
- * lie apart from the cache (checked), q_out apart from k and v (not checked).
+ * lie apart from the cache, q_out apart from k and v and, if it is not q, from
+ * q (checked; slices of one tensor, token by token or head by head, are apart).
  * A page may belong to several sequences, but a call stores into it for one of
  * them, and in one place of its table, only.  Tokens at negative positions and
  * at positions without a row of cos and sin leave their row of q_out as it was.
@@ -496,8 +497,8 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  *                    may overlap (other streams, graphs) need one each
  * The launch depends on the shapes alone: captured in a graph, it follows
  * block_table, seq_lens and query_start as they change between replays.
- * out, lse and the workspace lie apart from each other and from the cache
- * (checked).  A v_scale below 2^-64 counts as 2^-64, and above 2^64 the fp32
+ * out, lse and the workspace lie apart from each other and from the cache, and
+ * out, if it is not q, from q (checked).  A v_scale below 2^-64 counts as 2^-64, and above 2^64 the fp32
  * sums may overflow.  Results do not depend on timing.  Returns an fp8bq_status.
  */
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,

@@ -97,6 +97,43 @@ def test_written_rows_that_overlap(token, head):
     assert lib.fp8bq_kv_attention(cache(), batch(), bad, WS, 1 << 40, None) == INVALID
 
 
+ROWS = 9 * 4096 * 2   # bytes of nine tokens of 32 heads
+
+
+@no_gpu
+@pytest.mark.parametrize("at,strides,ok", [
+    (A, (4096, 128), True),                # in place
+    (A + ROWS, (4096, 128), True),         # behind the queries
+    (A + 8192, (4096, 128), False),        # a token further on
+    (A - 256, (4096, 128), False),         # a head before
+    (A, (128, 9 * 128), False),            # the same memory in another order
+    (A + 16, (4096, 128), False),
+])
+def test_outputs_over_their_queries(at, strides, ok):
+    lib = fq.load_library()
+    status = lib.fp8bq_kv_attention(cache(), batch(), query(out=at, strides=(4096, 128, *strides)), WS, 1 << 40, None)
+    assert (status != INVALID) == ok
+    status = lib.fp8bq_kv_append(cache(), batch(),
+                                 tokens(k=C, v=D, q=A, q_out=at, strides=(1024, 128, 1024, 128, 4096, 128, *strides)),
+                                 None)
+    assert (status != INVALID) == ok
+
+
+@no_gpu
+@pytest.mark.parametrize("token,head,k,v,q_out,ok", [
+    (6144, 128, 4096, 5120, 0, True),      # q, k and v of one projection, queries in place
+    (6144, 128, 4096, 5120, 128, False),
+    (6144, 128, 4088, 5120, 0, False),     # k begins within the queries
+    (6144, 128, 4096, 5128, 0, False),     # v ends in the next token's queries
+    (128, 3 * 9 * 128, 9 * 128, 18 * 128, 0, True),    # head by head
+    (128, 3 * 9 * 128, 9 * 128 - 8, 18 * 128, 0, False),
+    (128, 3 * 9 * 128, 18 * 128, 18 * 128 + 8, 0, False),
+])
+def test_queries_beside_keys_and_values(token, head, k, v, q_out, ok):
+    args = tokens(k=A + 2 * k, v=A + 2 * v, q=A, q_out=A + 2 * q_out, strides=(token, head) * 4)
+    assert (fq.load_library().fp8bq_kv_append(cache(), batch(), args, None) != INVALID) == ok
+
+
 @no_gpu
 def test_null_structs_and_workspace():
     lib = fq.load_library()
