@@ -137,10 +137,10 @@ void kv_for_dim(int32_t dim, F&& f) {
   }
 }
 
-// Sequences whose table has room for no more key tiles than this are done by
-// one workgroup for each row tile and head: a few more tiles to each wave
-// (about 1.5 us each) cost less than joining parts in a second launch.
-constexpr int64_t kKvWhole = 16;
+// Key tiles, of those a row tile can see at most, up to which splitting them
+// over workgroups does not pay: a few more tiles to each wave (1.5 to 2 us
+// each) cost less than joining parts in a second launch.
+constexpr int64_t kKvFew = 8, kKvWhole = 16, kKvWholeOfMany = 32;
 
 // How an attention call is cut up: from the shapes alone, so that the
 // workspace can be sized, and a launch captured, before any length is known.
@@ -154,6 +154,20 @@ constexpr int64_t kKvWhole = 16;
 //   33 to 64   tiles of 64 rows: 64 rows 75, in tiles of 128 rows 94; not
 //              above 128 channels, whose registers leave one wave per SIMD
 //   above      tiles of 128 rows
+// Where key tiles are few, tiles of 64 rows are also taken for 17 to 32 rows
+// of 128 channels, if workgroups of kv_attend_rows<32>, one to a CU, would take
+// turns (100 sequences of 200 or 500, 24 rows: 22.0 -> 16.9, 27.7 -> 25.3), and
+// for 129 to 192 rows, of which tiles of 128 would leave a quarter empty
+// (100 sequences of 300 or 1000, 144 rows: 41 -> 35, 84 -> 76; of 8192, where
+// keys are read from HBM, 162 -> 181, so not there).
+// Keys are not split over workgroups where row tiles see few key tiles (a small
+// window counts), or not many and there are many row tiles:
+//   kv_attend_rows   one sequence of 1256: 14.9 split, 15.0 not; 16 of 2000:
+//                    26.1 and 22.2; 8 of 2000: 18.2 and 22.0; 25 of 1256,
+//                    16 heads to a key head of 64: 20.1 and 12.3
+//   kv_attend_tiles  a prompt of 300 / 1000 / 2000: 21.3 / 45.8 / 70.1 split,
+//                    14.8 / 32.7 / 62.3 not; 500 tokens over 2000: 43.5 and
+//                    54.5; window of 30, 18 sequences: 26.6 and 13.0
 // `resident` workgroups are what registers and LDS let the card hold at once
 // and what was fastest: one sequence of 131071, rows of 16, 512: 52.8 us,
 // 384: 61.6, 768: 55.4; drafted tokens in tiles of 64, 1024: 49.2, 768: 52.9,
@@ -169,31 +183,46 @@ struct KvShape {
   size_t rows_at, ml_at, bytes;   // workspace: partial sums at 0, then these
 };
 
-KvShape kv_shape(const fp8bq_kv_cache& c, const fp8bq_kv_batch& b, int32_t q_heads, int64_t tokens) {
+KvShape kv_shape(const fp8bq_kv_cache& c, const fp8bq_kv_batch& b, int32_t q_heads, int64_t tokens,
+                 int32_t window) {
   KvShape s;
   s.group = q_heads / c.kv_heads;
   const int64_t per_seq = ceil_div(tokens * s.group, b.count);
+  const auto row_tiles = [&](int32_t rows) { return tokens * s.group / rows + b.count; };   // of a head, at most
+  const auto key_tiles = [&](int32_t rows) {   // of a row tile, at most
+    const int64_t all = ceil_div(static_cast<int64_t>(b.max_pages) * c.page_size, 64);
+    const int64_t seen = ceil_div(int64_t{window} + rows / s.group, 64) + 1;
+    return window > 0 && seen < all ? seen : all;
+  };
   s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 && c.head_dim <= 128 ? 64 : 128));
-  const int64_t base = tokens * s.group / s.rows + b.count;   // row tiles of all sequences, at most
+  if (s.rows == 32 && c.head_dim == 128 && key_tiles(32) <= kKvFew && row_tiles(32) * c.kv_heads > 256) s.rows = 64;
+  if (s.rows == 128 && c.head_dim <= 128 && per_seq > 128 && per_seq <= 192 && key_tiles(128) <= kKvWhole) s.rows = 64;
+  const int64_t base = row_tiles(s.rows), tiles = key_tiles(s.rows), items = base * c.kv_heads;
   const int resident =
       s.rows == 16 ? (c.head_dim == 64 ? 768 : 512) : (s.rows == 64 ? 1024 : (s.rows == 128 ? 512 : 256));
-  const int64_t tiles = ceil_div(static_cast<int64_t>(b.max_pages) * c.page_size, 64);
   s.min_tiles = 4;
   s.target = static_cast<int32_t>(ceil_div(resident, c.kv_heads));
-  if (s.rows <= 32 && tiles > kKvWhole) {
-    s.grid = s.target;
+  if (s.rows <= 32) {
+    if (tiles <= kKvWhole || (tiles <= kKvWholeOfMany && items >= 128)) s.target = 0;
+    s.grid = s.target ? s.target : static_cast<int32_t>(base);
     s.slots = 2 * s.target;
     s.jump = s.target;
   } else {
-    if (s.rows <= 32 || base * c.kv_heads >= resident) s.target = 0;
+    const int64_t few = c.head_dim <= 128 ? kKvFew : kKvFew / 2;   // a tile takes twice as long
+    if (tiles <= few || items >= resident || (tiles <= kKvWholeOfMany && items >= resident / 2)) s.target = 0;
     s.grid = static_cast<int32_t>(base + s.target);
     s.slots = s.grid;
     s.jump = 0;
   }
+  if (s.target == 0) {
+    s.slots = s.jump = 0;
+    s.ml_at = s.rows_at = s.bytes = 0;
+    return s;
+  }
   const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(c.kv_heads) * static_cast<size_t>(s.rows);
   s.ml_at = n * static_cast<size_t>(c.head_dim) * 4;
   s.rows_at = s.ml_at + n * 8;
-  s.bytes = s.target == 0 ? 0 : s.rows_at + static_cast<size_t>(tokens) * static_cast<size_t>(q_heads) * 8;
+  s.bytes = s.rows_at + static_cast<size_t>(tokens) * static_cast<size_t>(q_heads) * 8;
   return s;
 }
 
@@ -292,7 +321,7 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
       !kv_heads_ok(q_heads, cache->kv_heads, batch->count, tokens)) {
     return 0;
   }
-  return kv_shape(*cache, *batch, q_heads, tokens).bytes;
+  return kv_shape(*cache, *batch, q_heads, tokens, 0).bytes;
 }
 
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, const fp8bq_kv_query* q,
@@ -314,7 +343,10 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
                              cache->head_dim)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
-  const KvShape s = kv_shape(*cache, *batch, q->q_heads, q->tokens);
+  // The workspace is sized without the window: a shape that wants more is not taken.
+  KvShape s = kv_shape(*cache, *batch, q->q_heads, q->tokens, q->window);
+  const KvShape all = kv_shape(*cache, *batch, q->q_heads, q->tokens, 0);
+  if (s.bytes > all.bytes) s = all;
   if (s.bytes > 0 && (workspace == nullptr || workspace_bytes < s.bytes || !kv_aligned(workspace, 16))) {
     return FP8BQ_ERR_WORKSPACE;
   }

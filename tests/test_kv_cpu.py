@@ -170,6 +170,27 @@ def test_workspace_depends_on_shapes_alone():
     assert f(cache(), batch(**none, width=17, stride=17, count=9), 32, 9) > 0
 
 
+@no_gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_window_never_needs_more_workspace(dim):
+    """The size is asked for without the window that a call then has."""
+    lib, refused = fq.load_library(), []
+    for heads, group in ((1, 1), (1, 16), (4, 8), (8, 4), (16, 3)):
+        one = cache(heads=heads, dim=dim)
+        for count in (1, 3, 9, 20, 35, 40, 60, 75, 130):
+            for new in (1, 3, 4, 12, 18, 40, 300):
+                for width in (1, 7, 12, 17, 20, 33, 500):
+                    held = batch(count=count, width=width, stride=width)
+                    tokens = count * new
+                    need = lib.fp8bq_kv_attention_workspace_bytes(one, held, heads * group, tokens)
+                    for window in (1, 100, 400, 500, 600, 900, 1000, 1900, 5000):
+                        q = query(strides=(heads * group * dim, dim) * 2, tokens=tokens, q_heads=heads * group,
+                                  window=window)
+                        if lib.fp8bq_kv_attention(one, held, q, WS, need, None) == WORKSPACE:
+                            refused.append((heads, group, count, new, width, window))
+    assert not refused, (len(refused), refused[:5])
+
+
 def test_struct_sizes():
     assert (kv._CACHE.size, kv._BATCH.size, kv._TOKENS.size, kv._QUERY.size) == (56, 40, 144, 80)
 

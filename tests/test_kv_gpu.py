@@ -277,6 +277,9 @@ ATTENTION = [
     (192, 128, 1, 3, [260], [50], 0),
     (256, 32, 1, 2, [170], [77], 0),
     (256, 64, 1, 1, [129], [129], 0),
+    # few keys: two row tiles of 64 and a rest; many sequences of 17 to 32 rows
+    (128, 64, 1, 9, [170, 20], [20, 16], 0),
+    (128, 32, 3, 3, [40 + b for b in range(90)], [7] * 90, 0),
 ]
 
 
@@ -318,6 +321,21 @@ def test_attention_without_splits_over_many_row_tiles(gpu_lib):
     q = torch.randn((n * new, heads * group, 64), generator=g).to(torch.bfloat16)
     assert fq.kv_attention_workspace_bytes(cache, q.to(DEV), i32(table)) == 0
     check_attention(fq, cache, q, table, lens, starts, False)
+
+
+@pytest.mark.parametrize("window", [60, 900, 1500, 3000])
+@pytest.mark.parametrize("new", [1, 6, 30, 140])
+def test_attention_under_windows_in_long_tables(gpu_lib, new, window):
+    """Whether keys are split goes by what the window leaves to see."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(window + new)
+    lens = [3000, 40, 2500]
+    news = [new, min(new, 40), 2]
+    counts = [-(-x // 64) for x in lens]
+    cache = random_cache(fq, g, sum(counts) + 1, 1, 64, 64)
+    table = tables(g, counts, max(counts), cache.num_pages)
+    starts = starts_of(news)
+    q = torch.randn((starts[-1], 2, 64), generator=g).to(torch.bfloat16)
+    check_attention(fq, cache, q, table, lens, starts, False, window=window)
 
 
 @pytest.mark.parametrize("length", [5000, 20001])
