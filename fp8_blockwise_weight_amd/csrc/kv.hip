@@ -151,9 +151,13 @@ constexpr int64_t kKvFew = 8, kKvWhole = 16, kKvWholeOfMany = 32;
 //              sequences: 339 against 361; half the registers go unused)
 //   17 to 32   kv_attend_rows<32>: 24 rows 57.5, in tiles of 64 rows 64.2
 //              (256 channels: 102 against 222)
-//   33 to 64   tiles of 64 rows: 64 rows 75, in tiles of 128 rows 94; not
-//              above 128 channels, whose registers leave one wave per SIMD
-//   above      tiles of 128 rows
+//   33 to 64   tiles of 64 rows: 64 rows 75, in tiles of 128 rows 94; above 128
+//              channels, whose registers leave one wave per SIMD, twice
+//              kv_attend_rows<32>: 64 rows of 256 channels 172, in tiles of 128
+//              229 (but 100 sequences of 500, 80 and 71: tiles of 128 where
+//              keys are few and row tiles many)
+//   above      tiles of 128 rows (80 rows of 256 channels 232, in three of 32
+//              262)
 // Where key tiles are few, tiles of 64 rows are also taken for 17 to 32 rows
 // of 128 channels, if workgroups of kv_attend_rows<32>, one to a CU, would take
 // turns (100 sequences of 200 or 500, 24 rows: 22.0 -> 16.9, 27.7 -> 25.3), and
@@ -196,6 +200,10 @@ KvShape kv_shape(const fp8bq_kv_cache& c, const fp8bq_kv_batch& b, int32_t q_hea
   };
   s.rows = per_seq <= 16 ? 16 : (per_seq <= 32 ? 32 : (per_seq <= 64 && c.head_dim <= 128 ? 64 : 128));
   if (s.rows == 32 && c.head_dim == 128 && key_tiles(32) <= kKvFew && row_tiles(32) * c.kv_heads > 256) s.rows = 64;
+  if (s.rows == 128 && c.head_dim > 128 && per_seq <= 64 &&
+      (key_tiles(32) > kKvWhole || row_tiles(32) * c.kv_heads <= 256)) {
+    s.rows = 32;
+  }
   if (s.rows == 128 && c.head_dim <= 128 && per_seq > 128 && per_seq <= 192 && key_tiles(128) <= kKvWhole) s.rows = 64;
   const int64_t base = row_tiles(s.rows), tiles = key_tiles(s.rows), items = base * c.kv_heads;
   const int resident =

@@ -280,6 +280,9 @@ ATTENTION = [
     # few keys: two row tiles of 64 and a rest; many sequences of 17 to 32 rows
     (128, 64, 1, 9, [170, 20], [20, 16], 0),
     (128, 32, 3, 3, [40 + b for b in range(90)], [7] * 90, 0),
+    # 33 to 64 rows of wide heads, few and many row tiles
+    (256, 64, 2, 8, [200, 71, 130], [5, 6, 4], 0),
+    (192, 16, 3, 6, [20 + b for b in range(40)], [8] * 40, 30),
 ]
 
 
