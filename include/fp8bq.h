@@ -495,6 +495,8 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  *   workspace        device buffer of at least fp8bq_kv_attention_workspace_bytes
  *   workspace_bytes  bytes, 16-byte aligned, needing no initial value; calls that
  *                    may overlap (other streams, graphs) need one each
+ * The kernel is chosen by the mean number of query rows per sequence: prompts
+ * and single tokens are served faster in calls of their own.
  * The launch depends on the shapes alone: captured in a graph, it follows
  * block_table, seq_lens and query_start as they change between replays.
  * out, lse and the workspace lie apart from each other and from the cache, and
