@@ -841,6 +841,16 @@ __device__ __forceinline__ bf16x8 kv_widen(uint32_t a, uint32_t b) {
   return bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
+// Infinite queries as NaN (the exponent's carry sets the top bit of the
+// mantissa).  A row with either is then NaN as its scores are, each of them: an
+// infinity alone can give -inf for every key, which is what a row that sees
+// nothing has, and whose sums are zeros.
+__device__ __forceinline__ u32x4 kv_no_infinity(u32x4 x) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] |= (((x[e] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u) >> 9;
+  return x;
+}
+
 // The largest part of D channels, in equal parts of whole 16s, within `most`.
 constexpr int kv_part(int d, int most) {
   int parts = 1;
@@ -950,7 +960,7 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
       if (r < wk.count) {
         const int32_t tok = r / p.group, g = r - tok * p.group;
         x = *(const u32x4*)(p.q + (wk.row0 + tok) * p.q_tok + ((int64_t)h * p.group + g) * p.q_head + 8 * ch);
-        x ^= u32x4{flip, flip, flip, flip};
+        x = kv_no_infinity(x ^ u32x4{flip, flip, flip, flip});
       }
       *(u32x4*)(q_lds + rr * (D + 8) + 8 * ch) = x;
     }
@@ -1092,8 +1102,9 @@ __global__ __launch_bounds__(kThreads, kv_rows_per_simd(D, NT)) void kv_attend_r
     float top = -INFINITY, sum = 0.0f;
     if (mine) {
       for (int w = 0; w < 4; ++w) top = fmaxf(top, lds_m[w][rr]);
+      // a wave without a maximum has a sum of zero, or NaN, which stays
       for (int w = 0; w < 4; ++w) {
-        if (lds_m[w][rr] != -INFINITY) sum += lds_l[w][rr] * __builtin_amdgcn_exp2f(lds_m[w][rr] - top);
+        sum += lds_l[w][rr] * (lds_m[w][rr] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lds_m[w][rr] - top));
       }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -1205,12 +1216,18 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
   {
     const uint16_t* src = p.q + row * p.q_tok + head * p.q_head + 16 * half;
     const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
+    uint32_t most = 0;
 #pragma unroll
     for (int s = 0; s < 2 * kM; ++s) {
       u32x4 x = *(const u32x4*)(src + 32 * (s >> 1) + 8 * (s & 1));
       x ^= u32x4{flip, flip, flip, flip};
       if (!live) x = u32x4{0, 0, 0, 0};
+      most = pk_max_u16(most, fold_abs(x));
       q[s] = __builtin_bit_cast(bf16x8, x);
+    }
+    if (__ballot(halves_max(most) >= 0x7F80u) != 0) {
+#pragma unroll
+      for (int s = 0; s < 2 * kM; ++s) q[s] = __builtin_bit_cast(bf16x8, kv_no_infinity(__builtin_bit_cast(u32x4, q[s])));
     }
   }
   const float scale = fabsf(p.scale);
@@ -1547,15 +1564,16 @@ __global__ __launch_bounds__(N == 1 ? 256 : 64 * N) void kv_attend_join(KvBatch 
     float now = top;
 #pragma unroll
     for (int j = 0; j < 8; ++j) now = fmaxf(now, ml[j].x);
-    if (now == -INFINITY) continue;
-    const float keep = __builtin_amdgcn_exp2f(top - now);
+    // where no part has a maximum yet, sums are zero, or NaN, which stays
+    const float base = now == -INFINITY ? 0.0f : now;
+    const float keep = __builtin_amdgcn_exp2f(top - base);
     top = now;
     sum *= keep;
 #pragma unroll
     for (int y = 0; y < kV; ++y) acc[y] *= keep;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float f = i0 + j * N < n ? __builtin_amdgcn_exp2f(ml[j].x - now) : 0.0f;
+      const float f = i0 + j * N < n ? __builtin_amdgcn_exp2f(ml[j].x - base) : 0.0f;
       sum += ml[j].y * f;
 #pragma unroll
       for (int y = 0; y < kV; ++y) acc[y] += x[j][y] * f;

@@ -486,7 +486,8 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  *   s_j = scale * (q . decode(k_j) * k_scale)    j <= p, j > p - window
  *   out = sum_j exp(s_j - max s) decode(v_j) v_scale / sum_j exp(s_j - max s)
  *   lse = max s + log sum_j exp(s_j - max s)
- * A query that sees no token gets zeros and lse = -inf.  Scores, maxima and
+ * A query that sees no token gets zeros and lse = -inf; one that sees some and
+ * has a NaN or an infinity among its values gets NaN for both.  Scores, maxima and
  * sums are fp32; the weights exp(s - max) * v_scale are rounded to BF16 before
  * their product with the values, the output once more.  Any positive scales
  * are taken, not powers of two alone.  What lies in pages beyond the sequence

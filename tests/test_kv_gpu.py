@@ -704,3 +704,57 @@ def test_refusals(gpu_lib):
     assert (at(q=q, tb=torch.zeros((1, 0), dtype=torch.int32, device=DEV)) == 0).all()
     torch.cuda.synchronize()
     assert math.isfinite(float(at().float().sum()))
+
+
+FORMS = [
+    # dim, page, heads, group, new: every kernel, its rows split over workgroups and not
+    (64, 16, 2, 3, None), (128, 64, 2, 4, None), (256, 128, 1, 2, None),
+    (64, 64, 1, 5, [6, 4, 4, 1]), (128, 32, 2, 4, [6, 5, 6, 1]), (256, 64, 1, 8, [6, 5, 5, 1]),
+    (64, 32, 1, 8, [6, 5, 7, 1]), (128, 64, 2, 8, [5, 6, 4, 1]),
+    (64, 64, 2, 4, [40, 33, 50, 1]), (128, 16, 1, 4, [50, 40, 33, 1]), (256, 64, 1, 2, [70, 90, 50, 1]),
+]
+
+
+@pytest.mark.parametrize("room", [0, 1300])
+@pytest.mark.parametrize("dim,page,heads,group,new", FORMS)
+def test_query_rows_that_are_no_numbers(gpu_lib, dim, page, heads, group, new, room):
+    """A row of queries with a NaN or an infinity is NaN, and so is its sum, if
+    it sees a token: not the zeros of a row that sees none.  Its neighbours are
+    as without it.  Keys are positive in channel 0, so that an infinity of
+    either sign there makes all of its row's scores infinite alike."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(dim + page)
+    lens = [1300, 700, 130, 1]
+    n = [1] * 4 if new is None else new
+    starts = starts_of(n)
+    counts = [-(-x // page) for x in lens]
+    cache = random_cache(fq, g, sum(counts) + 1, heads, page, dim)
+    first = cache.k.view(torch.uint8)[..., 0]
+    first &= 0x7F
+    first[first == 0] = 0x38
+    width = -(-room // page) if room else 0
+    table = i32([r + [-1] * width for r in tables(g, counts, max(counts), cache.num_pages)])
+    q = torch.randn((starts[-1], heads * group, dim), generator=g).to(torch.bfloat16).to(DEV)
+    st = None if new is None else i32(starts)
+    want, want_lse = fq.kv_attention(cache, q, table, i32(lens), st, return_lse=True)
+    marks = [(0, 0, 3, math.nan), (0, heads * group - 1, 0, math.inf), (1, 0, 0, -math.inf), (1, heads, 0, math.inf),
+             (2, 1, dim - 1, math.nan), (3, 0, 0, -math.inf), (3, heads * group - 1, 5, math.nan)]
+    bad = torch.zeros((starts[-1], heads * group), dtype=torch.bool)
+    x = q.clone()
+    for b, h, c, value in marks:
+        for row in {starts[b], starts[b + 1] - 1}:
+            x[row, h, c] = value
+            bad[row, h] = True
+    bad = bad.to(DEV)
+    got, lse = fq.kv_attention(cache, x, table, i32(lens), st, return_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(got[~bad].view(torch.int16), want[~bad].view(torch.int16))
+    assert torch.equal(lse[~bad], want_lse[~bad])
+    # rows that see nothing are zero whatever they hold
+    x[:] = math.nan
+    got, lse = fq.kv_attention(cache, x, table, i32([0, 700, -5, 1]), st, return_lse=True)
+    torch.cuda.synchronize()
+    none = torch.zeros(starts[-1], dtype=torch.bool)
+    none[:starts[1]] = none[starts[2]:starts[3]] = True
+    assert (got[none.to(DEV)] == 0).all() and (lse[none.to(DEV)] == -math.inf).all()
+    assert torch.isnan(got[~none.to(DEV)]).all() and torch.isnan(lse[~none.to(DEV)]).all()
