@@ -142,3 +142,45 @@ def attention(cache, q, table, lens, starts, scale=None, window=0):
                 lse[row, h * group:(h + 1) * group] = (m + z.log())[:, 0]
                 tol_lse[row, h * group:(h + 1) * group] = (rel + 8 * e * (m.abs() + z.log() + 1))[:, 0]
     return out, lse, tol, tol_lse
+
+
+def attention_of_long(cache, q, table, lens, starts, scale=None, window=0):
+    """The same as ``attention``, a sequence and head at a time, for long
+    sequences whose pages are all pages and that hold all of their queries."""
+    kc, vc, ks, vs = cache
+    heads, size, dim = kc.shape[1:]
+    group = q.shape[1] // heads
+    scale = dim ** -0.5 if scale is None else scale
+    u, e = 2.0 ** -8, 2.0 ** -24
+    out, lse = torch.zeros(q.shape, dtype=torch.float64), torch.full(q.shape[:2], -math.inf, dtype=torch.float64)
+    tol, tol_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    for b in range(len(lens)):
+        n, L, rows = int(starts[b + 1] - starts[b]), int(lens[b]), slice(int(starts[b]), int(starts[b + 1]))
+        pg = np.array(table[b][:-(-L // size)])
+        pos, key = torch.arange(L - n, L)[:, None], torch.arange(L)
+        hidden = ((key > pos) | ((key <= pos - window) if window else (key < 0)))[:, None]
+        N = (~hidden).sum(2, keepdim=True).double()
+        for h in range(heads):
+            at = slice(h * group, (h + 1) * group)
+            k = torch.from_numpy((decode(kc[pg, h]) * ks[pg, h, None, None].astype(np.float64)).reshape(-1, dim)[:L])
+            v = torch.from_numpy((decode(vc[pg, h]) * vs[pg, h, None, None].astype(np.float64)).transpose(0, 2, 1)
+                                 .reshape(-1, dim)[:L])
+            lv = torch.from_numpy(np.abs(np.log2(vs[pg, h].astype(np.float64))).repeat(size)[:L])
+            lv = lv.expand(n, 1, L).masked_fill(hidden, 0).amax(2, keepdim=True)
+            x = q[rows, at].double().reshape(n * group, dim)
+            s = (x @ k.T * scale).view(n, group, L)
+            ds = ((dim + 4) * e * (x.abs() @ k.abs().T).view(n, group, L) * abs(scale) + 4 * e * s.abs())
+            ds = ds.masked_fill(hidden, 0).amax(2, keepdim=True)
+            s = s.masked_fill(hidden, -math.inf)
+            m = s.amax(2, keepdim=True)
+            far = (m - s).masked_fill(hidden, 0).amax(2, keepdim=True)
+            w = torch.exp(s - m)
+            z = w.sum(2, keepdim=True)
+            w = w.view(n * group, L)
+            o, a = (w @ v).view(n, group, dim) / z, (w @ v.abs()).view(n, group, dim) / z
+            rel = 2 * (ds + (5 + 3 * far + 4 * lv) * e + 2 * N * e)
+            out[rows, at] = o
+            tol[rows, at] = u * o.abs() + (u * (1 + u) + rel) * a + 1e-30
+            lse[rows, at] = (m + z.log())[..., 0]
+            tol_lse[rows, at] = (rel + 8 * e * (m.abs() + z.log() + 1))[..., 0]
+    return out, lse, tol, tol_lse

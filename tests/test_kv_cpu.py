@@ -248,3 +248,17 @@ def test_reference_codes_are_the_format():
 def test_reference_scale(amax, want):
     s = ref.fit(amax)
     assert s == want and 448.0 * s >= amax and (amax < 1e-9 or 448.0 * s / 2 < amax)
+
+
+@pytest.mark.parametrize("dim,page,heads,group,lens,new,window", [
+    (64, 16, 2, 3, [40, 17], [5, 17], 0), (128, 32, 1, 2, [90, 33], [9, 1], 20),
+])
+def test_reference_attention_of_long_is_the_same(dim, page, heads, group, lens, new, window):
+    g = torch.Generator().manual_seed(1)
+    codes = torch.randint(0, 126, (9, heads, page, dim), generator=g).to(torch.uint8).numpy()
+    turned = np.ascontiguousarray(codes[::-1].transpose(0, 1, 3, 2)) | 0x80
+    scales = [(0.001 + torch.rand((9, heads), generator=g)).numpy() for _ in range(2)]
+    q = torch.randn((sum(new), heads * group, dim), generator=g).to(torch.bfloat16)
+    args = ([codes, turned, *scales], q, [[4, 1, 3, 0], [2, 5, 8, 7]], lens, [0, new[0], sum(new)])
+    for a, b in zip(ref.attention(*args, window=window), ref.attention_of_long(*args, window=window)):
+        assert torch.allclose(a, b, rtol=1e-9, atol=0)

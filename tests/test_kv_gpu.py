@@ -2,6 +2,7 @@
 kv_reference.py: stored bytes, scales and rotated queries equal, attention
 within the error that its documented roundings allow."""
 
+import concurrent.futures
 import math
 
 import numpy as np
@@ -758,3 +759,113 @@ def test_query_rows_that_are_no_numbers(gpu_lib, dim, page, heads, group, new, r
     none[:starts[1]] = none[starts[2]:starts[3]] = True
     assert (got[none.to(DEV)] == 0).all() and (lse[none.to(DEV)] == -math.inf).all()
     assert torch.isnan(got[~none.to(DEV)]).all() and torch.isnan(lse[~none.to(DEV)]).all()
+
+
+# ------------------------------------------------- shares of many key tiles
+
+LONG = [6000, 2000, 4500, 3301]
+SHARES = [
+    # dim, page, heads, group, lens, new: totals of key tiles that make a share,
+    # or a chunk, of 8 to 60 tiles in each kernel, and prompts and single tokens in one call
+    (64, 16, 32, 1, LONG, None), (128, 64, 32, 2, LONG, None), (256, 128, 32, 1, LONG, None),
+    (64, 64, 32, 1, LONG, [24, 20, 29, 17]), (128, 64, 16, 1, LONG, [24, 31, 9, 28]), (256, 32, 16, 1, LONG, [44, 50, 9, 60]),
+    (64, 32, 32, 1, LONG, [48, 64, 33, 40]), (128, 64, 32, 1, LONG, [48, 64, 33, 40]),
+    (64, 64, 32, 1, LONG, [100, 128, 70, 129]), (128, 16, 32, 1, LONG, [100, 128, 70, 129]), (192, 64, 16, 1, LONG, [70, 1, 130, 66]),
+    (128, 64, 1, 8, [20001, 17], None), (128, 64, 2, 4, [20001], [400]), (128, 64, 2, 2, [1500, 900], [1500, 700]),
+    (256, 64, 1, 2, [1200], [1200]),
+    # a prompt among single tokens, by groups that choose each kernel
+    (128, 64, 2, 1, [700] + [40 + 31 * b for b in range(70)], [700] + [1] * 70),
+    (128, 64, 2, 2, [40 + 31 * b for b in range(70)] + [900], [1] * 70 + [700]),
+    (64, 16, 1, 4, [40 + 31 * b for b in range(35)] + [900] + [2000 - 31 * b for b in range(35)], [1] * 35 + [700] + [1] * 35),
+    (128, 32, 1, 8, [1300] + [40 + 31 * b for b in range(70)], [700] + [1] * 70),
+]
+
+
+@pytest.mark.parametrize("window", [0, 1111])
+@pytest.mark.parametrize("dim,page,heads,group,lens,new", SHARES)
+def test_every_key_counts_once(gpu_lib, dim, page, heads, group, lens, new, window):
+    """Queries of zero weigh all keys they see alike.  The sum of weights is
+    then their number, a sum of ones that fp32 holds exactly.  Its logarithm, up
+    to 9.91, errs by the hardware's log2 (an ulp below 16: 2^-20, times ln 2), the
+    product's rounding (2^-21) and that of ln 2 (9.91 * 2^-25): 1.5e-6, below
+    2^-19; one key too many or too few among 20001 changes it by 5e-5.  Channel
+    t % dim of a value is 1 in key tile t and 0 elsewhere, so that the output has
+    each tile's share, rounded once to BF16 (the weights are 1 exactly)."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(31)
+    one = new is None
+    n = [1] * len(lens) if one else new
+    starts = starts_of(n)
+    counts = [-(-x // page) for x in lens]
+    pages = sum(counts) + 1
+    cache = random_cache(fq, g, pages, heads, page, dim)
+    cache.v_scale.fill_(1.0)
+    table = tables(g, counts, max(counts), pages)
+    codes = torch.zeros((pages, dim, page), dtype=torch.uint8)
+    for b, x in enumerate(lens):
+        pos = torch.arange(x)
+        rows = torch.tensor(table[b][:counts[b]])
+        codes[rows[pos // page], (pos // 64) % dim, pos % page] = 0x38      # 1
+    cache.v.view(torch.uint8).copy_(codes.to(DEV)[:, None].expand(pages, heads, dim, page))
+    q = torch.zeros((starts[-1], heads * group, dim), dtype=torch.bfloat16, device=DEV)
+    got, lse = fq.kv_attention(cache, q, i32(table), i32(lens), None if one else i32(starts), window=window, return_lse=True)
+    torch.cuda.synchronize()
+    got, lse = got.cpu().double(), lse.cpu().double()
+    for b, x in enumerate(lens):
+        pos = torch.arange(x - n[b], x)[:, None]
+        key = torch.arange(x)[None, :]
+        seen = (key <= pos) & ((key > pos - window) if window else (key >= 0))
+        share = torch.zeros((n[b], dim), dtype=torch.float64).index_add_(1, (key[0] // 64) % dim, seen.double())
+        share /= seen.sum(1, keepdim=True)
+        mine = slice(starts[b], starts[b + 1])
+        assert ((lse[mine] - seen.sum(1, keepdim=True).double().log()).abs() <= 2.0 ** -19).all(), b
+        assert ((got[mine] - share[:, None]).abs() <= 1.001 * 2.0 ** -8 * share[:, None]).all(), b
+
+
+@pytest.mark.parametrize("dim,page,heads,group,lens,new", SHARES)
+def test_attention_over_many_key_tiles(gpu_lib, dim, page, heads, group, lens, new):
+    """Random keys and values against 64 bits at the same sizes."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(32)
+    one = new is None
+    starts = starts_of([1] * len(lens) if one else new)
+    counts = [-(-x // page) for x in lens]
+    cache = random_cache(fq, g, sum(counts) + 1, heads, page, dim, False)
+    table = tables(g, counts, max(counts), cache.num_pages)
+    q = torch.randn((starts[-1], heads * group, dim), generator=g).to(torch.bfloat16)
+    out, lse, tol, tol_lse = ref.attention_of_long(host(cache), q, table, lens, starts)
+    got, got_lse = fq.kv_attention(cache, q.to(DEV), i32(table), i32(lens), None if one else i32(starts), return_lse=True)
+    torch.cuda.synchronize()
+    off = (got.cpu().double() - out).abs()
+    assert (off <= tol).all(), float((off / tol).max())
+    off = (got_lse.cpu().double() - lse).abs()
+    assert (off <= tol_lse).all(), float((off / tol_lse).max())
+
+
+def test_threads_at_once(gpu_lib):
+    """Threads with a cache and a stream each append and attend at the same
+    time, and get what each gets alone."""
+    fq = gpu_lib
+    cos, sin = (torch.from_numpy(x).to(DEV) for x in rotation(64, 128))
+
+    def work(i, stream):
+        g = torch.Generator().manual_seed(40 + i)
+        with torch.cuda.stream(stream):
+            cache = fq.KvCache.empty(24, 2, 128, 16, device=DEV)
+            table = i32([r + [-1] * 80 for r in tables(g, [4] * 3, 4, 24)])
+            outs = []
+            for lens, new in (([20, 9, 1], [20, 9, 1]), ([21, 10, 2], None), ([30, 11, 9], [9, 1, 7]), ([31, 12, 10], None)) * 5:
+                starts = None if new is None else i32(starts_of(new))
+                T = 3 if new is None else sum(new)
+                qkv = torch.randn((T, 12 + 2 * i, 128), generator=g).to(torch.bfloat16).to(DEV)
+                q = fq.kv_append(cache, qkv[:, :2], qkv[:, 2:4], table, i32(lens), starts, q=qkv[:, 4:], cos=cos, sin=sin)
+                outs.append(fq.kv_attention(cache, q, table, i32(lens), starts))
+        stream.synchronize()
+        return [o.cpu() for o in outs], host(cache)
+
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    want = [work(i, streams[i]) for i in range(4)]
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        got = [f.result() for f in [pool.submit(work, i, streams[i]) for i in range(4)]]
+    for (a, ca), (b, cb) in zip(want, got):
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(a, b))
+        assert all(np.array_equal(x.view(np.uint8), y.view(np.uint8)) for x, y in zip(ca, cb))
