@@ -361,6 +361,11 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   const uint64_t out_bytes =
       kv_extent(q->tokens, q->out_token_stride, q->q_heads, q->out_head_stride, cache->head_dim);
   const uint64_t lse_bytes = q->lse ? 4 * static_cast<uint64_t>(q->tokens) * static_cast<uint64_t>(q->q_heads) : 0;
+  // Queries are still read while partial sums and finished rows are written.
+  const uint64_t q_bytes = kv_extent(q->tokens, q->q_token_stride, q->q_heads, q->q_head_stride, cache->head_dim);
+  if (overlap(q->q, q_bytes, q->lse, lse_bytes) || (s.bytes > 0 && overlap(q->q, q_bytes, workspace, s.bytes))) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
   if (!kv_apart(*cache, q->out, out_bytes) || !kv_apart(*cache, q->lse, lse_bytes) ||
       !kv_apart(*cache, workspace, s.bytes) || overlap(q->out, out_bytes, q->lse, lse_bytes) ||
       overlap(q->out, out_bytes, workspace, s.bytes) || overlap(q->lse, lse_bytes, workspace, s.bytes)) {

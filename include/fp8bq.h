@@ -500,9 +500,10 @@ size_t fp8bq_kv_attention_workspace_bytes(const fp8bq_kv_cache* cache, const fp8
  * and single tokens are served faster in calls of their own.
  * The launch depends on the shapes alone: captured in a graph, it follows
  * block_table, seq_lens and query_start as they change between replays.
- * out, lse and the workspace lie apart from each other and from the cache, and
- * out, if it is not q, from q (checked).  A v_scale below 2^-64 counts as 2^-64, and above 2^64 the fp32
- * sums may overflow.  Results do not depend on timing.  Returns an fp8bq_status.
+ * out, lse and the workspace lie apart from each other, from the cache and from
+ * q, except that out may be q (checked).  A v_scale below 2^-64 counts as 2^-64,
+ * and above 2^64 the fp32 sums may overflow.  Results do not depend on timing.
+ * Returns an fp8bq_status.
  */
 int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
                        const fp8bq_kv_query* query, void* workspace, size_t workspace_bytes,

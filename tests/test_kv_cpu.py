@@ -262,3 +262,25 @@ def test_reference_attention_of_long_is_the_same(dim, page, heads, group, lens, 
     args = ([codes, turned, *scales], q, [[4, 1, 3, 0], [2, 5, 8, 7]], lens, [0, new[0], sum(new)])
     for a, b in zip(ref.attention(*args, window=window), ref.attention_of_long(*args, window=window)):
         assert torch.allclose(a, b, rtol=1e-9, atol=0)
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [
+    dict(q=WS), dict(q=WS - ROWS + 16), dict(q=WS + 4096), dict(lse=A), dict(lse=A + ROWS - 4), dict(lse=A - 9 * 32 * 4 + 4),
+    dict(q=WS, out=WS),
+])
+def test_sums_and_workspace_over_the_queries(bad):
+    """Rows that finish early are written while others still read their queries."""
+    lib = fq.load_library()
+    need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
+    assert need > 4096
+    assert lib.fp8bq_kv_attention(cache(), batch(), query(**bad), WS, need, None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("good", [dict(q=WS - ROWS), dict(lse=A + ROWS), dict(lse=A - 9 * 32 * 4)])
+@on_a_thread
+def test_sums_and_workspace_beside_the_queries(good):
+    lib = fq.load_library()
+    need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
+    assert lib.fp8bq_kv_attention(cache(), batch(), query(**good), WS, need, None) not in (INVALID, WORKSPACE)
