@@ -110,6 +110,24 @@ bool kv_apart(const fp8bq_kv_cache& c, const void* p, uint64_t bytes) {
          !overlap(p, bytes, c.k_scale, 4 * blocks) && !overlap(p, bytes, c.v_scale, 4 * blocks);
 }
 
+// Whether a buffer that is written lies apart from the batch's arrays, which
+// workgroups read at any time.
+bool kv_apart(const fp8bq_kv_batch& b, const void* p, uint64_t bytes) {
+  const uint64_t n = static_cast<uint64_t>(b.count), width = static_cast<uint64_t>(b.max_pages);
+  const uint64_t table = width > 0 ? 4 * ((n - 1) * static_cast<uint64_t>(b.table_stride) + width) : 0;
+  const auto hits = [&](const void* at, uint64_t size) { return bytes > 0 && size > 0 && overlap(p, bytes, at, size); };
+  return !hits(b.block_table, table) && !hits(b.seq_lens, 4 * n) &&
+         !hits(b.query_start, b.query_start ? 4 * (n + 1) : 0);
+}
+
+// The same for all of a cache that is written.
+bool kv_apart(const fp8bq_kv_batch& b, const fp8bq_kv_cache& c) {
+  const uint64_t blocks = static_cast<uint64_t>(c.num_pages) * static_cast<uint64_t>(c.kv_heads);
+  const uint64_t codes = blocks * static_cast<uint64_t>(c.page_size) * static_cast<uint64_t>(c.head_dim);
+  return kv_apart(b, c.k, codes) && kv_apart(b, c.v, codes) && kv_apart(b, c.k_scale, 4 * blocks) &&
+         kv_apart(b, c.v_scale, 4 * blocks);
+}
+
 fp8bq::KvCache kv_device(const fp8bq_kv_cache& c) {
   fp8bq::KvCache d;
   d.k = static_cast<uint8_t*>(c.k);
@@ -263,6 +281,11 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   const int32_t dim = cache->head_dim;
+  if (!kv_apart(*batch, *cache) ||
+      (t->q && !kv_apart(*batch, t->q_out,
+                         kv_extent(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, dim)))) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
   if (!kv_apart(*cache, t->k, kv_extent(t->tokens, t->k_token_stride, cache->kv_heads, t->k_head_stride, dim)) ||
       !kv_apart(*cache, t->v, kv_extent(t->tokens, t->v_token_stride, cache->kv_heads, t->v_head_stride, dim)) ||
       (t->q && !kv_apart(*cache, t->q_out,
@@ -369,6 +392,10 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   if (!kv_apart(*cache, q->out, out_bytes) || !kv_apart(*cache, q->lse, lse_bytes) ||
       !kv_apart(*cache, workspace, s.bytes) || overlap(q->out, out_bytes, q->lse, lse_bytes) ||
       overlap(q->out, out_bytes, workspace, s.bytes) || overlap(q->lse, lse_bytes, workspace, s.bytes)) {
+    return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (!kv_apart(*batch, q->out, out_bytes) || !kv_apart(*batch, q->lse, lse_bytes) ||
+      !kv_apart(*batch, workspace, s.bytes)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   const int rc = device_check();

@@ -284,3 +284,39 @@ def test_sums_and_workspace_beside_the_queries(good):
     lib = fq.load_library()
     need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
     assert lib.fp8bq_kv_attention(cache(), batch(), query(**good), WS, need, None) not in (INVALID, WORKSPACE)
+
+
+LENGTHS, TABLE = 4 * 4, 4 * 4 * 40   # bytes of the batch's arrays (the offsets are one longer than the lengths)
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [
+    dict(table=B), dict(table=B - TABLE + 4), dict(lens=B + ROWS - 4), dict(lens=B - LENGTHS + 4), dict(starts=B - LENGTHS),
+    dict(table=SI), dict(lens=SI + 64), dict(starts=SI + 9 * 32 * 4 - 4), dict(table=WS), dict(lens=WS + 400), dict(starts=WS),
+])
+def test_attention_over_the_arrays_it_reads(bad):
+    lib = fq.load_library()
+    need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
+    assert lib.fp8bq_kv_attention(cache(), batch(**bad), query(lse=SI), WS, need, None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [
+    dict(table=D), dict(lens=D + ROWS - 4), dict(starts=D - LENGTHS), dict(table=K + 4096), dict(lens=V + 64),
+    dict(starts=KS), dict(table=VS - TABLE + 4), dict(lens=K - 4), dict(starts=VS + 100 * 8 * 4 - 4),
+])
+def test_append_over_the_arrays_it_reads(bad):
+    assert fq.load_library().fp8bq_kv_append(cache(), batch(**bad), tokens(), None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("good", [
+    dict(table=B - TABLE), dict(lens=B + ROWS), dict(starts=D - LENGTHS - 4), dict(lens=KS - LENGTHS), dict(starts=VS + 100 * 8 * 4),
+    dict(table=K + 100 * 8 * 64 * 128), dict(table=0, width=0),
+])
+@on_a_thread
+def test_arrays_beside_what_is_written(good):
+    lib = fq.load_library()
+    assert lib.fp8bq_kv_append(cache(), batch(**good), tokens(), None) != INVALID
+    need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
+    assert lib.fp8bq_kv_attention(cache(), batch(**good), query(lse=SI), WS, need, None) not in (INVALID, WORKSPACE)
