@@ -288,8 +288,9 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
   }
   if (!kv_apart(*cache, t->k, kv_extent(t->tokens, t->k_token_stride, cache->kv_heads, t->k_head_stride, dim)) ||
       !kv_apart(*cache, t->v, kv_extent(t->tokens, t->v_token_stride, cache->kv_heads, t->v_head_stride, dim)) ||
-      (t->q && !kv_apart(*cache, t->q_out,
-                         kv_extent(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, dim)))) {
+      (t->q && (!kv_apart(*cache, t->q, kv_extent(t->tokens, t->q_token_stride, t->q_heads, t->q_head_stride, dim)) ||
+                !kv_apart(*cache, t->q_out,
+                          kv_extent(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, dim))))) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
   }
   if (t->q) {
@@ -303,6 +304,17 @@ int fp8bq_kv_append(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch, co
   if (t->rot_dim > 0 && (!t->cos || !t->sin || !kv_aligned(t->cos, 16) || !kv_aligned(t->sin, 16) ||
                          t->positions < 0)) {
     return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
+  if (t->rot_dim > 0 && t->positions > 0) {
+    // saturated: no buffer is that long
+    const uint64_t rows = static_cast<uint64_t>(t->positions < (int64_t{1} << 48) ? t->positions : int64_t{1} << 48);
+    const uint64_t turns = rows * static_cast<uint64_t>(t->rot_dim) * 2;
+    const uint64_t written = t->q ? kv_extent(t->tokens, t->q_out_token_stride, t->q_heads, t->q_out_head_stride, dim) : 0;
+    for (const float* at : {t->cos, t->sin}) {
+      if (!kv_apart(*cache, at, turns) || (t->q && overlap(t->q_out, written, at, turns))) {
+        return FP8BQ_ERR_INVALID_ARGUMENT;
+      }
+    }
   }
   const int rc = device_check();
   if (rc != FP8BQ_OK) return rc;

@@ -448,9 +448,10 @@ typedef struct fp8bq_kv_tokens {
  * A power of two, unlike the amax / 448 of weights, lets a page's scale grow
  * without rounding the earlier codes again (other than below e4m3's smallest
  * normal value).  Slots behind the new tokens keep their bytes.  Values must
- * be finite: a block with others gets unspecified codes.  The inputs and q_out
- * lie apart from the cache, q_out apart from k and v and, if it is not q, from
- * q (checked; slices of one tensor, token by token or head by head, are apart).
+ * be finite: a block with others gets unspecified codes.  The inputs, cos and
+ * sin among them, and q_out lie apart from the cache, q_out apart from k, v, cos
+ * and sin and, if it is not q, from q (checked; slices of one tensor, token by
+ * token or head by head, are apart).
  * A page may belong to several sequences, but a call stores into it for one of
  * them, and in one place of its table, only.  Tokens at negative positions and
  * at positions without a row of cos and sin leave their row of q_out as it was.

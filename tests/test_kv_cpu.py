@@ -320,3 +320,26 @@ def test_arrays_beside_what_is_written(good):
     assert lib.fp8bq_kv_append(cache(), batch(**good), tokens(), None) != INVALID
     need = lib.fp8bq_kv_attention_workspace_bytes(cache(), batch(), 32, 9)
     assert lib.fp8bq_kv_attention(cache(), batch(**good), query(lse=SI), WS, need, None) not in (INVALID, WORKSPACE)
+
+
+TURNS = 4096 * 64 * 4   # bytes of 4096 rows of cos or sin
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", [
+    dict(q=K + 4096), dict(q=V - 128), dict(q=KS), dict(q=VS - ROWS + 16),
+    dict(cos=K), dict(sin=V + 4096), dict(cos=KS - TURNS + 16), dict(sin=VS + 16), dict(cos=D), dict(sin=D + ROWS - 16),
+    dict(cos=D - TURNS + 16), dict(cos=D - 64, positions=1 << 62), dict(q=CO, q_out=CO),
+])
+def test_append_over_its_inputs(bad):
+    assert fq.load_library().fp8bq_kv_append(cache(), batch(), tokens(**bad), None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("good", [
+    dict(q=K - ROWS), dict(q=KS + 100 * 8 * 4), dict(cos=K - TURNS), dict(sin=D + ROWS), dict(cos=D - TURNS),
+    dict(cos=K, sin=V, rot=0), dict(cos=K, sin=D, positions=0), dict(q=0, q_out=0, cos=D), dict(cos=K - TURNS // 2, rot=64),
+])
+@on_a_thread
+def test_append_beside_its_inputs(good):
+    assert fq.load_library().fp8bq_kv_append(cache(), batch(), tokens(**good), None) != INVALID
