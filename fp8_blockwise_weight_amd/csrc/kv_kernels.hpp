@@ -62,6 +62,12 @@ struct KvTokens {
   int32_t interleaved;
 };
 
+// Positions stay below 2^31 - 1024, so that a tile's end is in 32 bits; a
+// whole number of pages of any size.
+__device__ __forceinline__ int32_t kv_capacity(const KvBatch& bt, int32_t log_s) {
+  return (int32_t)min((int64_t)bt.max_pages << log_s, (int64_t)INT32_MAX - 1023);
+}
+
 // ------------------------------------------------------------------ append
 //
 // s = the smallest power of two with 448 s >= max|x| (448 = 1.75 * 2^8), not
@@ -142,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_step(KvCache c, KvBatch bt
   const int32_t pos = max(bt.lens[b], 0) - 1;
   if (pos < 0 || (t.half > 0 && pos >= t.positions)) return;
   const int32_t S = 1 << c.log_s, slot = pos & (S - 1), j = pos >> c.log_s;
-  const int32_t page = j < bt.max_pages ? bt.table[(int64_t)b * bt.stride + j] : -1;
+  const int32_t page = pos < kv_capacity(bt, c.log_s) ? bt.table[(int64_t)b * bt.stride + j] : -1;
   const bool stored = page >= 0 && page < c.pages;
 
   float kx[kP], ky[kP], cs[kP], sn[kP];
@@ -362,7 +368,7 @@ __global__ __launch_bounds__(kThreads, 3) void kv_append_pages(KvCache c, KvBatc
   int64_t hi = min(len, (j + 1) << c.log_s);
   if (t.half > 0) hi = min(hi, t.positions);
   if (lo >= hi) return;
-  const int32_t page = j < bt.max_pages ? bt.table[(int64_t)b * bt.stride + j] : -1;
+  const int32_t page = lo < kv_capacity(bt, c.log_s) ? bt.table[(int64_t)b * bt.stride + j] : -1;
   const bool stored = page >= 0 && page < c.pages;
   const int32_t held = (int32_t)(lo - (j << c.log_s));   // earlier tokens in the page
   const int32_t count = (int32_t)(hi - lo);
@@ -617,11 +623,6 @@ __device__ __forceinline__ T wave_scan(T v) {
 __device__ __forceinline__ int32_t lane_of(int32_t v, int32_t lane) { return __builtin_amdgcn_readlane(v, lane); }
 __device__ __forceinline__ int64_t lane_of(int64_t v, int32_t lane) {
   return (int64_t)(((uint64_t)(uint32_t)lane_of((int32_t)(v >> 32), lane) << 32) | (uint32_t)lane_of((int32_t)v, lane));
-}
-
-// Positions stay below 2^31 - 1024, so that a tile's end is in 32 bits.
-__device__ __forceinline__ int32_t kv_capacity(const KvBatch& bt, int32_t log_s) {
-  return (int32_t)min((int64_t)bt.max_pages << log_s, (int64_t)INT32_MAX - 1023);
 }
 
 // The first position that a query at pos - 1 sees.

@@ -396,8 +396,8 @@ typedef struct fp8bq_kv_cache {
  * These arrays live on the device and are not checked by the host.  The
  * kernels read and write nothing outside the buffers whatever they hold:
  * tokens whose page number is not in 0 .. num_pages - 1, or whose position is
- * negative, beyond max_pages pages or above 2^31 - 1024, are neither stored nor
- * seen, and query_start is clamped to 0 .. tokens.  Rows of no sequence are left
+ * negative, beyond max_pages pages or not below 2^31 - 1024, are neither stored
+ * nor seen, and query_start is clamped to 0 .. tokens.  Rows of no sequence are left
  * as they are.  What a call writes lies apart from these arrays (checked).
  */
 typedef struct fp8bq_kv_batch {

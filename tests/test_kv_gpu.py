@@ -224,6 +224,35 @@ def test_append_leaves_out_what_has_no_place(gpu_lib, single):
     assert torch.equal(got.cpu().view(torch.int16), q_want.view(torch.int16))
 
 
+@pytest.mark.parametrize("single", [True, False])
+def test_positions_that_attention_does_not_see_are_not_stored(gpu_lib, single):
+    """The last positions below 2^31 - 1024 are stored, those from there on are
+    not, though the table has pages for them; their queries are rotated all the
+    same (here by nothing)."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(23)
+    S, D, limit = 256, 64, (1 << 31) - 1024
+    lens = [limit, limit + 1, (1 << 31) - 1] if single else [limit + 2, limit + 300, (1 << 31) - 1]
+    new = [1, 1, 1] if single else [4, 301, 9]
+    starts = starts_of(new)
+    cache = random_cache(fq, g, 12, 1, S, D)
+    want = host(cache)
+    table = torch.full((3, 1 << 23), -1, dtype=torch.int32, device=DEV)
+    for b in range(3):
+        table[b, -5:-1] = i32([4 * b, 4 * b + 1, 4 * b + 2, 4 * b + 3])
+    table[2, -1] = 11
+    near = [[-1] * 3 + [4 * b] for b in range(3)]    # the same slots of short sequences
+    _, q, k, v = append_inputs(g, starts[-1], 1, 2, D)
+    keep = [(b, r) for b in range(3) for r in range(new[b]) if lens[b] - new[b] + r < limit]
+    if keep:
+        kept = [starts[b] + r for b, r in keep]
+        counts = [sum(1 for x, _ in keep if x == b) for b in range(3)]
+        ref.append(want, k[kept], v[kept], near, [4 * S if c else 0 for c in counts], starts_of(counts))
+    got = fq.kv_append(cache, k.to(DEV), v.to(DEV), table, i32(lens), None if single else i32(starts), q=q.to(DEV))
+    torch.cuda.synchronize()
+    same_cache(cache, want)
+    assert torch.equal(got.cpu().view(torch.int16), q.contiguous().view(torch.int16))
+
+
 # -------------------------------------------------------------- attention
 
 def check_attention(fq, cache, q, table, lens, starts, one, **kw):
