@@ -22,7 +22,8 @@ _QUERY = struct.Struct("=QQQ5qiifi")       # fp8bq_kv_query
 
 
 class KvCache:
-    """The buffers of a paged cache, checked once.
+    """The buffers of a paged cache, checked once; other buffers are another
+    ``KvCache`` (the attributes are read-only).
 
     ``k`` is float8_e4m3fn [pages, kv_heads, page_size, head_dim], ``v``
     float8_e4m3fn [pages, kv_heads, head_dim, page_size] (a channel's tokens
@@ -64,11 +65,19 @@ class KvCache:
                 raise TypeError("the cache must be on a GPU (there is no CPU implementation)")
             if t.device != k.device:
                 raise ValueError("the cache's buffers must be on one device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, dim
-        self.device, self._index = k.device, k.get_device()
-        self._packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                   pages, size, heads, dim, 0)
+        packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                             pages, size, heads, dim, 0)
+        for name, value in zip(self.__slots__, (k, v, k_scale, v_scale, pages, size, heads, dim, k.device,
+                                                k.get_device(), packed)):
+            object.__setattr__(self, name, value)
+
+    # Calls go by the addresses taken above: another tensor put in a buffer's
+    # place would change nothing that they read, and free what they do.
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KvCache.{name} is read-only")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"KvCache.{name} is read-only")
 
     @classmethod
     def empty(cls, num_pages, kv_heads, head_dim, page_size=64, device="cuda"):

@@ -343,3 +343,15 @@ def test_append_over_its_inputs(bad):
 @on_a_thread
 def test_append_beside_its_inputs(good):
     assert fq.load_library().fp8bq_kv_append(cache(), batch(), tokens(**good), None) != INVALID
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "num_pages", "page_size", "kv_heads", "head_dim", "device"])
+def test_a_cache_keeps_its_buffers(name):
+    """Calls go by the addresses that the constructor took."""
+    held = object.__new__(fq.KvCache)
+    object.__setattr__(held, name, 1)
+    with pytest.raises(AttributeError, match="read-only"):
+        setattr(held, name, 2)
+    with pytest.raises(AttributeError, match="read-only"):
+        delattr(held, name)
+    assert getattr(held, name) == 1

@@ -898,3 +898,15 @@ def test_threads_at_once(gpu_lib):
     for (a, ca), (b, cb) in zip(want, got):
         assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(a, b))
         assert all(np.array_equal(x.view(np.uint8), y.view(np.uint8)) for x, y in zip(ca, cb))
+
+
+def test_a_cache_keeps_its_buffers(gpu_lib):
+    fq, g = gpu_lib, torch.Generator().manual_seed(18)
+    cache, other = (random_cache(fq, g, 4, 2, 16, 64) for _ in range(2))
+    k, packed = cache.k, cache._packed
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError, match="read-only"):
+            setattr(cache, name, getattr(other, name))
+    assert cache.k is k and cache._packed == packed
+    assert (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim) == (4, 2, 16, 64)
+    assert cache.device == cache.k.device
