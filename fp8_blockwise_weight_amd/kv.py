@@ -79,6 +79,10 @@ class KvCache:
     def __delattr__(self, name):
         raise AttributeError(f"KvCache.{name} is read-only")
 
+    # A copy, or one loaded from a file, takes its own buffers' addresses.
+    def __reduce__(self):
+        return KvCache, (self.k, self.v, self.k_scale, self.v_scale)
+
     @classmethod
     def empty(cls, num_pages, kv_heads, head_dim, page_size=64, device="cuda"):
         """A cache of ``num_pages`` zeroed pages."""

@@ -355,3 +355,12 @@ def test_a_cache_keeps_its_buffers(name):
     with pytest.raises(AttributeError, match="read-only"):
         delattr(held, name)
     assert getattr(held, name) == 1
+
+
+def test_a_copied_cache_is_made_anew():
+    """From its buffers alone: no address goes along."""
+    held = object.__new__(fq.KvCache)
+    for i, name in enumerate(fq.KvCache.__slots__):
+        object.__setattr__(held, name, i)
+    for protocol in (2, 4):
+        assert held.__reduce_ex__(protocol) == (fq.KvCache, (0, 1, 2, 3))

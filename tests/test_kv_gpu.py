@@ -3,6 +3,8 @@ kv_reference.py: stored bytes, scales and rotated queries equal, attention
 within the error that its documented roundings allow."""
 
 import concurrent.futures
+import copy
+import io
 import math
 
 import numpy as np
@@ -910,3 +912,25 @@ def test_a_cache_keeps_its_buffers(gpu_lib):
     assert cache.k is k and cache._packed == packed
     assert (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim) == (4, 2, 16, 64)
     assert cache.device == cache.k.device
+
+
+def test_a_copied_cache_has_its_own_buffers(gpu_lib):
+    """Appends to a deep copy, or to a cache that was saved and loaded, reach
+    the copy; a shallow copy shares the buffers."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(19)
+    cache = random_cache(fq, g, 4, 2, 16, 64)
+    x = torch.randn((1, 2, 64), generator=g).to(torch.bfloat16).to(DEV)
+    before = host(cache)
+    after = host(cache)
+    ref.append(after, x.cpu(), x.cpu(), [[3]], [5], [0, 1])
+    saved = io.BytesIO()
+    torch.save(cache, saved)
+    saved.seek(0)
+    for again in (copy.deepcopy(cache), torch.load(saved, weights_only=False)):
+        fq.kv_append(again, x, x, i32([[3]]), i32([5]))
+        torch.cuda.synchronize()
+        same_cache(cache, before)
+        same_cache(again, after)
+    fq.kv_append(copy.copy(cache), x, x, i32([[3]]), i32([5]))
+    torch.cuda.synchronize()
+    same_cache(cache, after)
