@@ -168,7 +168,9 @@ constexpr int64_t kKvFew = 8, kKvWhole = 16, kKvWholeOfMany = 32;
 //   up to 16   kv_attend_rows<16>: 16 rows 55.0 us, with <32> 56.6 (128
 //              sequences: 339 against 361; half the registers go unused)
 //   17 to 32   kv_attend_rows<32>: 24 rows 57.5, in tiles of 64 rows 64.2
-//              (256 channels: 102 against 222)
+//              (256 channels: 102 against 222); not so for few long sequences
+//              (2 of 40000, 32 rows: 34.7 against 29.0), which the rule, that
+//              goes by rows, does not tell apart
 //   33 to 64   tiles of 64 rows: 64 rows 75, in tiles of 128 rows 94; above 128
 //              channels, whose registers leave one wave per SIMD, twice
 //              kv_attend_rows<32>: 64 rows of 256 channels 172, in tiles of 128

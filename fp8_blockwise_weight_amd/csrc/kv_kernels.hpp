@@ -136,8 +136,18 @@ __device__ __forceinline__ uint16_t bf16_down(float v) {
 }
 
 // One token for every sequence: a wave for each (sequence, key/value head),
-// lanes over channel pairs.  There is nothing to reuse: the time is the chain
-// of dependent loads (length -> page -> scale) and the launch.
+// lanes over channel pairs.  There is nothing to reuse.  One sequence, 32 + 8 +
+// 8 heads of 128, takes the chain of dependent loads (length -> page -> scale)
+// and the launch, 4 us.  256 sequences take 8.3 in pages of 64; 6.6 in pages
+// of 16, where the channels' bytes of v share cache lines, and 7.6 without
+// queries, which are loaded and stored in turn behind the keys.
+//
+// That is without growth.  A page that grows is recoded by its one wave, a
+// round trip to memory after another: the last slot of a page of 64 tokens of
+// 128 channels 18 us (47 where all 2048 blocks grow at once), of 256 tokens of
+// 256 channels 71 (267).  Some page grows in most steps of a large batch: the
+// 256 sequences with new random tokens at each step take 19 us, 11 of equal
+// magnitudes, which let no page grow (pages of 16: 15 and 9).
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv_append_step(KvCache c, KvBatch bt, KvTokens t) {
   constexpr int kP = (D / 2 + 63) / 64;   // pairs of a lane
@@ -1181,19 +1191,23 @@ __device__ __forceinline__ float half_max(float v) {
 // one column, fall on different banks: with row / 2 for rows of 128 bytes and
 // row / 4 for rows of 64, conflicts went from 37% of LDS's cycles to none.
 //
-// VALU work per score bounds this kernel (the exponential at a quarter rate,
-// and the widening of codes), so what can be is kept out of the inner loop:
-// k's scale and the softmax scale are one factor per 16 tokens inside the
+// Neither matrix units nor VALU are busy throughout: a wave's products, softmax
+// and products follow one another, and overlap only with the other phases of
+// the SIMD's other wave, as chance has it.  VALU work per score (the
+// exponential at a quarter rate, and the widening of codes) is the smaller part
+// of the distance to the matrix rate (below), but what can be is kept out of
+// the inner loop: k's scale and the softmax scale are one factor per 16 tokens inside the
 // fused multiply-add in front of the exponential; v's scale enters there too,
 // as its logarithm; sums and maxima are only rescaled when a row's maximum
 // has grown by more than 2^8; and a page that holds a whole tile (kOne) makes
 // its addresses and scales uniform (307 -> 294 us).
 //
-// Two prompts of 4096, 32 heads over 8 of 128: 294 us, 934 TFLOP/s of the
-// 1360 of a large matrix product; 500 tokens over 32768: 293 us with the join.
+// Two prompts of 4096, 32 heads over 8 of 128: 295 to 307 us on different
+// cards, 895 to 934 TFLOP/s of the 1360 of a large matrix product (202 us);
+// 500 tokens over 32768: 293 to 300 us with the join.
 // Matrix units busy 40% of the cycles, VALU issue 64%, waits 21% of a wave's
-// time; without any exponential and widening it would be 285 us of the 311
-// that it then took.  64 rows a wave, to widen half as often, spills (586 us).
+// time; a copy without any exponential and widening took 285 us where this one
+// took 311: 26 us of the 109 above the matrix rate.  64 rows a wave, to widen half as often, spills (586 us).
 template <int D, int W, bool kOne>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCache c, KvBatch bt, KvQuery p) {
   constexpr int R = 32 * W, kN = 64 * W;
@@ -1534,7 +1548,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void kv_attend_tiles(KvCa
 // second is `jump` + 1 behind the first, the others follow it).  N waves share a row, each taking every Nth partial, all in
 // flight at once: with few rows of many splits, as one long sequence has, one
 // wave per row would add up its partials one round trip after another.
-// Latency alone: 5 us for 32 rows of some 60 partials, 8 for 4608 rows.
+// Latency alone: 5 us for 32 rows of some 60 partials, 8 for 4608 rows, 12 for
+// 16000.
 template <int D, int N>
 __global__ __launch_bounds__(N == 1 ? 256 : 64 * N) void kv_attend_join(KvBatch bt, KvQuery p, int32_t heads,
                                                                         int32_t R) {

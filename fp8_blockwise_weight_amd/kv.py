@@ -191,6 +191,9 @@ def kv_append(cache, k, v, block_table, seq_lens, query_start=None, *, q=None, q
 
     Returns the rotated queries where ``q`` (BF16 [tokens, q_heads, head_dim])
     is given, in ``q_out`` (which may be ``q``) or a new tensor, else None.
+    Rows of no sequence (padding before ``query_start[0]`` or from
+    ``query_start[-1]`` on) and of tokens that are left out are not written:
+    what ``q_out`` held stays there, and a new tensor holds anything.
     """
     import torch
 
@@ -254,9 +257,13 @@ def kv_attention(cache, q, block_table, seq_lens, query_start=None, *, scale=Non
 
     Arguments as in ``kv_append``.  A query sees the tokens up to its own
     position, with ``window`` no more than that many of them; one that sees
-    none gets zeros.  ``scale`` defaults to head_dim ** -0.5.  Returns ``out``
+    none gets zeros, one that sees some and holds a NaN or an infinity gets NaN.
+    ``scale`` defaults to head_dim ** -0.5.  Returns ``out``
     (BF16, like q), and with ``return_lse`` also the logarithm of each row's
     sum of exponentials (float32 [tokens, q_heads]; ``lse`` may supply it).
+    Rows of no sequence (padding before ``query_start[0]`` or from
+    ``query_start[-1]`` on) are not written: what ``out`` and ``lse`` held stays
+    there, and new tensors hold anything.
     The kernel is chosen by the mean number of query tokens, so that prompts
     and single tokens are served faster in calls of their own (128 tokens over
     8192 each and a prompt of 2048: 337 + 58 us, in one call 553).  Nothing here

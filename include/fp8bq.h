@@ -397,8 +397,8 @@ typedef struct fp8bq_kv_cache {
  * kernels read and write nothing outside the buffers whatever they hold:
  * tokens whose page number is not in 0 .. num_pages - 1, or whose position is
  * negative, beyond max_pages pages or not below 2^31 - 1024, are neither stored
- * nor seen, and query_start is clamped to 0 .. tokens.  Rows of no sequence are left
- * as they are.  What a call writes lies apart from these arrays (checked).
+ * nor seen, and query_start is clamped to 0 .. tokens.  Rows of no sequence are
+ * left as they are.  What a call writes lies apart from these arrays (checked).
  */
 typedef struct fp8bq_kv_batch {
   const int32_t* block_table;  /* [count, max_pages], rows table_stride apart */
