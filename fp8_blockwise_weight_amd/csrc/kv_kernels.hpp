@@ -1204,7 +1204,7 @@ __device__ __forceinline__ float half_max(float v) {
 //
 // Two prompts of 4096, 32 heads over 8 of 128: 295 to 307 us on different
 // cards, 895 to 934 TFLOP/s of the 1360 of a large matrix product (202 us);
-// 500 tokens over 32768: 293 to 300 us with the join.
+// 500 tokens over 32768: 293 to 305 us with the join.
 // Matrix units busy 40% of the cycles, VALU issue 64%, waits 21% of a wave's
 // time; a copy without any exponential and widening took 285 us where this one
 // took 311: 26 us of the 109 above the matrix rate.  64 rows a wave, to widen half as often, spills (586 us).

@@ -747,15 +747,15 @@ FORMS = [
 ]
 
 
-@pytest.mark.parametrize("room", [0, 1300])
+@pytest.mark.parametrize("split", [False, True])
 @pytest.mark.parametrize("dim,page,heads,group,new", FORMS)
-def test_query_rows_that_are_no_numbers(gpu_lib, dim, page, heads, group, new, room):
+def test_query_rows_that_are_no_numbers(gpu_lib, dim, page, heads, group, new, split):
     """A row of queries with a NaN or an infinity is NaN, and so is its sum, if
     it sees a token: not the zeros of a row that sees none.  Its neighbours are
     as without it.  Keys are positive in channel 0, so that an infinity of
     either sign there makes all of its row's scores infinite alike."""
     fq, g = gpu_lib, torch.Generator().manual_seed(dim + page)
-    lens = [1300, 700, 130, 1]
+    lens = [1300, 700, 130, 1] if split else [250, 130, 70, 1]
     n = [1] * 4 if new is None else new
     starts = starts_of(n)
     counts = [-(-x // page) for x in lens]
@@ -763,10 +763,11 @@ def test_query_rows_that_are_no_numbers(gpu_lib, dim, page, heads, group, new, r
     first = cache.k.view(torch.uint8)[..., 0]
     first &= 0x7F
     first[first == 0] = 0x38
-    width = -(-room // page) if room else 0
-    table = i32([r + [-1] * width for r in tables(g, counts, max(counts), cache.num_pages)])
+    room = 1300 // page if split else 0
+    table = i32([r + [-1] * room for r in tables(g, counts, max(counts), cache.num_pages)])
     q = torch.randn((starts[-1], heads * group, dim), generator=g).to(torch.bfloat16).to(DEV)
     st = None if new is None else i32(starts)
+    assert (fq.kv_attention_workspace_bytes(cache, q, table) > 0) == split
     want, want_lse = fq.kv_attention(cache, q, table, i32(lens), st, return_lse=True)
     marks = [(0, 0, 3, math.nan), (0, heads * group - 1, 0, math.inf), (1, 0, 0, -math.inf), (1, heads, 0, math.inf),
              (2, 1, dim - 1, math.nan), (3, 0, 0, -math.inf), (3, heads * group - 1, 5, math.nan)]
@@ -784,7 +785,7 @@ def test_query_rows_that_are_no_numbers(gpu_lib, dim, page, heads, group, new, r
     assert torch.equal(lse[~bad], want_lse[~bad])
     # rows that see nothing are zero whatever they hold
     x[:] = math.nan
-    got, lse = fq.kv_attention(cache, x, table, i32([0, 700, -5, 1]), st, return_lse=True)
+    got, lse = fq.kv_attention(cache, x, table, i32([0, lens[1], -5, 1]), st, return_lse=True)
     torch.cuda.synchronize()
     none = torch.zeros(starts[-1], dtype=torch.bool)
     none[:starts[1]] = none[starts[2]:starts[3]] = True
