@@ -52,6 +52,13 @@ EXPORTS = (
     "fp8bq_kv_append",
     "fp8bq_kv_attention",
     "fp8bq_kv_attention_workspace_bytes",
+    "fp8bq_latent_append",
+    "fp8bq_latent_attention",
+    "fp8bq_latent_attention_workspace_bytes",
+    "fp8bq_latent_prompt_attention",
+    "fp8bq_cache_fork",
+    "fp8bq_cache_compact",
+    "fp8bq_cache_compact_workspace_bytes",
     "fp8bq_set_resident_wait_us",
     "fp8bq_status_string",
     "fp8bq_last_hip_error",
@@ -165,6 +172,23 @@ def load_library() -> ctypes.CDLL:
     lib.fp8bq_kv_attention.restype = ctypes.c_int
     lib.fp8bq_kv_attention_workspace_bytes.argtypes = [c_vp, c_vp, c_i32, c_i64]
     lib.fp8bq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+    # structs packed by latent.py
+    lib.fp8bq_latent_append.argtypes = [c_vp, c_vp, c_vp, c_vp]
+    lib.fp8bq_latent_append.restype = ctypes.c_int
+    lib.fp8bq_latent_attention.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]
+    lib.fp8bq_latent_attention.restype = ctypes.c_int
+    lib.fp8bq_latent_attention_workspace_bytes.argtypes = [c_vp, c_vp, c_i32, c_i64]
+    lib.fp8bq_latent_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.fp8bq_latent_prompt_attention.argtypes = [c_vp, c_vp]
+    lib.fp8bq_latent_prompt_attention.restype = ctypes.c_int
+    # structs packed by pages.py
+    lib.fp8bq_cache_fork.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp]
+    lib.fp8bq_cache_fork.restype = ctypes.c_int
+    lib.fp8bq_cache_compact.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_vp,
+                                        ctypes.c_size_t, c_vp]
+    lib.fp8bq_cache_compact.restype = ctypes.c_int
+    lib.fp8bq_cache_compact_workspace_bytes.argtypes = [c_i64]
+    lib.fp8bq_cache_compact_workspace_bytes.restype = ctypes.c_size_t
     lib.fp8bq_encode_e4m3.argtypes = [c_vp, c_vp, c_i64, c_vp]
     lib.fp8bq_encode_e4m3.restype = ctypes.c_int
     lib.fp8bq_set_resident_wait_us.argtypes = [c_i64]
@@ -771,9 +795,14 @@ def encode_e4m3(y):
 
 
 from .kv import KvCache, kv_append, kv_attention, kv_attention_workspace_bytes  # noqa: E402
+from .latent import (LatentCache, latent_append, latent_attention,  # noqa: E402
+                     latent_attention_workspace_bytes, latent_prompt_attention)
+from .pages import cache_compact, cache_compact_workspace_bytes, cache_fork  # noqa: E402
 
 __all__ = [
     "KvCache", "kv_append", "kv_attention", "kv_attention_workspace_bytes",
+    "LatentCache", "latent_append", "latent_attention", "latent_attention_workspace_bytes",
+    "latent_prompt_attention", "cache_fork", "cache_compact", "cache_compact_workspace_bytes",
     "DqEntry", "EXPORTS", "Fp8bqError", "TensorEntry", "block_shape", "dequantize",
     "dequantize_many", "encode_e4m3",
     "load_library", "local_grid", "quantize_with_amax", "quantize_with_amax_many", "tile_amax",

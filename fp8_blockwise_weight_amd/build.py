@@ -28,10 +28,12 @@ ROOT = os.path.dirname(HERE)
 # One translation unit, which includes the others.
 SRC = os.path.join(HERE, "csrc", "lib.hip")
 # The weight quantizers (what the committed counter profiles are keyed on),
-# and the key/value cache beside them.
+# and the caches beside them.
 KERNEL_SOURCES = [os.path.join(HERE, "csrc", "kernels.hpp"), os.path.join(HERE, "csrc", "fp8bq.hip"),
                   os.path.join(HERE, "csrc", "div31.hpp")]
-KV_SOURCES = [SRC, os.path.join(HERE, "csrc", "kv.hip"), os.path.join(HERE, "csrc", "kv_kernels.hpp")]
+KV_SOURCES = [SRC] + [os.path.join(HERE, "csrc", name) for name in
+                      ("kv.hip", "kv_kernels.hpp", "latent.hip", "latent_kernels.hpp",
+                       "prompt_kernels.hpp", "pages.hip", "pages_kernels.hpp")]
 DEPS = KERNEL_SOURCES + KV_SOURCES + [os.path.join(ROOT, "include", "fp8bq.h")]
 LIB = os.path.join(HERE, "libfp8bq.so")
 ARCH = "gfx950"

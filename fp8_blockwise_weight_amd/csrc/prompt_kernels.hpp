@@ -1,0 +1,207 @@
+// Device code of attention in the expanded form (gfx950): every head has keys
+// and values of its own, and one rotated key, which the heads share.
+#pragma once
+
+#include "latent_kernels.hpp"
+
+namespace fp8bq {
+
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+
+struct PromptQuery {
+  const uint16_t* q;       // BF16 [tokens, heads, D + 64]
+  const uint16_t* k;       // BF16 [keys, heads, D]
+  const uint16_t* r;       // BF16 [keys, 64]
+  const uint16_t* v;       // BF16 [keys, heads, D]
+  uint16_t* out;           // BF16 [tokens, heads, D]
+  float* lse;              // fp32 [tokens, heads], or null
+  const int32_t* q_at;     // [count + 1]
+  const int32_t* k_at;     // [count + 1]
+  int64_t q_tok, q_head, k_tok, k_head, r_tok, v_tok, v_head, o_tok, o_head;
+  int32_t tokens, keys, heads, count;
+  float scale;             // of the scores, times log2(e)
+};
+
+// A workgroup takes R = 32 W query tokens of one head.  Slot w of the grid
+// belongs to the sequence with floor(q_at[b] / R) + b <= w, which leaves every
+// sequence as many slots as it has row tiles, whatever the offsets are.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
+  constexpr int R = 32 * W;
+  constexpr int kJ = D / 16, kO = D / 32;
+  constexpr int kC = D / 8;                       // 16-byte chunks of a row
+  constexpr int kK = 64 * 2 * D, kR = 64 * 2 * kRope;
+  constexpr int kBytes = 2 * kK + kR;             // keys, rotated keys, values
+  __shared__ __align__(1024) uint8_t lds[2 * kBytes];
+  const int32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t col = lane & 31, half = lane >> 5;
+  const int32_t w_item = blockIdx.x / p.heads, h = blockIdx.x - w_item * p.heads;
+  const auto q_row = [&](int32_t i) { return kv_clamp(p.q_at[i], p.tokens); };
+  const auto k_row = [&](int32_t i) { return kv_clamp(p.k_at[i], p.keys); };
+  const auto first_slot = [&](int32_t i) { return (int64_t)(q_row(i) / R) + i; };
+  const int32_t b = kv_find(p.count, w_item, first_slot);
+  const int32_t row0 = __builtin_amdgcn_readfirstlane(q_row(b));
+  const int32_t n = __builtin_amdgcn_readfirstlane(q_row(b + 1)) - row0;
+  const int32_t key0 = __builtin_amdgcn_readfirstlane(k_row(b));
+  const int32_t keys = max(__builtin_amdgcn_readfirstlane(k_row(b + 1)) - key0, 0);
+  const int32_t tiles = (max(n, 0) + R - 1) / R;
+  const int64_t local = w_item - (__builtin_amdgcn_readfirstlane((int32_t)(row0 / R)) + (int64_t)b);
+  if (local < 0 || local >= tiles) return;
+  const int32_t first = (tiles - 1 - (int32_t)local) * R;   // the last rows see the most keys: they go first
+  const int32_t r_in = first + wave * 32 + col;
+  const bool live = r_in < n;
+  const int64_t row = row0 + min(r_in, n - 1);
+  const int64_t before = (int64_t)keys - n;                 // keys in front of the first query's own
+  const int32_t row_hi = live ? (int32_t)max(before + r_in + 1, (int64_t)0) : 0;
+  const int32_t see_hi = (int32_t)max(before + min(first + R, n), (int64_t)0);
+  const int32_t all_hi = (int32_t)max(before + first + 1, (int64_t)0);
+  const int32_t last = (see_hi + kKeyTile - 1) / kKeyTile - 1;
+
+  const uint32_t lds0 = lds_address(lds);
+  const uint8_t* kp = (const uint8_t*)(p.k + key0 * p.k_tok + h * p.k_head);
+  const uint8_t* rp = (const uint8_t*)(p.r + key0 * p.r_tok);
+  const uint8_t* vp = (const uint8_t*)(p.v + key0 * p.v_tok + h * p.v_head);
+  // 16-byte chunks are exchanged within a row so that what is read at a time,
+  // one chunk of 16 keys or four chunks of four, falls on different banks.
+  const auto turn_k = [](int32_t key) { return kC == 16 ? key & 15 : (key >> 1) & 7; };
+  const auto turn_r = [](int32_t key) { return (key >> 1) & 7; };
+  const auto turn_v = [](int32_t key) { return kC == 16 ? (key & 3) << 2 : ((key >> 1) & 1) << 2; };
+  // Keys behind the last one that is seen count as that one.
+  const auto stage = [&](int32_t tile, int32_t slot) {
+    const uint32_t to = lds0 + slot * kBytes;
+    const int32_t t0 = tile * kKeyTile, end = see_hi - 1 - t0;
+    constexpr int kKeys = 64 / kC;   // of an instruction
+#pragma unroll
+    for (int i = 0; i < 64 / kKeys / W; ++i) {
+      const int32_t k0 = (i * W + wave) * kKeys, key = k0 + lane / kC;
+      const int64_t at = t0 + min(key, end);
+      lds_load16_at(kp + at * p.k_tok * 2 + ((lane % kC) ^ turn_k(key)) * 16, to + k0 * 2 * D);
+      lds_load16_at(vp + at * p.v_tok * 2 + ((lane % kC) ^ turn_v(key)) * 16, to + kK + kR + k0 * 2 * D);
+    }
+#pragma unroll
+    for (int i = 0; i < 8 / W; ++i) {
+      const int32_t k0 = (i * W + wave) * 8, key = k0 + (lane >> 3);
+      const int64_t at = t0 + min(key, end);
+      lds_load16_at(rp + at * p.r_tok * 2 + ((lane & 7) ^ turn_r(key)) * 16, to + kK + k0 * 128);
+    }
+  };
+  if (last >= 0) stage(0, 0);
+
+  bf16x8 q[kJ + 4];
+  {
+    const uint16_t* src = p.q + row * p.q_tok + h * p.q_head + 8 * half;
+    const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
+#pragma unroll
+    for (int j = 0; j < kJ + 4; ++j) {
+      u32x4 x = *(const u32x4*)(src + 16 * j) ^ u32x4{flip, flip, flip, flip};
+      q[j] = __builtin_bit_cast(bf16x8, kv_no_infinity(x));
+    }
+  }
+  const float factor = fmaxf(fabsf(p.scale), kTiny);
+  f32x16 o[kO];
+#pragma unroll
+  for (int i = 0; i < kO; ++i) o[i] = f32x16{};
+  float m = -INFINITY, l = 0.0f;
+
+  for (int32_t tile = 0; tile <= last; ++tile) {
+    const int32_t slot = tile & 1, t0 = tile * kKeyTile;
+    uint8_t* from = lds + slot * kBytes;
+    lds_arrived();
+    if (t0 + kKeyTile > see_hi) {
+      // values that nobody sees count as zeros, whatever is there
+      for (int32_t i = tid; i < 64 * kC; i += 64 * W) {
+        if (t0 + i / kC >= see_hi) *(u32x4*)(from + kK + kR + 16 * i) = u32x4{0, 0, 0, 0};
+      }
+      lds_written();
+    }
+    if (tile < last) stage(tile + 1, slot ^ 1);
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int32_t key = 32 * u + col;
+      s[u] = f32x16{};
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const bf16x8 a = *(const bf16x8*)(from + key * 2 * D + ((2 * j + half) ^ turn_k(key)) * 16);
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[j], s[u], 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 a = *(const bf16x8*)(from + kK + key * 128 + ((2 * j + half) ^ turn_r(key)) * 16);
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[kJ + j], s[u], 0, 0, 0);
+      }
+    }
+    if (t0 + kKeyTile > all_hi) {
+      asm volatile("");   // a branch
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int32_t hi = row_hi - t0 - 32 * u - 4 * half;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[u][e] = 8 * (e >> 2) + (e & 3) < hi ? s[u][e] : -INFINITY;
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+    }
+    top = half_max(top) * factor;
+    if (__ballot(top > m + 8.0f) != 0) {
+      const float to = fmaxf(m, top);
+      const float g = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= g;
+#pragma unroll
+      for (int i = 0; i < kO; ++i) o[i] *= g;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    bf16x8 w[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], factor, -base));
+        l += x;
+        w[2 * u + (e >> 3)][e & 7] = (__bf16)x;
+      }
+    }
+    // Lane half x holds, of each 16 keys, 4 x .. 4 x + 3 and 8 + 4 x .. 8 + 4 x + 3.
+#pragma unroll
+    for (int i = 0; i < kO; ++i) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        bf16x8 a;
+        s16x4 x[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int32_t key = 16 * t + 8 * y + 4 * half + ((lane & 15) >> 2);
+          const int32_t chunk = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+          x[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+              from + kK + kR + key * 2 * D + (chunk ^ turn_v(key)) * 16 + 8 * (lane & 1)));
+        }
+        const auto both = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        a = __builtin_bit_cast(bf16x8, both);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[t], o[i], 0, 0, 0);
+      }
+    }
+  }
+  l += __shfl_xor(l, 32);
+  if (!live) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* to = p.out + row * p.o_tok + h * p.o_head + 4 * half;
+#pragma unroll
+  for (int i = 0; i < kO; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      *(bf16x4*)(to + 32 * i + 8 * e) =
+          bf16x4{(__bf16)(o[i][4 * e] * inv), (__bf16)(o[i][4 * e + 1] * inv), (__bf16)(o[i][4 * e + 2] * inv),
+                 (__bf16)(o[i][4 * e + 3] * inv)};
+    }
+  }
+  if (half == 0 && p.lse) {
+    p.lse[row * p.heads + h] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace fp8bq

@@ -16,6 +16,7 @@ HEAD_DIMS = (64, 128, 192, 256)
 MAX_ROWS = 1 << 25             # tokens x query heads of a call
 
 _CACHE = struct.Struct("=QQQQqiiii")       # fp8bq_kv_cache
+_BUFFER = struct.Struct("=Qq")             # fp8bq_page_buffer
 _BATCH = struct.Struct("=QQQqii")          # fp8bq_kv_batch
 _TOKENS = struct.Struct("=QQQQQQ10qiiii")  # fp8bq_kv_tokens
 _QUERY = struct.Struct("=QQQ5qiifi")       # fp8bq_kv_query
@@ -34,7 +35,7 @@ class KvCache:
     """
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "page_size", "kv_heads", "head_dim",
-                 "device", "_index", "_packed")
+                 "device", "_index", "_packed", "_buffers")
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
@@ -67,8 +68,10 @@ class KvCache:
                 raise ValueError("the cache's buffers must be on one device")
         packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                              pages, size, heads, dim, 0)
+        buffers = b"".join(_BUFFER.pack(t.data_ptr(), t.numel() // pages * t.element_size())
+                           for t in (k, v, k_scale, v_scale))
         for name, value in zip(self.__slots__, (k, v, k_scale, v_scale, pages, size, heads, dim, k.device,
-                                                k.get_device(), packed)):
+                                                k.get_device(), packed, buffers)):
             object.__setattr__(self, name, value)
 
     # Calls go by the addresses taken above: another tensor put in a buffer's

@@ -511,6 +511,215 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
                        void* stream);
 
 /*
+ * A paged cache of latents, for attention whose heads share one latent and one
+ * rotated key per token (latent attention): the key of head h is
+ * (U_h c, r), its value V_h c.  Stored are c in e4m3, one descale per token,
+ * and r in BF16:
+ *   fp8bq_latent_append     rotates new keys' (and queries') rotary channels and
+ *                           stores latents and keys
+ *   fp8bq_latent_attention  the absorbed form, over what is stored: queries come
+ *                           as q U_h, outputs go to V_h
+ *   fp8bq_latent_prompt_attention  the expanded form, over keys and values of
+ *                           each head in BF16: prompts, before or beside the cache
+ * Sequences are described as for the key/value cache (fp8bq_kv_batch).
+ */
+typedef struct fp8bq_latent_cache {
+  void* c;            /* e4m3fn [num_pages, page_size, latent_dim], 16-byte aligned */
+  void* r;            /* BF16 [num_pages, page_size, 64], 16-byte aligned */
+  float* scale;       /* fp32 [num_pages, page_size], powers of two from 2^-112 to 2^112 for every
+                         token in use: of another value, its exponent counts alone */
+  int64_t num_pages;  /* 1 .. 2^31 - 1 */
+  int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t latent_dim; /* 256 or 512 */
+} fp8bq_latent_cache;
+
+/* New tokens.  Rows are BF16, contiguous, 16-byte aligned; strides are in
+ * elements, multiples of 8 and below 2^36.  Rows that are written share no
+ * elements (checked). */
+typedef struct fp8bq_latent_tokens {
+  const void* c;      /* [tokens, latent_dim] */
+  const void* r;      /* [tokens, 64] the key's rotary channels */
+  void* r_out;        /* [tokens, 64] the rotated key once more, for the expanded form; may be r
+                         itself (same stride), or NULL */
+  const void* q;      /* [tokens, q_heads, 64] the queries' rotary channels, or NULL */
+  void* q_out;        /* the rotated queries; may be q itself (same strides) */
+  const float* cos;   /* [positions, 32], contiguous, 16-byte aligned; NULL: nothing is rotated */
+  const float* sin;
+  int64_t c_token_stride, r_token_stride, r_out_token_stride;
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride;
+  int64_t tokens;     /* tokens * (q_heads, at least 1) <= 2^25 */
+  int64_t positions;  /* rows of cos and sin: tokens at later positions are left out */
+  int32_t q_heads;    /* 1 .. 1024 (ignored without q) */
+  int32_t interleaved;  /* pairs are channels (i, i + 32) if 0, (2i, 2i + 1) if not */
+} fp8bq_latent_tokens;
+
+/*
+ * Append: for the tokens of each sequence at positions p
+ *   r, q: rotated as fp8bq_kv_append rotates, rounded to BF16
+ *   s   = the smallest power of two with 448 * s >= max(max|c|, FP8BQ_EPS)
+ *   c   -> e4m3fn(clamp(c / s, -448, 448)), nearest, ties to even; s is its scale
+ * A token's codes depend on nothing but the token.  Values must be finite: a
+ * token with others gets unspecified codes.  Tokens whose page is none, or lies
+ * beyond the table, are not stored, but rotated; those at negative positions, at
+ * positions without a row of cos and sin, or of no sequence leave all rows as
+ * they were.  What is written (the cache, q_out, r_out) lies apart from the rest
+ * and from each other (checked); what fp8bq_kv_append says of pages that several
+ * sequences hold goes for single slots here.
+ * No workspace; one launch; may be captured in a graph.
+ * Returns an fp8bq_status.
+ */
+int fp8bq_latent_append(const fp8bq_latent_cache* cache, const fp8bq_kv_batch* batch,
+                        const fp8bq_latent_tokens* tokens, void* stream);
+
+/* Queries of an absorbed call, rows as in fp8bq_latent_tokens. */
+typedef struct fp8bq_latent_query {
+  const void* q;      /* BF16 [tokens, q_heads, latent_dim]: q U_h */
+  const void* q_rope; /* BF16 [tokens, q_heads, 64], rotated */
+  void* out;          /* BF16 [tokens, q_heads, latent_dim]; apart from q and q_rope */
+  float* lse;         /* fp32 [tokens, q_heads], contiguous: log of the sum of exp(score); or NULL */
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_rope_token_stride, q_rope_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int64_t tokens;     /* tokens * q_heads <= 2^25 */
+  int32_t q_heads;    /* 1 .. 1024 */
+  float scale;        /* of the scores; finite, and its product with log2(e) too */
+} fp8bq_latent_query;
+
+/* Device workspace bytes of fp8bq_latent_attention (0: none).  Of the structs
+ * only page_size, latent_dim, count and max_pages are read: the size depends on
+ * the shapes alone, not on any length. */
+size_t fp8bq_latent_attention_workspace_bytes(const fp8bq_latent_cache* cache, const fp8bq_kv_batch* batch,
+                                              int32_t q_heads, int64_t tokens);
+
+/*
+ * Attention in the absorbed form: for the query at position p of its sequence
+ *   s_j = scale * (q . c_j + q_rope . r_j)    j <= p, c_j = decode(codes) * scale_j
+ *   out = sum_j exp(s_j - max s) c_j / sum_j exp(s_j - max s)
+ *   lse = max s + log sum_j exp(s_j - max s)
+ * Rows that see nothing, rows that are not numbers, pages that are none, what
+ * lies beyond a sequence, the workspace, graphs and overlaps: as for
+ * fp8bq_kv_attention, except that out lies apart from the queries.
+ * Scores, maxima and sums are fp32.  The weights exp(s - max) * scale_j are
+ * rounded to two e4m3 terms (2^-8 of a weight, as BF16; 2^-22 of the largest of
+ * its 32 neighbours), queries in the same way (exact but for 2^-22 of the row's
+ * largest value), the output to BF16.  In sums of eight products, as the matrix
+ * instruction makes them, what lies 2^-13 below the largest may be lost.
+ * The kernel is chosen by the mean number of query rows (tokens * q_heads) per
+ * sequence.
+ * Returns an fp8bq_status.
+ */
+int fp8bq_latent_attention(const fp8bq_latent_cache* cache, const fp8bq_kv_batch* batch,
+                           const fp8bq_latent_query* query, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* A call in the expanded form.  Rows are BF16, contiguous, 16-byte aligned;
+ * strides are in elements, multiples of 8 and below 2^36. */
+typedef struct fp8bq_latent_prompt {
+  const void* q;        /* [tokens, heads, head_dim + 64]: the rotated channels last */
+  const void* k;        /* [keys, heads, head_dim] */
+  const void* k_rope;   /* [keys, 64], rotated: one for all heads */
+  const void* v;        /* [keys, heads, head_dim] */
+  void* out;            /* [tokens, heads, head_dim]; apart from the rest */
+  float* lse;           /* fp32 [tokens, heads], contiguous, or NULL */
+  const int32_t* query_start;  /* [count + 1]: sequence b's queries are rows query_start[b] .. */
+  const int32_t* key_start;    /* [count + 1] the same of its keys; NULL: the same as query_start */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, k_rope_token_stride;
+  int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+  int64_t tokens;       /* tokens * heads <= 2^25 */
+  int64_t keys;         /* keys * heads <= 2^25; equal to tokens without key_start */
+  int32_t heads;        /* 1 .. 1024 */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t count;        /* sequences, 0 .. 2^20; count * heads <= 2^21 */
+  float scale;          /* of the scores; finite, and its product with log2(e) too */
+} fp8bq_latent_prompt;
+
+/*
+ * Attention in the expanded form: a sequence's queries are its last ones, its
+ * i-th of n queries sees its first (keys - n + i + 1) keys:
+ *   s_j = scale * (q[:head_dim] . k_j + q[head_dim:] . k_rope_j)
+ *   out = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s)
+ *   lse = max s + log sum_j exp(s_j - max s)
+ * Rows that see nothing get zeros and -inf, rows that see some and hold a NaN or
+ * an infinity NaN; rows of no sequence are left as they are.  Offsets live on
+ * the device; they are clamped to 0 .. tokens and 0 .. keys.  Keys and values
+ * of a sequence must be finite; what lies behind a sequence's keys is not used.
+ * Scores, maxima and sums are fp32; weights are rounded to BF16 before their
+ * product with the values, the output once more.
+ * No workspace; may be captured in a graph, and follows the offsets.
+ * Returns an fp8bq_status.
+ */
+int fp8bq_latent_prompt_attention(const fp8bq_latent_prompt* prompt, void* stream);
+
+/*
+ * The pages of caches.  A sequence of a rollout forks into n samples of its
+ * prompt; sequences end and leave their pages between those of others.  Both
+ * calls work on all layers' caches at once, whose pages one block table names.
+ */
+typedef struct fp8bq_page_buffer {
+  void* p;             /* device, [num_pages, page_bytes], 4-byte aligned */
+  int64_t page_bytes;  /* of one page in this buffer: a multiple of 4, below 2^31 */
+} fp8bq_page_buffer;
+
+/* The paged buffers of a call: of an fp8bq_kv_cache k, v, k_scale and v_scale, of
+ * an fp8bq_latent_cache c, r and scale, for each layer.  They lie apart (checked). */
+typedef struct fp8bq_pages {
+  const fp8bq_page_buffer* buffers;  /* HOST array, read before the call returns */
+  int64_t num_pages;                 /* 1 .. 2^31 - 1 */
+  int32_t count;                     /* buffers, 1 .. 4096 */
+  int32_t page_size;                 /* tokens of a page: 16, 32, 64, 128 or 256 */
+} fp8bq_pages;
+
+/*
+ * Fork: sequence children[i] becomes a copy of sequence parents[i].  With L
+ * tokens in the parent,
+ *   seq_lens[child] = L
+ *   table[child][j] = table[parent][j]   for the L / page_size whole pages, which
+ *                     both sequences share from now on
+ *   the next entry  = fresh[i] if L % page_size > 0, and the parent's page there
+ *                     is copied to page fresh[i] in every buffer
+ *   and -1 behind.
+ *   block_table  device, [count, max_pages], rows table_stride apart; changed in place
+ *   seq_lens     device, [count]; changed in place (a negative length counts as 0)
+ *   parents, children, fresh  device, [forks], forks 0 .. 2^20
+ * The device's arrays are not checked by the host; nothing outside the buffers
+ * is touched whatever they hold.  Forks whose parent or child is not in 0 ..
+ * count - 1, or that are each other, are left out; a page number that is none gives a
+ * child without that page (-1).  A child that is named twice or is also a
+ * parent, or a page that is named twice or in use, leaves these rows and pages
+ * with unspecified contents.  No workspace; may be captured in a graph.
+ * Returns an fp8bq_status.
+ */
+int fp8bq_cache_fork(const fp8bq_pages* pages, int32_t* block_table, int64_t table_stride, int32_t count,
+                     int32_t max_pages, int32_t* seq_lens, const int32_t* parents, const int32_t* children,
+                     const int32_t* fresh, int32_t forks, void* stream);
+
+/* Device workspace bytes of fp8bq_cache_compact for caches of num_pages pages
+ * (0: more than it takes). */
+size_t fp8bq_cache_compact_workspace_bytes(int64_t num_pages);
+
+/*
+ * Compact: pages in use are those that the table names within the sequences'
+ * lengths (a sequence of length 0 uses none: so it is freed).  With U of them,
+ * the k-th page in use of those numbered U and more moves, in every buffer, to the
+ * k-th page below U that is not in use, and table_out names pages by their new
+ * numbers, -1 behind each length and for entries that are no page.  Pages that
+ * several sequences hold stay shared.  Afterwards pages U .. num_pages - 1 are free
+ * (they keep their bytes).
+ *   table_out  device, [count, max_pages], rows out_stride apart; may be
+ *              block_table itself (same stride)
+ *   used       device, [1]: U
+ *   workspace  device, fp8bq_cache_compact_workspace_bytes bytes, 16-byte
+ *              aligned, needing no initial value; calls that may overlap need one each
+ * num_pages is at most 2^20.  What is written lies apart from all else (checked).
+ * May be captured in a graph, and follows the table and the lengths.
+ * Returns an fp8bq_status.
+ */
+int fp8bq_cache_compact(const fp8bq_pages* pages, const int32_t* block_table, int64_t table_stride, int32_t count,
+                        int32_t max_pages, const int32_t* seq_lens, int32_t* table_out, int64_t out_stride,
+                        int32_t* used, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The final cast alone (clamp to +-448, round to e4m3fn), for checking the
  * hardware convert over every float32 input.
  *   y  device, fp32 [n];  q  device, uint8 [n];  n >= 0.
