@@ -436,6 +436,8 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
   d.target = s.target;
   d.jump = s.jump;
   d.min_tiles = s.min_tiles;
+  d.tile_rows = s.rows;
+  d.extra = 0;
   d.scale = scale;
   hipStream_t st = static_cast<hipStream_t>(stream);
   kv_for_dim(cache->head_dim, [&](auto dim) {

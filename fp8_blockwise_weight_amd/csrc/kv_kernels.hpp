@@ -587,8 +587,16 @@ struct KvQuery {
   int32_t target;      // work items per head that splitting aims at; 0: no splits
   int32_t jump;        // second and later slots of a row tile: first + jump + 1, ...
   int32_t min_tiles;   // least key tiles of a split
+  int32_t tile_rows;   // rows of a row tile where R below is 0
+  int32_t extra;       // what starting and ending a row tile counts for in a share, in tiles
   float scale;         // of the scores, times log2(e)
 };
+
+// Rows of a row tile: R, or with R = 0 what the call says.
+template <int R>
+__device__ __forceinline__ int32_t kv_tile_rows(const KvQuery& p) {
+  return R > 0 ? R : p.tile_rows;
+}
 
 constexpr int kKeyTile = 64;
 // Least factor of a score: a masked one, minus infinity, stays that.
@@ -658,7 +666,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvQuery& p, int
     s.row0 = b;
     s.n = 1;
   }
-  s.rtiles = (int32_t)(((uint32_t)s.n * (uint32_t)p.group + R - 1) / R);   // at most 2^25 rows
+  const uint32_t rows = (uint32_t)kv_tile_rows<R>(p);
+  s.rtiles = (int32_t)(((uint32_t)s.n * (uint32_t)p.group + rows - 1) / rows);   // at most 2^25 rows
   const int32_t hi = min(s.len, cap), lo = kv_low(s.len - s.n + 1, p.window);
   if (s.n > 0 && hi > lo) {
     s.tile0 = lo / kKeyTile;
@@ -746,7 +755,7 @@ struct KvShares {
   KvSeq s;
 
   // Units of a row tile: one that sees nothing is written, too.
-  __device__ __forceinline__ int32_t units(const KvSeq& s) const { return p.target == 0 ? 1 : max(s.tiles, 1); }
+  __device__ __forceinline__ int32_t units(const KvSeq& s) const { return p.target == 0 ? 1 : max(s.tiles, 1) + p.extra; }
   __device__ __forceinline__ int64_t weight(const KvSeq& s) const { return (int64_t)s.rtiles * units(s); }
 
   __device__ __forceinline__ KvShares(const KvBatch& bt_, const KvQuery& p_, int32_t cap_, int32_t index_)
@@ -806,10 +815,10 @@ struct KvShares {
     k.row0 = s.row0;
     k.n = s.n;
     k.pos0 = s.len - s.n;
-    k.first = rtile * R;
+    k.first = rtile * kv_tile_rows<R>(p);
     k.count = s.n * p.group;
-    k.tile0 = s.tile0 + t;
-    k.tile1 = s.tile0 + (p.target == 0 ? s.tiles : min(t + take, s.tiles));
+    k.tile0 = s.tile0 + max(t - p.extra, 0);
+    k.tile1 = s.tile0 + (p.target == 0 ? s.tiles : min(max(t + take - p.extra, 0), s.tiles));
     k.begin = t == 0;
     k.parts = 1;
     if (t > 0 || t + take < tiles) {

@@ -85,8 +85,9 @@ fp8bq::LatentCache latent_device(const fp8bq_latent_cache& c) {
 // How an absorbed call is cut up, from the shapes alone.
 struct LatentShape {
   int32_t rows;        // query rows of a workgroup
+  int32_t subs;        // workgroups that take the same keys for rows side by side
   int32_t grid;
-  int32_t target;      // shares that the key tiles are cut into; 0: one workgroup per row tile
+  int32_t target;      // shares that the key tiles are cut into; 0: one for each row tile
   int32_t slots;
   size_t rows_at, ml_at, bytes;   // workspace: partial sums at 0, then these
 };
@@ -94,16 +95,17 @@ struct LatentShape {
 LatentShape latent_shape(const fp8bq_latent_cache& c, const fp8bq_kv_batch& b, int32_t heads, int64_t tokens) {
   LatentShape s;
   const int64_t per_seq = ceil_div(tokens * heads, b.count);
-  s.rows = per_seq <= 32 ? 32 : (per_seq <= 64 ? 64 : 128);
-  const int64_t row_tiles = tokens * heads / s.rows + b.count;
+  s.rows = per_seq <= 32 ? 32 : 64;
+  s.subs = per_seq <= 64 ? 1 : (per_seq <= 128 ? 2 : 4);
+  const int64_t row_tiles = tokens * heads / (s.rows * s.subs) + b.count;
   const int64_t key_tiles = ceil_div(static_cast<int64_t>(b.max_pages) * c.page_size, 64);
-  s.target = s.rows == 32 ? 512 : 256;
+  s.target = (s.rows == 32 ? 512 : 256) / s.subs;
   if (key_tiles <= 2) s.target = 0;
-  s.grid = s.target ? s.target : static_cast<int32_t>(row_tiles);
+  s.grid = static_cast<int32_t>(s.target ? s.target : ceil_div(row_tiles, 8) * 8) * s.subs;
   s.slots = 2 * s.target;
   s.ml_at = s.rows_at = s.bytes = 0;
   if (s.target == 0) return s;
-  const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(s.rows);
+  const size_t n = static_cast<size_t>(s.slots) * static_cast<size_t>(s.rows * s.subs);
   s.ml_at = n * static_cast<size_t>(c.latent_dim) * 4;
   s.rows_at = s.ml_at + n * 8;
   s.bytes = s.rows_at + static_cast<size_t>(tokens) * static_cast<size_t>(heads) * 8;
@@ -115,19 +117,17 @@ void latent_launch(const LatentShape& s, const fp8bq::LatentCache& c, const fp8b
                    const fp8bq::LatentQuery& q, int64_t rows, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(s.grid));
   if (s.rows == 32) {
-    hipLaunchKernelGGL((fp8bq::latent_attend<L, 2, 2>), grid, dim3(128), 0, st, c, b, q);
-  } else if (s.rows == 64) {
-    hipLaunchKernelGGL((fp8bq::latent_attend<L, 4, 2>), grid, dim3(256), 0, st, c, b, q);
+    hipLaunchKernelGGL((fp8bq::latent_attend<L, 2>), grid, dim3(128), 0, st, c, b, q);
   } else {
-    hipLaunchKernelGGL((fp8bq::latent_attend<L, 4, 1>), grid, dim3(256), 0, st, c, b, q);
+    hipLaunchKernelGGL((fp8bq::latent_attend<L, 4>), grid, dim3(256), 0, st, c, b, q);
   }
   if (s.target == 0) return;
   if (rows <= 1024) {
     hipLaunchKernelGGL((fp8bq::kv_attend_join<L, 8>), dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, b, q.k, 1,
-                       s.rows);
+                       s.rows * s.subs);
   } else {
     hipLaunchKernelGGL((fp8bq::kv_attend_join<L, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0, st,
-                       b, q.k, 1, s.rows);
+                       b, q.k, 1, s.rows * s.subs);
   }
 }
 
@@ -300,6 +300,9 @@ int fp8bq_latent_attention(const fp8bq_latent_cache* cache, const fp8bq_kv_batch
   d.k.target = s.target;
   d.k.jump = s.target;
   d.k.min_tiles = 1;
+  d.k.tile_rows = s.rows * s.subs;
+  d.k.extra = 4;
+  d.subs = s.subs;
   d.k.scale = scale;
   d.r = static_cast<const uint16_t*>(q->q_rope);
   d.r_tok = q->q_rope_token_stride;

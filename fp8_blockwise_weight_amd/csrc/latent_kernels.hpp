@@ -123,6 +123,7 @@ struct LatentQuery {
   KvQuery k;             // k.q: the absorbed channels; k.group: heads
   const uint16_t* r;     // the rotated channels
   int64_t r_tok, r_head;
+  int32_t subs;          // row tiles that share keys, side by side on one XCD
 };
 
 // 16 bytes a lane (4 with kWord) from memory into LDS, past the registers: lane
@@ -162,6 +163,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // `hi` is the code of x / s, `lo` of (x - hi s) / (s / 32): with |x| < 256 s
 // the rest is at most 8 s.
 constexpr int kLoShift = 5;
+constexpr float kRise = 32.0f;   // by how much (log2) scores pass their maximum before it follows
 __device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo, bool upper) {
   const float t = s * (1.0f / (1 << kLoShift));
   s16x2 h = __builtin_bit_cast(s16x2, hi), l = __builtin_bit_cast(s16x2, lo);
@@ -190,6 +192,74 @@ __device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, con
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, kSelA, sa, kSelB, sb);
 }
 
+// Sums stay in accumulation registers a0 .. a127 from the first product to the
+// last, by name.  Left to itself the compiler moves all of them to other
+// registers and back in every tile, for the sake of the path that scales them
+// once in a while (245 us for what takes 150).  So every use is assembly: the
+// products (which need two cycles behind whatever vector instruction wrote their
+// operands), scaling and reading (behind the wait that a product's result needs).
+template <int I>
+struct Acc;
+#define FP8BQ_ACC_MUL(n) \
+  "v_accvgpr_read_b32 %1, a" #n "\n\ts_nop 1\n\tv_mul_f32_e32 %1, %1, %2\n\ts_nop 1\n\tv_accvgpr_write_b32 a" #n ", %1\n\t"
+#define FP8BQ_ACC(I, R, n0, n1, n2, n3, n4, n5, n6, n7, n8, n9, n10, n11, n12, n13, n14, n15)                        \
+  template <>                                                                                                        \
+  struct Acc<I> {                                                                                                    \
+    static __device__ __forceinline__ void clear(f32x16& o) {                                                        \
+      o = f32x16{};                                                                                                  \
+      asm volatile("" : "+{" R "}"(o));                                                                              \
+    }                                                                                                                \
+    static __device__ __forceinline__ void add_hi(f32x16& o, const i32x8& a, const i32x8& b, int32_t sa, int32_t sb) { \
+      asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 " R ", %1, %2, " R ", %3, %4 op_sel_hi:[0,0,0]"        \
+                   : "+{" R "}"(o)                                                                                   \
+                   : "v"(a), "v"(b), "v"(sa), "v"(sb));                                                              \
+    }                                                                                                                \
+    static __device__ __forceinline__ void add_lo(f32x16& o, const i32x8& a, const i32x8& b, int32_t sa, int32_t sb) { \
+      asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 " R ", %1, %2, " R                                   \
+                   ", %3, %4 op_sel:[0,1,0] op_sel_hi:[0,0,0]"                                                       \
+                   : "+{" R "}"(o)                                                                                   \
+                   : "v"(a), "v"(b), "v"(sa), "v"(sb));                                                              \
+    }                                                                                                                \
+    static __device__ __forceinline__ void scale(f32x16& o, float g) {                                               \
+      float t;                                                                                                       \
+      asm volatile(FP8BQ_ACC_MUL(n0) FP8BQ_ACC_MUL(n1) FP8BQ_ACC_MUL(n2) FP8BQ_ACC_MUL(n3) FP8BQ_ACC_MUL(n4)         \
+                   FP8BQ_ACC_MUL(n5) FP8BQ_ACC_MUL(n6) FP8BQ_ACC_MUL(n7) FP8BQ_ACC_MUL(n8) FP8BQ_ACC_MUL(n9)         \
+                   FP8BQ_ACC_MUL(n10) FP8BQ_ACC_MUL(n11) FP8BQ_ACC_MUL(n12) FP8BQ_ACC_MUL(n13) FP8BQ_ACC_MUL(n14)    \
+                   FP8BQ_ACC_MUL(n15)                                                                                \
+                   : "+{" R "}"(o), "=&v"(t)                                                                         \
+                   : "v"(g));                                                                                        \
+    }                                                                                                                \
+  };
+FP8BQ_ACC(0, "a[0:15]", 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15)
+FP8BQ_ACC(1, "a[16:31]", 16, 17, 18, 19, 20, 21, 22, 23, 24, 25, 26, 27, 28, 29, 30, 31)
+FP8BQ_ACC(2, "a[32:47]", 32, 33, 34, 35, 36, 37, 38, 39, 40, 41, 42, 43, 44, 45, 46, 47)
+FP8BQ_ACC(3, "a[48:63]", 48, 49, 50, 51, 52, 53, 54, 55, 56, 57, 58, 59, 60, 61, 62, 63)
+FP8BQ_ACC(4, "a[64:79]", 64, 65, 66, 67, 68, 69, 70, 71, 72, 73, 74, 75, 76, 77, 78, 79)
+FP8BQ_ACC(5, "a[80:95]", 80, 81, 82, 83, 84, 85, 86, 87, 88, 89, 90, 91, 92, 93, 94, 95)
+FP8BQ_ACC(6, "a[96:111]", 96, 97, 98, 99, 100, 101, 102, 103, 104, 105, 106, 107, 108, 109, 110, 111)
+FP8BQ_ACC(7, "a[112:127]", 112, 113, 114, 115, 116, 117, 118, 119, 120, 121, 122, 123, 124, 125, 126, 127)
+#undef FP8BQ_ACC
+#undef FP8BQ_ACC_MUL
+// The wait, before the compiler may move sums anywhere (an operand of each, so
+// that moves come behind it), and once more before they are products' operands.
+template <int N>
+__device__ __forceinline__ void acc_wait(f32x16 (&o)[N]) {
+  static_assert(N == 4 || N == 8, "the channels of a wave");
+  if constexpr (N == 8) {
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+{a[0:15]}"(o[0]), "+{a[16:31]}"(o[1]), "+{a[32:47]}"(o[2]), "+{a[48:63]}"(o[3]),
+                   "+{a[64:79]}"(o[4]), "+{a[80:95]}"(o[5]), "+{a[96:111]}"(o[6]), "+{a[112:127]}"(o[7]));
+  } else {
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+{a[0:15]}"(o[0]), "+{a[16:31]}"(o[1]), "+{a[32:47]}"(o[2]), "+{a[48:63]}"(o[3]));
+  }
+}
+__device__ __forceinline__ float acc_read(float a) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+
 // A tile of 64 keys in LDS: rows of L codes, whose 16-byte chunks are exchanged
 // within 16 of them (XOR), rows of 64 BF16 rotated channels, exchanged within 8,
 // and the scales.
@@ -202,396 +272,579 @@ __device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, con
 __device__ __forceinline__ int32_t code_turn(int32_t key) { return ((key & 7) << 1) | ((key >> 4) & 1); }
 __device__ __forceinline__ int32_t rope_turn(int32_t key) { return ((key >> 1) & 3) | (((key >> 4) & 1) << 2); }
 
-template <int L, int W, int S>
+template <int L, int W>
 struct LatentTile {
-  static constexpr bool kRopeStaged = !(W == 2);
-  static constexpr int kCodes = 64 * L, kRopes = kRopeStaged ? 64 * 2 * kRope : 0;
+  static constexpr bool kDeep = W == 4;
+  static constexpr int kSlots = kDeep ? 3 : 2;
+  static constexpr int kCodes = 64 * L, kRopes = kDeep ? 64 * 2 * kRope : 0;
   static constexpr int kBytes = kCodes + kRopes + 256;
 };
 
-// W waves; S of them share 32 query rows.  With S = 1 a wave makes all scores of
-// its rows and all channels of their sums.  With S = 2 it makes those of every
-// other 32 keys, the weights go through LDS, and each wave sums half the
+// The weights of 32 rows and 32 keys, as two terms, in the order in which the
+// product takes them; the maximum they are taken from, the scale's exponent.
+struct LatentWeights {
+  u32x4 hi[64], lo[64];
+  float m[32];
+  int32_t e[32];
+};
+
+// f(std::integral_constant<int, i>) for i = 0 .. N - 1.
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (N > 0) {
+    unrolled<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+// W waves, two of them for 32 query rows: each makes the scores and weights of
+// every other 32 keys, the weights go through LDS, and each sums half the
 // channels.
-template <int L, int W, int S>
+template <int L, int W>
 __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatch bt, LatentQuery lq) {
-  constexpr int R = 32 * W / S, N = 64 * W;
+  constexpr int R = 16 * W, N = 64 * W;
   constexpr int kJ = L / 64;              // 64-channel pieces of the scores
-  constexpr int kU = 2 / S;               // 32-key blocks of a wave's scores
-  constexpr int kO = L / 32 / S;          // 32-channel tiles of a wave's sums
-  using Tile = LatentTile<L, W, S>;
-  constexpr bool kRopeStaged = Tile::kRopeStaged;
-  struct Weights {                        // of 32 rows and 32 keys
-    u32x4 hi[64], lo[64];
-    float m[32];
-    int32_t e[32];
-  };
-  __shared__ __align__(1024) uint8_t lds[2 * Tile::kBytes];
-  __shared__ Weights ex[S == 2 ? W : 1];
+  constexpr int kO = L / 64;              // 32-channel tiles of a wave's sums
+  using Tile = LatentTile<L, W>;
+  constexpr bool kDeep = Tile::kDeep;
+  constexpr int kSlots = Tile::kSlots;
+  __shared__ __align__(1024) uint8_t lds[kSlots * Tile::kBytes];
+  __shared__ LatentWeights ex[kDeep ? 2 : 1][W];
+  __shared__ u32x4 turned[W / 2][4][64];   // the queries' rotated channels: registers are scarce
   const KvQuery& p = lq.k;
   const int32_t cap = kv_capacity(bt, c.log_s);
-  const float scale = fabsf(p.scale);
   const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the factor below is positive
+  const float factor = fmaxf(fabsf(p.scale), kTiny);
   const int32_t wave = __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x >> 6);
-  const int32_t part = S == 2 ? wave & 1 : 0;                // which keys, which channels
-  const int32_t lds0 = (int32_t)lds_address(lds);
-  KvShares<R> shares(bt, p, cap, blockIdx.x);
+  const int32_t part = wave & 1;                             // which keys, which channels
+  const uint32_t lds0 = lds_address(lds);
+  // Workgroups go round the eight XCDs: those of one share follow each other on one.
+  const int32_t turn_of = blockIdx.x >> 3, sub = turn_of % lq.subs;
+  KvShares<0> shares(bt, p, cap, (turn_of / lq.subs) * 8 + (blockIdx.x & 7));
   KvWork wk;
   while (shares.next(wk)) {
     int32_t tid = threadIdx.x;
     asm volatile("" : "+v"(tid));   // as in kv_attend_rows
     const int32_t lane = tid & 63, col = lane & 31, half = lane >> 5;
+    wk.first += sub * R;
+    if (wk.first >= wk.count) continue;
     const KvSeen see = kv_seen<R>(wk, p, cap);
-    const int32_t r_in = (wave / S) * 32 + col, r_mine = wk.first + r_in;
+    const int32_t r_in = (wave >> 1) * 32 + col, r_mine = wk.first + r_in;
     const bool live = r_mine < wk.count;
     const int32_t tok_mine = live ? r_mine / p.group : 0;
     const int64_t head = live ? r_mine - tok_mine * p.group : 0;
     const int64_t row = wk.row0 + tok_mine;
     const int32_t row_hi = live ? min(wk.pos0 + tok_mine + 1, cap) : 0;
+    const int32_t last = see.tile1 - 1;
 
-    // Pages of a tile's runs of 16 tokens, the same in every lane; -1 where the
-    // table's entry is no page or none of the tokens is seen.
-    const FP8BQ_CONSTANT int32_t* table =
-        (const FP8BQ_CONSTANT int32_t*)(uintptr_t)(bt.table + (int64_t)wk.b * bt.stride);
+    // Pages of a tile's runs of 16 tokens (runs that nobody sees: that of the
+    // last token), the same in every lane; -1 where the table's entry is no page.
+    // 64 entries of the table lie in a register, a lane each: loaded one tile at a
+    // time, even two tiles ahead, they were waited for in every tile.
+    const int32_t* table = bt.table + (int64_t)wk.b * bt.stride;
+    int32_t held = INT32_MIN / 2, entries = 0;
     struct Pages {
       int32_t of[4];
     };
+    auto entry_of = [&](int32_t tile, int32_t r) { return min(tile * kKeyTile + 16 * r, see.see_hi - 1) >> c.log_s; };
     auto pages = [&](int32_t tile) {
+      if (entry_of(tile, 3) - held >= 64) {
+        held = entry_of(tile, 0);
+        entries = table[min(held + lane, entry_of(last, 3))];
+        asm volatile("" : "+v"(entries));   // waited for here
+      }
       Pages x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int32_t t0 = tile * kKeyTile + 16 * r;
-        int32_t pg = -1;
-        if (t0 < see.see_hi) pg = table[t0 >> c.log_s];
-        pg = __builtin_amdgcn_readfirstlane(pg);
-        x.of[r] = pg >= 0 && pg < c.pages ? pg : -1;
+        const int32_t pg = lane_of(entries, entry_of(tile, r) - held);
+        x.of[r] = (uint32_t)pg < (uint32_t)c.pages ? pg : -1;
       }
       return x;
     };
+    auto bad = [](const Pages& x) { return (x.of[0] | x.of[1] | x.of[2] | x.of[3]) < 0; };
     auto pick = [](const Pages& x, int32_t r) {
       const int32_t a = r & 1 ? x.of[1] : x.of[0], b = r & 1 ? x.of[3] : x.of[2];
       return r & 2 ? b : a;
     };
-    // A wave stages 4 / W runs of 16 tokens.
-    auto stage = [&](int32_t tile, int32_t slot, const Pages& x) {
-      const uint32_t to = lds0 + slot * Tile::kBytes;
+    auto place_of = [&](const Pages& x, int32_t tile, int32_t run) {
+      return ((int64_t)max(pick(x, run), 0) << c.log_s) + ((tile * kKeyTile + 16 * run) & ((1 << c.log_s) - 1));
+    };
+    // A wave stages 4 / W runs of 16 tokens, in kPieces instructions: one takes
+    // 1024 / L tokens' codes, or the rotated channels of 8, or all scales (which
+    // every wave loads, so that there is no branch).
+    constexpr int kKeys = 1024 / L, kRuns = 4 / W, kPerRun = 16 / kKeys + (kDeep ? 2 : 0), kPieces = kRuns * kPerRun + 1;
+    const int32_t k_in = lane / (L / 16), r_in8 = lane >> 3;
+    struct Stage {
+      const uint8_t* code[kRuns];
+      const uint8_t* rope[kRuns];
+      const float* scale;
+      uint32_t to;
+    };
+    auto plan = [&](int32_t tile, int32_t slot, const Pages& x) {
+      Stage g;
 #pragma unroll
-      for (int i = 0; i < 4 / W; ++i) {
-        const int32_t run = wave * (4 / W) + i, t0 = tile * kKeyTile + 16 * run;
-        const int64_t place = ((int64_t)max(pick(x, run), 0) << c.log_s) + (t0 & ((1 << c.log_s) - 1));
-        const uint8_t* from = c.c + place * L;
-        constexpr int kKeys = 1024 / L;   // of an instruction
-#pragma unroll
-        for (int k = 0; k < 16; k += kKeys) {
-          const int32_t key = 16 * run + k + lane / (L / 16);
-          const uint32_t off = (lane / (L / 16)) * L + ((lane % (L / 16)) ^ code_turn(key)) * 16;
-          lds_load16(from + k * L, off, to + (16 * run + k) * L);
-        }
-        if constexpr (kRopeStaged) {
-          const uint8_t* rope = (const uint8_t*)(c.r + place * kRope);
-#pragma unroll
-          for (int k = 0; k < 16; k += 8) {
-            const int32_t key = 16 * run + k + (lane >> 3);
-            const uint32_t off = (lane >> 3) * 128 + ((lane & 7) ^ rope_turn(key)) * 16;
-            lds_load16(rope + k * 128, off, to + Tile::kCodes + (16 * run + k) * 128);
-          }
-        }
+      for (int i = 0; i < kRuns; ++i) {
+        const int64_t place = place_of(x, tile, wave * kRuns + i);
+        g.code[i] = c.c + place * L;
+        g.rope[i] = (const uint8_t*)(c.r + place * kRope);
       }
-      if (wave == 0) {
-        const int32_t run = lane >> 4, t0 = tile * kKeyTile + 16 * run;
-        const int64_t place = ((int64_t)max(pick(x, run), 0) << c.log_s) + (t0 & ((1 << c.log_s) - 1)) + (lane & 15);
-        lds_load4(c.scale + place, to + Tile::kCodes + Tile::kRopes);
+      g.scale = c.scale + place_of(x, tile, lane >> 4) + (lane & 15);
+      g.to = lds0 + slot * Tile::kBytes;
+      return g;
+    };
+    auto piece = [&](const Stage& g, auto which) {
+      constexpr int n = decltype(which)::value;
+      if constexpr (n == kPieces - 1) {
+        lds_load4(g.scale, g.to + Tile::kCodes + Tile::kRopes);
+      } else if constexpr (n < kPieces - 1) {
+        constexpr int i = n / kPerRun, at = n - i * kPerRun;
+        const int32_t run = wave * kRuns + i;
+        if constexpr (at < 16 / kKeys) {
+          constexpr int k = at * kKeys;
+          const uint32_t off = k_in * L + ((lane % (L / 16)) ^ code_turn(16 * run + k + k_in)) * 16;
+          lds_load16(g.code[i] + k * L, off, g.to + (16 * run + k) * L);
+        } else {
+          constexpr int k = (at - 16 / kKeys) * 8;
+          const uint32_t off = r_in8 * 128 + ((lane & 7) ^ rope_turn(16 * run + k + r_in8)) * 16;
+          lds_load16(g.rope[i] + k * 128, off, g.to + Tile::kCodes + (16 * run + k) * 128);
+        }
       }
     };
-    // Rotated channels of this wave's own keys, where they do not go through LDS.
-    u32x4 rope[kRopeStaged ? 1 : 4];
+    // Key that is row `col` of this wave's scores.
+    const int32_t key = 32 * part + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
+    // Its rotated channels, where they do not go through LDS.
+    u32x4 rope[kDeep ? 1 : 4];
     auto fetch_rope = [&](int32_t tile, const Pages& x) {
-      if constexpr (!kRopeStaged) {
-        const int32_t key = 32 * part + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
-        const int32_t t0 = tile * kKeyTile + (key & ~15);
-        const int64_t place = ((int64_t)max(pick(x, key >> 4), 0) << c.log_s) + (t0 & ((1 << c.log_s) - 1)) + (key & 15);
+      if constexpr (!kDeep) {
+        const uint16_t* from = c.r + (place_of(x, tile, key >> 4) + (key & 15)) * kRope + 8 * half;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rope[j] = *(const u32x4*)(c.r + place * kRope + 16 * j + 8 * half);
+        for (int j = 0; j < 4; ++j) rope[j] = *(const u32x4*)(from + 16 * j);
       }
+    };
+    // What nobody sees counts as zeros, whatever is there.
+    auto clear = [&](uint8_t* to, int32_t tile, const Pages& x) {
+      for (int32_t i = tid; i < 64 * (L / 16); i += N) {
+        const int32_t k = i / (L / 16);
+        if (pick(x, k >> 4) < 0 || tile * kKeyTile + k >= see.see_hi) *(u32x4*)(to + 16 * i) = u32x4{0, 0, 0, 0};
+      }
+      if (tid < 64 && (pick(x, tid >> 4) < 0 || tile * kKeyTile + tid >= see.see_hi)) {
+        *(float*)(to + Tile::kCodes + Tile::kRopes + 4 * tid) = 1.0f;
+      }
+      lds_written();
     };
 
-    const int32_t last = see.tile1 - 1;
-    Pages now, next;
+    Pages now;
     lds_written();   // LDS is free of the row tile before
     if (see.tile0 <= last) {
       now = pages(see.tile0);
-      stage(see.tile0, 0, now);
-      next = pages(min(see.tile0 + 1, last));
+      const Stage g = plan(see.tile0, 0, now);
+      unrolled<kPieces>([&](auto n) { piece(g, n); });
+      fetch_rope(see.tile0, now);
     }
 
-    // The queries, as codes and as what is left: one scale for a row.
+    // The queries, as codes and as what is left.  Each wave of a pair splits half
+    // the channels, with a scale for its half of a row, and both take both from
+    // LDS, out of slots that are not filled yet.
     i32x8 qh[kJ], ql[kJ];
-    bf16x8 qr[4];
-    int32_t q_scale;
+    int32_t q_scale[2];
     {
-      const uint16_t* src = p.q + row * p.q_tok + head * p.q_head + 32 * half;
-      u32x4 x[kJ][4];
-      uint32_t most = 0;
+      constexpr int kH = kJ / 2;
+      static_assert((W / 2) * 2 * kH * 4 * 64 * 16 <= (kSlots - 1) * Tile::kBytes, "behind the first slot");
+      // (rows beyond the last one read the sequence's first, for nothing)
+      const uint16_t* src = p.q + row * p.q_tok + head * p.q_head + 64 * kH * part + 32 * half;
+      const uint16_t* rot = lq.r + row * lq.r_tok + head * lq.r_head + 8 * half;
+      u32x4 x[kH][4], y[4];
+      uint32_t most = 0, most_r = 0;
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
+      for (int j = 0; j < kH; ++j) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          x[j][y] = *(const u32x4*)(src + 64 * j + 8 * y);
-          if (!live) x[j][y] = u32x4{0, 0, 0, 0};
-          x[j][y] = kv_no_infinity(x[j][y] ^ u32x4{flip, flip, flip, flip});
-          most = pk_max_u16(most, fold_abs(x[j][y]));
-        }
+        for (int z = 0; z < 4; ++z) x[j][z] = *(const u32x4*)(src + 64 * j + 8 * z);
       }
-      // what is not a number has the largest magnitude; it becomes a code that is none under any scale
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = *(const u32x4*)(rot + 16 * j);
+#pragma unroll
+      for (int j = 0; j < kH; ++j) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z) most = pk_max_u16(most, fold_abs(x[j][z]));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most_r = pk_max_u16(most_r, fold_abs(y[j]));
+      // What is not a number counts as the largest that is: it becomes a code that
+      // is none anyway.
+      const bool odd = __ballot(halves_max(pk_max_u16(most, most_r)) >= 0x7F80u) != 0;
       const float top = half_max(__uint_as_float(min(halves_max(most), 0x7F7Fu) << 16));
       const int32_t e = split_exponent(top);
-      q_scale = e | ((e - kLoShift) << 8);
+      const float es = exponent_scale(e);
+      if (odd || flip != 0) {
+        const auto clean = [&](u32x4 v) { return kv_no_infinity(v ^ u32x4{flip, flip, flip, flip}); };
+#pragma unroll
+        for (int j = 0; j < kH; ++j) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[j][z] = clean(x[j][z]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = clean(y[j]);
+      }
+      u32x4* pass = (u32x4*)(lds + Tile::kBytes) + (wave & ~1) * kH * 4 * 64 + lane;
+#pragma unroll
+      for (int j = 0; j < kH; ++j) {
+        u32x4 h[2], l[2];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t a = 0, b = 0;
+            split2(bf_lo(x[j][z][2 * w]), bf_hi(x[j][z][2 * w]), es, a, b, false);
+            split2(bf_lo(x[j][z][2 * w + 1]), bf_hi(x[j][z][2 * w + 1]), es, a, b, true);
+            h[z >> 1][2 * (z & 1) + w] = a;
+            l[z >> 1][2 * (z & 1) + w] = b;
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          pass[((part * kH + j) * 4 + z) * 64] = h[z];
+          pass[((part * kH + j) * 4 + 2 + z) * 64] = l[z];
+        }
+      }
+      if (part == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turned[wave >> 1][j][lane] = y[j];
+      }
+      if (half == 0) ex[0][wave].e[col] = e;
+      lds_written();
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int z = 0; z < 2; ++z) {
+          const u32x4 h = pass[(j * 4 + z) * 64], l = pass[(j * 4 + 2 + z) * 64];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            uint32_t h = 0, l = 0;
-            split2(bf_lo(x[j][y][2 * z]), bf_hi(x[j][y][2 * z]), exponent_scale(e), h, l, false);
-            split2(bf_lo(x[j][y][2 * z + 1]), bf_hi(x[j][y][2 * z + 1]), exponent_scale(e), h, l, true);
-            qh[j][2 * y + z] = (int32_t)h;
-            ql[j][2 * y + z] = (int32_t)l;
+          for (int w = 0; w < 4; ++w) {
+            qh[j][4 * z + w] = (int32_t)h[w];
+            ql[j][4 * z + w] = (int32_t)l[w];
           }
         }
       }
-      const uint16_t* rot = lq.r + row * lq.r_tok + head * lq.r_head + 8 * half;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4 y = *(const u32x4*)(rot + 16 * j);
-        if (!live) y = u32x4{0, 0, 0, 0};
-        qr[j] = __builtin_bit_cast(bf16x8, kv_no_infinity(y ^ u32x4{flip, flip, flip, flip}));
+      for (int z = 0; z < 2; ++z) {
+        const int32_t of = ex[0][(wave & ~1) + z].e[col];
+        q_scale[z] = of | ((of - kLoShift) << 8);
       }
     }
 
     f32x16 o[kO];
-#pragma unroll
-    for (int i = 0; i < kO; ++i) o[i] = f32x16{};
+    unrolled<kO>([&](auto i) { Acc<decltype(i)::value>::clear(o[decltype(i)::value]); });
     // The maximum that weights are taken from, a whole number, so that changes of
-    // it are exact: of this wave's keys, and of the sums (S = 2).
+    // it are exact: of this wave's keys, and of the sums.
     float m = -INFINITY, ref = -INFINITY, l = 0.0f;
 
-    if (see.tile0 <= last) fetch_rope(see.tile0, now);
-    for (int32_t tile = see.tile0; tile <= last; ++tile) {
-      const int32_t slot = (tile - see.tile0) & 1;
-      const uint8_t* from = lds + slot * Tile::kBytes;
-      const float* scales = (const float*)(from + Tile::kCodes + Tile::kRopes);
-      lds_arrived();
-      u32x4 rope_now[kRopeStaged ? 1 : 4];
-      if constexpr (!kRopeStaged) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) rope_now[j] = rope[j];
-      }
-      const int32_t t0 = tile * kKeyTile;
-      const bool bad = (now.of[0] | now.of[1] | now.of[2] | now.of[3]) < 0;
-      if (bad || t0 + kKeyTile > see.see_hi) {
-        // what nobody sees counts as zeros, whatever is there
-        uint8_t* to = lds + slot * Tile::kBytes;
-        for (int32_t i = tid; i < 64 * (L / 16); i += N) {
-          const int32_t key = i / (L / 16);
-          if (pick(now, key >> 4) < 0 || t0 + key >= see.see_hi) *(u32x4*)(to + 16 * i) = u32x4{0, 0, 0, 0};
-        }
-        if (tid < 64 && (pick(now, tid >> 4) < 0 || t0 + tid >= see.see_hi)) {
-          *(float*)(to + Tile::kCodes + Tile::kRopes + 4 * tid) = 1.0f;
-        }
-        lds_written();
-      }
-      const Pages mine = now;
-      if (tile < last) {
-        stage(tile + 1, slot ^ 1, next);
-        fetch_rope(tile + 1, next);
-        now = next;
-        next = pages(min(tile + 2, last));
-      }
+    // Places in a tile that this lane reads: chunk 0, from which the others are
+    // an exchange away (places of tiles are multiples of 256).
+    static_assert(Tile::kBytes % 256 == 0, "an XOR with less than 256 stays in its row");
+    const uint32_t k_at = key * L + ((2 * half) ^ code_turn(key)) * 16;
+    const uint32_t r_at = Tile::kCodes + key * 128 + (half ^ rope_turn(key)) * 16;
+    // Channel 32 i + (lane mod 32) of this wave's half, 8 keys to a read.
+    const int32_t v_key = 16 * half + ((lane & 15) >> 1), v_bit = (lane >> 4) & 1;
+    const uint32_t v_at = v_key * L + ((2 * part * kO + v_bit) ^ code_turn(v_key)) * 16 + 8 * (lane & 1);
+    const int32_t k0 = 32 * part + 16 * half;   // the 16 keys of a lane's scores
 
-      // scores
-      f32x16 s[kU];
+    // Scores, operands read two pieces ahead, the next tile's loads in between:
+    // one wave to a SIMD, nothing else hides what it waits for.  Each step is
+    // held where it is written.
+    auto lds_of = [&](const uint8_t* from) { return (uint32_t)(from - lds); };
+    auto scores = [&](const uint8_t* from, const Stage& g, auto staging, auto&& at_end) {
+      constexpr int kAhead = 1, kSteps = kJ + 2, kEach = kDeep ? (kPieces + kSteps - 1) / kSteps : 5;
+      u32x4 a[kAhead + 1][2];
+      bf16x8 ra[2], rq[2];
+      const uint32_t k_now = k_at + lds_of(from), r_now = r_at + lds_of(from);
+      const auto read = [&](int j) {
 #pragma unroll
-      for (int v = 0; v < kU; ++v) {
-        const int32_t u = S == 2 ? part : v;
-        const int32_t key = 32 * u + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
-        const uint8_t* krow = from + key * L;
-        const int32_t turn = code_turn(key);
-        const int32_t ks = (__float_as_uint(scales[key]) >> 23) & 255;
-        s[v] = f32x16{};
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const u32x4 a = *(const u32x4*)(krow + ((4 * j + 2 * half) ^ turn) * 16);
-          const u32x4 b = *(const u32x4*)(krow + ((4 * j + 2 * half + 1) ^ turn) * 16);
-          const i32x8 k = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-          s[v] = mfma_codes<0, 0>(k, qh[j], s[v], ks, q_scale);
-          s[v] = mfma_codes<0, 1>(k, ql[j], s[v], ks, q_scale);
+        for (int y = 0; y < 2; ++y) a[j % (kAhead + 1)][y] = *(const u32x4*)(lds + (k_now ^ ((4 * (j & 3) + y) * 16)) + (j >> 2) * 256);
+      };
+      const auto read_rope = [&](int j) {
+        if constexpr (kDeep) {
+          ra[j & 1] = *(const bf16x8*)(lds + (r_now ^ (2 * j * 16)));
+        } else {
+          ra[j & 1] = __builtin_bit_cast(bf16x8, rope[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u32x4 a;
-          if constexpr (kRopeStaged) {
-            a = *(const u32x4*)(from + Tile::kCodes + key * 128 + ((2 * j + half) ^ rope_turn(key)) * 16);
-          } else {
-            a = rope_now[j];
-          }
-          s[v] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), qr[j], s[v], 0, 0, 0);
+        rq[j & 1] = __builtin_bit_cast(bf16x8, turned[wave >> 1][j][lane]);
+      };
+      const int32_t ks = (__float_as_uint(*(const float*)(from + Tile::kCodes + Tile::kRopes + 4 * key)) >> 23) & 255;
+      read(0);
+      f32x16 s = {};
+      __builtin_amdgcn_sched_barrier(0);
+      unrolled<kJ>([&](auto step) {
+        constexpr int j = decltype(step)::value;
+        if constexpr (j + kAhead < kJ) read(j + kAhead);
+        if constexpr (j + kAhead == kJ) {
+          read_rope(0);
+          read_rope(1);
         }
+        const u32x4 x = a[j % (kAhead + 1)][0], y = a[j % (kAhead + 1)][1];
+        const i32x8 k = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+        s = mfma_codes<0, 0>(k, qh[j], s, ks, q_scale[2 * j / kJ]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(staging)::value) {
+          unrolled<kEach>([&](auto z) { piece(g, std::integral_constant<int, kEach * j + decltype(z)::value>{}); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        s = mfma_codes<0, 1>(k, ql[j], s, ks, q_scale[2 * j / kJ]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ra[0], rq[0], s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ra[1], rq[1], s, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      read_rope(2);
+      read_rope(3);
+      if constexpr (decltype(staging)::value) {
+        unrolled<2 * kEach>([&](auto z) { piece(g, std::integral_constant<int, kEach * kJ + decltype(z)::value>{}); });
       }
-      if (bad || t0 + kKeyTile > see.all_hi) {
-        asm volatile("");   // a branch
+      __builtin_amdgcn_sched_barrier(0);
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ra[0], rq[0], s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ra[1], rq[1], s, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      at_end();
+      return s;
+    };
+    auto hide = [&](f32x16& s, int32_t tile, const Pages& x) {
+      const int32_t hi = pick(x, k0 >> 4) >= 0 ? row_hi - tile * kKeyTile - k0 : 0;
 #pragma unroll
-        for (int v = 0; v < kU; ++v) {
-          const int32_t k0 = 32 * (S == 2 ? part : v) + 16 * half;
-          const int32_t hi = pick(mine, k0 >> 4) >= 0 ? row_hi - t0 - k0 : 0;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[v][e] = e < hi ? s[v][e] : -INFINITY;
-        }
+      for (int e = 0; e < 16; ++e) s[e] = e < hi ? s[e] : -INFINITY;
+    };
+    // Weights of this wave's keys, written for both waves: in 16 parts, one
+    // behind each product of the sums.
+    struct Weigh {
+      f32x16 s;
+      float top, was, base, most, sum, ws;
+      f32x4 scale[2];
+      int32_t e;
+      u32x4 hi, lo;
+    };
+    auto weigh = [&](Weigh& x, const uint8_t* from, LatentWeights& to, auto which) {
+      constexpr int n = decltype(which)::value;
+      // scales of four keys, two parts ahead
+      if constexpr (n == 1 || n == 3 || n == 5 || n == 7) {
+        x.scale[(n >> 1) & 1] = *(const f32x4*)(from + Tile::kCodes + Tile::kRopes + 4 * k0 + 16 * (n >> 1));
       }
-      // weights
-      float top = -INFINITY;
+      if constexpr (n == 0) {
+        x.top = x.s[0];
 #pragma unroll
-      for (int v = 0; v < kU; ++v) {
+        for (int e = 1; e < 16; ++e) x.top = fmaxf(x.top, x.s[e]);
+        asm volatile("" : "+v"(x.top));
+      } else if constexpr (n == 1) {
+        x.top = half_max(x.top) * factor;
+        // The maximum follows when weights would pass 2^32: their scale goes with
+        // them, and sums are floats.
+        x.was = m;
+        m = x.top > m + kRise ? __builtin_ceilf(x.top) : m;
+        asm volatile("" : "+v"(m));
+      } else if constexpr (n == 2) {
+        l *= x.was == m ? 1.0f : __builtin_amdgcn_exp2f(x.was - m);
+        x.base = m == -INFINITY ? 0.0f : m;
+        x.most = x.sum = 0.0f;
+        asm volatile("" : "+v"(l), "+v"(x.base));
+      } else if constexpr (n < 11) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[v][e]);
-      }
-      const float factor = fmaxf(scale, kTiny);
-      top = half_max(top) * factor;
-      if (__ballot(top > m + 8.0f) != 0) {
-        const float to = fmaxf(m, __builtin_ceilf(top));
-        const float g = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-        m = to;
-        l *= g;
-        if constexpr (S == 1) {
-#pragma unroll
-          for (int i = 0; i < kO; ++i) o[i] *= g;
+        for (int z = 0; z < 2; ++z) {
+          constexpr int e0 = 2 * (n - 3);
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x.s[e0 + z], factor, -x.base));
+          x.sum += w;
+          x.s[e0 + z] = w * x.scale[(e0 >> 2) & 1][(e0 & 3) + z];
         }
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      uint32_t wh[kU][4], wl[kU][4];
-      int32_t we[kU];
-#pragma unroll
-      for (int v = 0; v < kU; ++v) {
-        const int32_t k0 = 32 * (S == 2 ? part : v) + 16 * half;
-        float w[16], most = 0.0f;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const f32x4 sc = *(const f32x4*)(scales + k0 + 4 * y);
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int e = 4 * y + z;
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v][e], factor, -base));
-            l += x;
-            w[e] = x * __uint_as_float(__float_as_uint(sc[z]) & 0x7F800000u);
-            most = fmaxf(most, w[e]);
-          }
-        }
-        we[v] = split_exponent(half_max(most));
-        const float ws = exponent_scale(we[v]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          wh[v][y] = wl[v][y] = 0;
-          split2(w[4 * y], w[4 * y + 1], ws, wh[v][y], wl[v][y], false);
-          split2(w[4 * y + 2], w[4 * y + 3], ws, wh[v][y], wl[v][y], true);
-        }
-      }
-      i32x8 ph, pl;
-      int32_t p_scale;
-      if constexpr (S == 1) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            ph[4 * v + y] = (int32_t)wh[v][y];
-            pl[4 * v + y] = (int32_t)wl[v][y];
-          }
-        }
-        p_scale = half ? we[1] : we[0];
+        x.most = fmaxf(fmaxf(x.most, x.s[2 * (n - 3)]), x.s[2 * (n - 3) + 1]);
+        asm volatile("" : "+v"(x.most), "+v"(x.sum));
+      } else if constexpr (n == 11) {
+        l += x.sum;
+        x.e = split_exponent(half_max(x.most));
+        x.ws = exponent_scale(x.e);
+        asm volatile("" : "+v"(x.ws));
       } else {
-        Weights& to = ex[wave];
-        to.hi[lane] = u32x4{wh[0][0], wh[0][1], wh[0][2], wh[0][3]};
-        to.lo[lane] = u32x4{wl[0][0], wl[0][1], wl[0][2], wl[0][3]};
-        if (half == 0) {
-          to.m[col] = m;
-          to.e[col] = we[0];
+        constexpr int y = n - 12;
+        uint32_t a = 0, b = 0;
+        split2(x.s[4 * y], x.s[4 * y + 1], x.ws, a, b, false);
+        split2(x.s[4 * y + 2], x.s[4 * y + 3], x.ws, a, b, true);
+        asm volatile("" : "+v"(a), "+v"(b));
+        x.hi[y] = a;
+        x.lo[y] = b;
+        if constexpr (n == 15) {
+          to.hi[lane] = x.hi;
+          to.lo[lane] = x.lo;
+          if (half == 0) {
+            to.m[col] = m;
+            to.e[col] = x.e;
+          }
         }
-        lds_written();
-        const Weights& w0 = ex[wave & ~1];
-        const Weights& w1 = ex[wave | 1];
-        const float m0 = w0.m[col], m1 = w1.m[col], both = fmaxf(m0, m1);
-        if (__ballot(both > ref + 8.0f) != 0) {
-          const float to_ref = fmaxf(ref, both);
-          const float g = to_ref == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ref - to_ref);
-          ref = to_ref;
+      }
+    };
+    // Both waves' weights, and what they are taken from.
+    struct Both {
+      i32x8 h, l;
+      float m0, m1;
+      int32_t e, scale;
+    };
+    auto gather = [&](const LatentWeights* w) {
+      const LatentWeights& w0 = w[wave & ~1];
+      const LatentWeights& w1 = w[wave | 1];
+      Both x;
+      x.m0 = w0.m[col];
+      x.m1 = w1.m[col];
+      // The second 16 bytes of both halves, the odd wave's, have the upper half's scale.
+      x.e = (half ? w1 : w0).e[col];
+      const u32x4 h0 = w0.hi[lane], h1 = w1.hi[lane], l0 = w0.lo[lane], l1 = w1.lo[lane];
 #pragma unroll
-          for (int i = 0; i < kO; ++i) o[i] *= g;
-        }
-        const u32x4 h0 = w0.hi[lane], h1 = w1.hi[lane], l0 = w0.lo[lane], l1 = w1.lo[lane];
+      for (int y = 0; y < 4; ++y) {
+        x.h[y] = (int32_t)h0[y];
+        x.h[4 + y] = (int32_t)h1[y];
+        x.l[y] = (int32_t)l0[y];
+        x.l[4 + y] = (int32_t)l1[y];
+      }
+      return x;
+    };
+    auto follow = [&](Both& x) {
+      const float top = fmaxf(x.m0, x.m1), was = ref;
+      const bool rise = top > ref + kRise;
+      ref = rise ? top : ref;
+      // sums without a maximum yet are zeros, or no numbers
+      if (__builtin_expect(__ballot(rise && was > -INFINITY) != 0, 0)) {
+        const float g = rise && was > -INFINITY ? __builtin_amdgcn_exp2f(was - ref) : 1.0f;
+        acc_wait(o);
+        unrolled<kO>([&](auto i) { Acc<decltype(i)::value>::scale(o[decltype(i)::value], g); });
+        acc_wait(o);
+      }
+      // Weights without a maximum are zeros or no numbers.
+      const float mm = half ? x.m1 : x.m0;
+      const float by = mm == -INFINITY ? 0.0f : fmaxf(mm - ref, -256.0f);
+      const int32_t e = min(max(x.e + (int32_t)by, kLoShift), 254);
+      x.scale = e | ((e - kLoShift) << 8);
+    };
+    // The weighted sums of a tile, and between its products what `between` does
+    // in 16 parts.
+    auto add = [&](const uint8_t* from, const Both& x, auto&& between) {
+      constexpr int kAhead = 1, kParts = 8 / kO;
+      i32x8 v[kAhead + 1];
+      const uint32_t v_now = v_at + lds_of(from);
+      const auto read = [&](int i) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          ph[y] = (int32_t)h0[y];
-          ph[4 + y] = (int32_t)h1[y];
-          pl[y] = (int32_t)l0[y];
-          pl[4 + y] = (int32_t)l1[y];
+          const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2*)(lds + (v_now ^ (2 * i * 16)) + (32 * (y >> 1) + 8 * (y & 1)) * L));
+          v[i % (kAhead + 1)][2 * y] = t[0];
+          v[i % (kAhead + 1)][2 * y + 1] = t[1];
         }
-        // weights of a block without a maximum are zeros or no numbers
-        const float mm = half ? m1 : m0;
-        const float by = mm == -INFINITY ? 0.0f : fmaxf(mm - ref, -256.0f);
-        p_scale = min(max((half ? w1.e[col] : w0.e[col]) + (int32_t)by, kLoShift), 254);
-      }
-      p_scale |= (p_scale - kLoShift) << 8;
+      };
+      read(0);
+      __builtin_amdgcn_sched_barrier(0);
+      unrolled<kO>([&](auto step) {
+        constexpr int i = decltype(step)::value;
+        Acc<i>::add_hi(o[i], v[i % (kAhead + 1)], x.h, 127, x.scale);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (i + kAhead < kO) read(i + kAhead);
+        unrolled<kParts>([&](auto z) { between(std::integral_constant<int, 2 * kParts * i + decltype(z)::value>{}); });
+        __builtin_amdgcn_sched_barrier(0);
+        Acc<i>::add_lo(o[i], v[i % (kAhead + 1)], x.l, 127, x.scale);
+        __builtin_amdgcn_sched_barrier(0);
+        unrolled<kParts>(
+            [&](auto z) { between(std::integral_constant<int, 2 * kParts * i + kParts + decltype(z)::value>{}); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    const auto nothing = [](auto) {};
 
-      // the weighted sum
-#pragma unroll
-      for (int i = 0; i < kO; ++i) {
-        const int32_t tile_of = i + part * kO;
-        i32x8 v;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int32_t key = 32 * (y >> 1) + 16 * half + 8 * (y & 1) + ((lane & 15) >> 1);
-          const int32_t chunk = 2 * tile_of + ((lane >> 4) & 1);
-          const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(
-              from + key * L + (chunk ^ code_turn(key)) * 16 + 8 * (lane & 1)));
-          v[2 * y] = x[0];
-          v[2 * y + 1] = x[1];
+    if (see.tile0 <= last) {
+      int32_t slot = 0, tile = see.tile0;
+      // kEdge: tiles that not every row sees all of, or the last one; kFirst: no
+      // sums are due yet.
+      const auto step = [&](auto first, auto edge) {
+        constexpr bool kFirst = decltype(first)::value, kEdge = decltype(edge)::value;
+        const int32_t after = slot + 1 == kSlots ? 0 : slot + 1, ahead = slot == 0 ? kSlots - 1 : slot - 1;
+        uint8_t* from = lds + slot * Tile::kBytes;
+        lds_arrived();
+        const Pages mine = now;
+        if constexpr (kEdge) {
+          if (bad(mine) || (tile + 1) * kKeyTile > see.see_hi) clear(from, tile, mine);
         }
-        o[i] = mfma_codes<0, 0>(v, ph, o[i], 127, p_scale);
-        o[i] = mfma_codes<0, 1>(v, pl, o[i], 127, p_scale);
+        now = pages(min(tile + 1, last));
+        Both x;
+        const auto at_end = [&] {
+          if constexpr (kDeep && !kFirst) x = gather(ex[(tile + 1) & 1]);
+        };
+        Weigh w;
+        if constexpr (kEdge) {
+          if (tile < last) {
+            const Stage g = plan(tile + 1, after, now);
+            unrolled<kPieces>([&](auto n) { piece(g, n); });
+          }
+          w.s = scores(from, Stage{}, std::false_type{}, at_end);
+          if (tile < last) fetch_rope(tile + 1, now);
+          hide(w.s, tile, mine);
+        } else {
+          w.s = scores(from, plan(tile + 1, after, now), std::true_type{}, at_end);
+          fetch_rope(tile + 1, now);
+        }
+        if constexpr (kDeep) {
+          // The products of the tile before, and between them this tile's weights.
+          const auto part_of = [&](auto n) { weigh(w, from, ex[tile & 1][wave], n); };
+          if constexpr (kFirst) {
+            unrolled<16>(part_of);
+          } else {
+            follow(x);
+            add(lds + ahead * Tile::kBytes, x, part_of);
+          }
+        } else {
+          unrolled<16>([&](auto n) { weigh(w, from, ex[0][wave], n); });
+          lds_written();
+          x = gather(ex[0]);
+          follow(x);
+          add(from, x, nothing);
+        }
+        slot = after;
+        ++tile;
+      };
+      if constexpr (kDeep) step(std::true_type{}, std::true_type{});
+      while (tile <= last) {
+        while (tile < last && (tile + 1) * kKeyTile <= see.all_hi && !bad(now)) step(std::false_type{}, std::false_type{});
+        step(std::false_type{}, std::true_type{});
       }
+      if constexpr (kDeep) {
+        lds_written();
+        Both x = gather(ex[last & 1]);
+        follow(x);
+        add(lds + (slot == 0 ? kSlots - 1 : slot - 1) * Tile::kBytes, x, nothing);
+      }
+      acc_wait(o);
     }
 
+    // The pair's sums, over one maximum.
     l += __shfl_xor(l, 32);
-    if constexpr (S == 2) {
-      // the pair's sums, over one maximum
-      lds_written();
-      Weights& to = ex[wave];
-      if (half == 0) {
-        to.m[col] = m;
-        to.e[col] = __float_as_int(l);
-      }
-      lds_written();
-      const Weights& w0 = ex[wave & ~1];
-      const Weights& w1 = ex[wave | 1];
+    lds_written();
+    if (half == 0) {
+      ex[0][wave].m[col] = m;
+      ex[0][wave].e[col] = __float_as_int(l);
+    }
+    lds_written();
+    {
+      const LatentWeights& w0 = ex[0][wave & ~1];
+      const LatentWeights& w1 = ex[0][wave | 1];
       const float f0 = w0.m[col] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(w0.m[col] - ref);
       const float f1 = w1.m[col] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(w1.m[col] - ref);
       l = __int_as_float(w0.e[col]) * f0 + __int_as_float(w1.e[col]) * f1;
-      m = ref;
     }
     const bool writes = live && half == 0 && part == 0;
     const int64_t item = row * p.group + head;
+    const int32_t in_share = sub * R + r_in;
     if (wk.parts > 1) {
-      const int64_t at = (int64_t)wk.slot * R + r_in;
+      const int64_t at = (int64_t)wk.slot * p.tile_rows + in_share;
       if (live) {
         float* to = p.part + at * L + 32 * kO * part + 4 * half;
 #pragma unroll
         for (int i = 0; i < kO; ++i) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            *(f32x4*)(to + 32 * i + 8 * e) = f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+            *(f32x4*)(to + 32 * i + 8 * e) = f32x4{acc_read(o[i][4 * e]), acc_read(o[i][4 * e + 1]),
+                                                   acc_read(o[i][4 * e + 2]), acc_read(o[i][4 * e + 3])};
           }
         }
       }
-      if (writes) p.part_ml[at] = kv_part_ml(m, l);
+      if (writes) p.part_ml[at] = kv_part_ml(ref, l);
     } else {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       if (live) {
@@ -601,14 +854,14 @@ __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatc
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             *(bf16x4*)(to + 32 * i + 8 * e) =
-                bf16x4{(__bf16)(o[i][4 * e] * inv), (__bf16)(o[i][4 * e + 1] * inv), (__bf16)(o[i][4 * e + 2] * inv),
-                       (__bf16)(o[i][4 * e + 3] * inv)};
+                bf16x4{(__bf16)(acc_read(o[i][4 * e]) * inv), (__bf16)(acc_read(o[i][4 * e + 1]) * inv),
+                       (__bf16)(acc_read(o[i][4 * e + 2]) * inv), (__bf16)(acc_read(o[i][4 * e + 3]) * inv)};
           }
         }
       }
-      if (writes && p.lse) p.lse[item] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+      if (writes && p.lse) p.lse[item] = l == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
     }
-    if (writes && wk.begin && p.rows) p.rows[item] = int2{wk.slot * R + r_in, wk.parts};
+    if (writes && wk.begin && p.rows) p.rows[item] = int2{wk.slot * p.tile_rows + in_share, wk.parts};
   }
 }
 
