@@ -8,6 +8,7 @@
 namespace {
 
 constexpr int32_t kLatentMaxHeads = 1024;
+constexpr int64_t kPromptMaxStride = int64_t{1} << 23;   // of keys and values, elements
 
 // The buffers of a cache.
 struct LatentBuffers {
@@ -340,6 +341,10 @@ int fp8bq_latent_prompt_attention(const fp8bq_latent_prompt* p, void* stream) {
                             {{p->k_rope, p->k_rope_token_stride, 1, 0}, fp8bq::kRope},
                             {{p->v, p->v_token_stride, p->heads, p->v_head_stride}, D}};
   if (!q.ok() || !out.ok() || !out.distinct(p->tokens)) return FP8BQ_ERR_INVALID_ARGUMENT;
+  // places of a tile's rows stay in 32 bits
+  for (const int64_t pitch : {p->k_token_stride, p->k_rope_token_stride, p->v_token_stride}) {
+    if (pitch >= kPromptMaxStride) return FP8BQ_ERR_INVALID_ARGUMENT;
+  }
   const uint64_t out_bytes = out.extent(p->tokens);
   const uint64_t lse_bytes = p->lse ? 4 * static_cast<uint64_t>(p->tokens) * static_cast<uint64_t>(p->heads) : 0;
   const uint64_t starts = 4 * (static_cast<uint64_t>(p->count) + 1);

@@ -22,6 +22,23 @@ struct PromptQuery {
   float scale;             // of the scores, times log2(e)
 };
 
+// The scores of 64 keys, their softmax with a running maximum, the weighted sum
+// of the values: both products on the matrix units, K Q and V W, so that a lane
+// holds one query's scores and its weights are operands where they lie.  A wave
+// holds 32 queries; W = 4 of them share the tiles in LDS, which loads put there
+// past the registers while the tile before is worked on, and two such workgroups
+// share a CU: one's products run while the other takes exponentials, and the
+// priority that a wave has within its products keeps them taking turns.  What
+// bounds it: a wave reads the whole tile, 40 KB, for 32 rows, which keeps LDS
+// busy for as long as the products take.
+//
+// Two prompts of 4096 tokens, 32 heads of 128 channels, 344 GFLOP: 322 us, 1070
+// TFLOP/s (a large BF16 matrix product reaches 1330); operands read when they
+// were wanted 335, without the priorities 333, a lane's place in a tile worked
+// out for every load 349.  Waves of 64 queries, one to a SIMD, with the weights
+// of 32 keys between the products of the next, halve LDS's traffic and take 520:
+// a wave alone does not keep both units busy.
+//
 // A workgroup takes R = 32 W query tokens of one head.  Slot w of the grid
 // belongs to the sequence with floor(q_at[b] / R) + b <= w, which leaves every
 // sequence as many slots as it has row tiles, whatever the offsets are.
@@ -48,11 +65,11 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
   const int64_t local = w_item - (__builtin_amdgcn_readfirstlane((int32_t)(row0 / R)) + (int64_t)b);
   if (local < 0 || local >= tiles) return;
   const int32_t first = (tiles - 1 - (int32_t)local) * R;   // the last rows see the most keys: they go first
-  const int32_t r_in = first + wave * 32 + col;
-  const bool live = r_in < n;
-  const int64_t row = row0 + min(r_in, n - 1);
+  const int32_t r_mine = first + wave * 32 + col;
+  const bool live = r_mine < n;
+  const int64_t row = row0 + min(r_mine, n - 1);
   const int64_t before = (int64_t)keys - n;                 // keys in front of the first query's own
-  const int32_t row_hi = live ? (int32_t)max(before + r_in + 1, (int64_t)0) : 0;
+  const int32_t row_hi = live ? (int32_t)max(before + r_mine + 1, (int64_t)0) : 0;
   const int32_t see_hi = (int32_t)max(before + min(first + R, n), (int64_t)0);
   const int32_t all_hi = (int32_t)max(before + first + 1, (int64_t)0);
   const int32_t last = (see_hi + kKeyTile - 1) / kKeyTile - 1;
@@ -66,23 +83,43 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
   const auto turn_k = [](int32_t key) { return kC == 16 ? key & 15 : (key >> 1) & 7; };
   const auto turn_r = [](int32_t key) { return (key >> 1) & 7; };
   const auto turn_v = [](int32_t key) { return kC == 16 ? (key & 3) << 2 : ((key >> 1) & 1) << 2; };
-  // Keys behind the last one that is seen count as that one.
+  // A row's place in a tile goes with the lane, for every instruction of a wave
+  // the same (16 or 32 rows on, the exchange is): what advances is the base, in
+  // scalar registers.  Of the last tile, keys behind the last one that is seen
+  // count as that one.
+  constexpr int kKeys = 64 / kC;                  // of an instruction
+  const int32_t key_in = wave * kKeys + lane / kC, r_in8 = wave * 8 + (lane >> 3);
+  const int32_t k_pitch = (int32_t)p.k_tok * 2, v_pitch = (int32_t)p.v_tok * 2, r_pitch = (int32_t)p.r_tok * 2;
+  const int32_t k_off = ((lane % kC) ^ turn_k(key_in)) * 16, v_off = ((lane % kC) ^ turn_v(key_in)) * 16;
+  const int32_t r_off = ((lane & 7) ^ turn_r(r_in8)) * 16;
+  const uint32_t k_in = key_in * k_pitch + k_off, v_in = key_in * v_pitch + v_off, r_in = r_in8 * r_pitch + r_off;
   const auto stage = [&](int32_t tile, int32_t slot) {
     const uint32_t to = lds0 + slot * kBytes;
     const int32_t t0 = tile * kKeyTile, end = see_hi - 1 - t0;
-    constexpr int kKeys = 64 / kC;   // of an instruction
+    const uint8_t* kb = kp + t0 * (p.k_tok * 2);
+    const uint8_t* vb = vp + t0 * (p.v_tok * 2);
+    const uint8_t* rb = rp + t0 * (p.r_tok * 2);
+    const bool whole = end >= kKeyTile - 1;
 #pragma unroll
     for (int i = 0; i < 64 / kKeys / W; ++i) {
-      const int32_t k0 = (i * W + wave) * kKeys, key = k0 + lane / kC;
-      const int64_t at = t0 + min(key, end);
-      lds_load16_at(kp + at * p.k_tok * 2 + ((lane % kC) ^ turn_k(key)) * 16, to + k0 * 2 * D);
-      lds_load16_at(vp + at * p.v_tok * 2 + ((lane % kC) ^ turn_v(key)) * 16, to + kK + kR + k0 * 2 * D);
+      const int32_t k0 = i * W * kKeys, at = to + (k0 + wave * kKeys) * 2 * D;
+      if (whole) {
+        lds_load16(kb + k0 * (int64_t)k_pitch, k_in, at);
+        lds_load16(vb + k0 * (int64_t)v_pitch, v_in, at + kK + kR);
+      } else {
+        const int32_t key = min(k0 + key_in, end);
+        lds_load16(kb, key * k_pitch + k_off, at);
+        lds_load16(vb, key * v_pitch + v_off, at + kK + kR);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 8 / W; ++i) {
-      const int32_t k0 = (i * W + wave) * 8, key = k0 + (lane >> 3);
-      const int64_t at = t0 + min(key, end);
-      lds_load16_at(rp + at * p.r_tok * 2 + ((lane & 7) ^ turn_r(key)) * 16, to + kK + k0 * 128);
+      const int32_t k0 = i * W * 8, at = to + kK + (k0 + wave * 8) * 128;
+      if (whole) {
+        lds_load16(rb + k0 * (int64_t)r_pitch, r_in, at);
+      } else {
+        lds_load16(rb, min(k0 + r_in8, end) * r_pitch + r_off, at);
+      }
     }
   };
   if (last >= 0) stage(0, 0);
@@ -115,22 +152,33 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
       lds_written();
     }
     if (tile < last) stage(tile + 1, slot ^ 1);
+    __builtin_amdgcn_s_setprio(1);
     f32x16 s[2];
+    s[0] = f32x16{};
+    s[1] = f32x16{};
+    {
+      // operands of 16 channels, two steps ahead
+      bf16x8 ring[4][2];
+      const auto get = [&](int j) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int32_t key = 32 * u + col;
-      s[u] = f32x16{};
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const bf16x8 a = *(const bf16x8*)(from + key * 2 * D + ((2 * j + half) ^ turn_k(key)) * 16);
-        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[j], s[u], 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8 a = *(const bf16x8*)(from + kK + key * 128 + ((2 * j + half) ^ turn_r(key)) * 16);
-        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[kJ + j], s[u], 0, 0, 0);
-      }
+        for (int u = 0; u < 2; ++u) {
+          const int32_t key = 32 * u + col;
+          ring[j & 3][u] = j < kJ ? *(const bf16x8*)(from + key * 2 * D + ((2 * j + half) ^ turn_k(key)) * 16)
+                                  : *(const bf16x8*)(from + kK + key * 128 + ((2 * (j - kJ) + half) ^ turn_r(key)) * 16);
+        }
+      };
+      get(0);
+      get(1);
+      __builtin_amdgcn_sched_barrier(0);
+      unrolled<kJ + 4>([&](auto step) {
+        constexpr int j = decltype(step)::value;
+        if constexpr (j + 2 < kJ + 4) get(j + 2);
+        s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j & 3][0], q[j], s[0], 0, 0, 0);
+        s[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[j & 3][1], q[j], s[1], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
+    __builtin_amdgcn_s_setprio(0);
     if (t0 + kKeyTile > all_hi) {
       asm volatile("");   // a branch
 #pragma unroll
@@ -166,25 +214,34 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
         w[2 * u + (e >> 3)][e & 7] = (__bf16)x;
       }
     }
+    __builtin_amdgcn_s_setprio(1);
     // Lane half x holds, of each 16 keys, 4 x .. 4 x + 3 and 8 + 4 x .. 8 + 4 x + 3.
-#pragma unroll
-    for (int i = 0; i < kO; ++i) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        bf16x8 a;
+    {
+      bf16x8 ring[4];   // three steps ahead
+      const auto get = [&](int n) {
         s16x4 x[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int32_t key = 16 * t + 8 * y + 4 * half + ((lane & 15) >> 2);
-          const int32_t chunk = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+          const int32_t key = 16 * (n / kO) + 8 * y + 4 * half + ((lane & 15) >> 2);
+          const int32_t chunk = 4 * (n % kO) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
           x[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
               from + kK + kR + key * 2 * D + (chunk ^ turn_v(key)) * 16 + 8 * (lane & 1)));
         }
         const auto both = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        a = __builtin_bit_cast(bf16x8, both);
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[t], o[i], 0, 0, 0);
-      }
+        ring[n & 3] = __builtin_bit_cast(bf16x8, both);
+      };
+      get(0);
+      get(1);
+      get(2);
+      unrolled<4 * kO>([&](auto step) {
+        constexpr int n = decltype(step)::value;
+        if constexpr (n + 3 < 4 * kO) get(n + 3);
+        o[n % kO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[n & 3], w[n / kO], o[n % kO], 0, 0, 0);
+        // (the first of them among the weights' instructions, as they come)
+        if constexpr (n >= kO) __builtin_amdgcn_sched_barrier(0);
+      });
     }
+    __builtin_amdgcn_s_setprio(0);
   }
   l += __shfl_xor(l, 32);
   if (!live) return;

@@ -614,7 +614,8 @@ int fp8bq_latent_attention(const fp8bq_latent_cache* cache, const fp8bq_kv_batch
                            void* stream);
 
 /* A call in the expanded form.  Rows are BF16, contiguous, 16-byte aligned;
- * strides are in elements, multiples of 8 and below 2^36. */
+ * strides are in elements, multiples of 8 and below 2^36, token strides of k,
+ * k_rope and v below 2^23. */
 typedef struct fp8bq_latent_prompt {
   const void* q;        /* [tokens, heads, head_dim + 64]: the rotated channels last */
   const void* k;        /* [keys, heads, head_dim] */

@@ -26,17 +26,17 @@ def cache(c=C, r=R, scale=SC, pages=100, size=64, dim=512):
     return latent._CACHE.pack(c, r, scale, pages, size, dim)
 
 
-def tokens(c=X, r=XR, r_out=RO, q=Q, q_out=QO, cos=CO, sin=SI, strides=(576, 576, 64, 3072, 192, 1024, 64), tokens=9,
+def tokens(c=X, r=XR, r_out=RO, q=Q, q_out=QO, cos=CO, sin=SI, strides=(576, 576, 64, 3200, 192, 1024, 64), tokens=9,
            positions=4096, heads=16, interleaved=0):
     return latent._TOKENS.pack(c, r, r_out, q, q_out, cos, sin, *strides, tokens, positions, heads, interleaved)
 
 
-def query(q=Q, r=QO, out=OUT, lse=0, strides=(512, 4608, 3072, 192, 8192, 512), tokens=9, heads=16, scale=0.1):
+def query(q=Q, r=QO, out=OUT, lse=0, strides=(512, 4608, 3200, 192, 8192, 512), tokens=9, heads=16, scale=0.1):
     return latent._QUERY.pack(q, r, out, lse, *strides, tokens, heads, scale)
 
 
 def prompt(q=Q, k=X, r=XR, v=X + 256, out=OUT, lse=0, q_at=CO, k_at=SI,
-           strides=(3072, 192, 4096, 256, 64, 4096, 256, 2048, 128), tokens=9, keys=20, heads=16, dim=128, count=2, scale=0.1):
+           strides=(3200, 192, 4096, 256, 64, 4096, 256, 2048, 128), tokens=9, keys=20, heads=16, dim=128, count=2, scale=0.1):
     return latent._PROMPT.pack(q, k, r, v, out, lse, q_at, k_at, *strides, tokens, keys, heads, dim, count, scale)
 
 
@@ -63,7 +63,7 @@ def strides(base, **at):
     return tuple(at.get(f"s{i}", x) for i, x in enumerate(base))
 
 
-T = (576, 576, 64, 3072, 192, 1024, 64)
+T = (576, 576, 64, 3200, 192, 1024, 64)
 
 
 @no_gpu
@@ -89,13 +89,13 @@ def test_tokens_that_pass(what=None):
     tensor: these get as far as looking for a device."""
     lib = fq.load_library()
     for good in (dict(), dict(r_out=0), dict(q=0, q_out=0), dict(cos=0, sin=0), dict(r_out=XR, strides=strides(T, s2=576)),
-                 dict(q_out=Q, strides=strides(T, s5=3072, s6=192)), dict(positions=0), dict(tokens=9, heads=1024,
+                 dict(q_out=Q, strides=strides(T, s5=3200, s6=192)), dict(positions=0), dict(tokens=9, heads=1024,
                  strides=strides(T, s3=192 * 1024, s5=65536)),
                  dict(c=X, r=X + 1024, r_out=X + 1024, strides=strides(T, s2=576))):
         assert lib.fp8bq_latent_append(cache(), batch(), tokens(**good), None) == fq.ERR_HIP, good
 
 
-A = (512, 4608, 3072, 192, 8192, 512)
+A = (512, 4608, 3200, 192, 8192, 512)
 
 
 @no_gpu
@@ -128,14 +128,15 @@ def test_workspace():
     assert lib.fp8bq_latent_attention(cache(), batch(count=0, starts=0), query(tokens=0), None, 0, None) == fq.OK
 
 
-P = (3072, 192, 4096, 256, 64, 4096, 256, 2048, 128)
+P = (3200, 192, 4096, 256, 64, 4096, 256, 2048, 128)
 
 
 @no_gpu
 @pytest.mark.parametrize("bad", [
     dict(q=0), dict(k=0), dict(r=0), dict(v=0), dict(out=0), dict(q_at=0), dict(q=Q + 8), dict(k=X + 2), dict(r=XR + 4),
     dict(v=X + 248), dict(out=OUT + 8), dict(lse=LSE + 1), dict(q_at=CO + 2), dict(k_at=SI + 1), dict(k_at=0),
-    dict(strides=strides(P, s0=3070)), dict(strides=strides(P, s2=-8)), dict(strides=strides(P, s4=1 << 36)),
+    dict(strides=strides(P, s0=3198)), dict(strides=strides(P, s2=-8)), dict(strides=strides(P, s4=1 << 36)),
+    dict(strides=strides(P, s2=1 << 23)), dict(strides=strides(P, s4=1 << 23)), dict(strides=strides(P, s5=1 << 23)),
     dict(strides=strides(P, s7=0)), dict(strides=strides(P, s8=120)), dict(tokens=-1), dict(keys=-1), dict(count=-1),
     dict(count=1 << 21), dict(heads=0), dict(heads=1025), dict(dim=96), dict(dim=192), dict(tokens=1 << 25),
     dict(keys=1 << 25), dict(scale=float("nan")), dict(scale=float("inf")), dict(out=Q), dict(out=X), dict(out=X + 4096),
