@@ -93,15 +93,26 @@ struct LatentShape {
   size_t rows_at, ml_at, bytes;   // workspace: partial sums at 0, then these
 };
 
+// Figures below: us of a step over L = 512, 8000 tokens a sequence where not said.
 LatentShape latent_shape(const fp8bq_latent_cache& c, const fp8bq_kv_batch& b, int32_t heads, int64_t tokens) {
   LatentShape s;
+  // One pair of waves, two workgroups to a CU, as long as a sequence's rows fit in
+  // it, else two pairs that share the keys: 96 sequences of 16 rows 116 and 139, of
+  // 32 rows 125 and 131; 60 of 40 rows 106 and 91, of 64 rows 113 and 99.
+  // Where rows need more workgroups than one, these take the same keys side by
+  // side on one XCD, whose cache serves all but the first: 60 sequences of 128
+  // rows 155 -> 151, 30 of 256 rows 144 -> 140.
   const int64_t per_seq = ceil_div(tokens * heads, b.count);
   s.rows = per_seq <= 32 ? 32 : 64;
   s.subs = per_seq <= 64 ? 1 : (per_seq <= 128 ? 2 : 4);
   const int64_t row_tiles = tokens * heads / (s.rows * s.subs) + b.count;
   const int64_t key_tiles = ceil_div(static_cast<int64_t>(b.max_pages) * c.page_size, 64);
-  s.target = (s.rows == 32 ? 512 : 256) / s.subs;
-  if (key_tiles <= 2) s.target = 0;
+  s.target = (s.rows == 32 ? 512 : 256) / s.subs;   // one round of workgroups
+  // Short tables leave nothing to cut up: without shares, their partial sums and
+  // the join, steps at 200 tokens (4 tiles) of 96 sequences take 18 instead of 24
+  // at 16 heads and 24 instead of 53 at 128, one sequence 17.1 instead of 16.5; at
+  // 500 tokens (8 tiles) 96 sequences 26 either way, one 24 instead of 17.
+  if (key_tiles <= 4) s.target = 0;
   s.grid = static_cast<int32_t>(s.target ? s.target : ceil_div(row_tiles, 8) * 8) * s.subs;
   s.slots = 2 * s.target;
   s.ml_at = s.rows_at = s.bytes = 0;
@@ -123,7 +134,7 @@ void latent_launch(const LatentShape& s, const fp8bq::LatentCache& c, const fp8b
     hipLaunchKernelGGL((fp8bq::latent_attend<L, 4>), grid, dim3(256), 0, st, c, b, q);
   }
   if (s.target == 0) return;
-  if (rows <= 1024) {
+  if (rows <= 1024) {   // as for the key/value cache
     hipLaunchKernelGGL((fp8bq::kv_attend_join<L, 8>), dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, b, q.k, 1,
                        s.rows * s.subs);
   } else {
@@ -209,7 +220,10 @@ int fp8bq_latent_append(const fp8bq_latent_cache* cache, const fp8bq_kv_batch* b
   hipStream_t st = static_cast<hipStream_t>(stream);
   const auto launch = [&](auto dim) {
     constexpr int L = decltype(dim)::value;
-    if (d.heads > 24) {
+    // Four waves to a token from 24 heads on, below that one: 17,000 tokens with 8,
+    // 16, 24, 32 and 128 heads take 22, 26, 28, 35 and 116 us with four, 18, 25,
+    // 30, 37 and 121 with one; 96 tokens 12 to 13 either way.
+    if (d.heads >= 24) {
       hipLaunchKernelGGL((fp8bq::latent_append<L, 4>), dim3(static_cast<unsigned>(t->tokens)), dim3(fp8bq::kThreads), 0,
                          st, c, b, d);
     } else {
@@ -302,6 +316,10 @@ int fp8bq_latent_attention(const fp8bq_latent_cache* cache, const fp8bq_kv_batch
   d.k.jump = s.target;
   d.k.min_tiles = 1;
   d.k.tile_rows = s.rows * s.subs;
+  // What a row tile costs beyond its key tiles, in key tiles (queries split, sums
+  // written): shares of 96 sequences x 16 heads, 60 x 128 and 64 x 40 heads with
+  // drafts come out at 126, 139 and 59 us without it, 120, 133 and 51 with 3, 119,
+  // 127 and 52 with 5.
   d.k.extra = 4;
   d.subs = s.subs;
   d.k.scale = scale;

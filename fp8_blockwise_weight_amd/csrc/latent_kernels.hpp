@@ -47,7 +47,9 @@ struct LatentTokens {
 //
 // kWaves waves share a token: 64 lanes hold its latent, 8 channels each (L =
 // 512; half the lanes at 256), the others, or all of them later, turn 16
-// channels at a time of the key and of the queries.
+// channels at a time of the key and of the queries.  Bound by memory: 17,633
+// tokens with 128 query heads, 616 MB, 134 us, 4.6 TB/s (a copy reaches 4.9);
+// steps by their launch, 5.5 us of 10.
 template <int L, int kWaves>
 __global__ __launch_bounds__(kThreads) void latent_append(LatentCache c, KvBatch bt, LatentTokens t) {
   const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -126,15 +128,12 @@ struct LatentQuery {
   int32_t subs;          // row tiles that share keys, side by side on one XCD
 };
 
-// 16 bytes a lane (4 with kWord) from memory into LDS, past the registers: lane
-// i's go to lds + 16 i.  Written as assembly because the compiler, which cannot
+// 16 bytes a lane, or 4, from memory into LDS, past the registers: lane i's go to
+// lds + 16 i, lds + 4 i.  Written as assembly because the compiler, which cannot
 // tell one buffer from another, waits for all of them before any read of LDS.
 __device__ __forceinline__ void lds_load16(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory");
-}
-__device__ __forceinline__ void lds_load16_at(const void* at, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(at) : "memory");
 }
 __device__ __forceinline__ void lds_load4(const void* at, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(at) : "memory");
@@ -195,7 +194,8 @@ __device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, con
 // Sums stay in accumulation registers a0 .. a127 from the first product to the
 // last, by name.  Left to itself the compiler moves all of them to other
 // registers and back in every tile, for the sake of the path that scales them
-// once in a while (245 us for what takes 150).  So every use is assembly: the
+// once in a while (96 sequences at 16 heads: 245 us for what then took 150).  So
+// every use is assembly: the
 // products (which need two cycles behind whatever vector instruction wrote their
 // operands), scaling and reading (behind the wait that a product's result needs).
 template <int I>
@@ -297,9 +297,26 @@ __device__ __forceinline__ void unrolled(F&& f) {
   }
 }
 
-// W waves, two of them for 32 query rows: each makes the scores and weights of
-// every other 32 keys, the weights go through LDS, and each sums half the
-// channels.
+// The absorbed form: for 32 query rows, tile by tile of 64 keys, scores Q C, the
+// weights with a running maximum, and the weighted sum of the same C, which is
+// read from memory and from LDS's loads once.
+//
+// W waves, two of them for 32 rows: each makes the scores and weights of every
+// other 32 keys, the weights go through LDS, and each sums half the channels: 32
+// rows of 512 sums and their queries as codes fill what two waves hold of
+// registers.  One wave to a SIMD, so nothing hides a wait but the wave's own
+// order: operands are read a step ahead, the next tile's loads are issued
+// between products, and with four waves the sums run a tile behind the scores,
+// with that tile's weights between their products.  Two waves alone (two
+// workgroups to a CU) take turns instead.
+//
+// What bounds it: up to 32 rows the loads (96 sequences of up to 16,384
+// tokens, 16 heads, 512 MB: 116 us, 4.4 TB/s, of which loading alone takes 98);
+// from 64 rows on the products and what is not hidden between them, 2.2 us a tile
+// of 64 rows by 64 keys (60 sequences of up to 12,000 tokens, 128 heads, 100
+// GFLOP: 130 us, of which 32 are the queries' splitting, the sums' writing and
+// the join).  One wave with all channels of 32 rows, without the exchange,
+// takes 2.0 us for that but 24 us more around it.
 template <int L, int W>
 __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatch bt, LatentQuery lq) {
   constexpr int R = 16 * W, N = 64 * W;

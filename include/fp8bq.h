@@ -526,8 +526,8 @@ int fp8bq_kv_attention(const fp8bq_kv_cache* cache, const fp8bq_kv_batch* batch,
 typedef struct fp8bq_latent_cache {
   void* c;            /* e4m3fn [num_pages, page_size, latent_dim], 16-byte aligned */
   void* r;            /* BF16 [num_pages, page_size, 64], 16-byte aligned */
-  float* scale;       /* fp32 [num_pages, page_size], powers of two from 2^-112 to 2^112 for every
-                         token in use: of another value, its exponent counts alone */
+  float* scale;       /* fp32 [num_pages, page_size], powers of two from 2^-60 to 2^60 for every
+                         token in use: others give unspecified results */
   int64_t num_pages;  /* 1 .. 2^31 - 1 */
   int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256 */
   int32_t latent_dim; /* 256 or 512 */
@@ -560,7 +560,7 @@ typedef struct fp8bq_latent_tokens {
  *   s   = the smallest power of two with 448 * s >= max(max|c|, FP8BQ_EPS)
  *   c   -> e4m3fn(clamp(c / s, -448, 448)), nearest, ties to even; s is its scale
  * A token's codes depend on nothing but the token.  Values must be finite: a
- * token with others gets unspecified codes.  Tokens whose page is none, or lies
+ * token with others gets unspecified codes (and attention wants them below 2^68).  Tokens whose page is none, or lies
  * beyond the table, are not stored, but rotated; those at negative positions, at
  * positions without a row of cos and sin, or of no sequence leave all rows as
  * they were.  What is written (the cache, q_out, r_out) lies apart from the rest
@@ -602,8 +602,8 @@ size_t fp8bq_latent_attention_workspace_bytes(const fp8bq_latent_cache* cache, c
  * fp8bq_kv_attention, except that out lies apart from the queries.
  * Scores, maxima and sums are fp32.  The weights exp(s - max) * scale_j are
  * rounded to two e4m3 terms (2^-8 of a weight, as BF16; 2^-22 of the largest of
- * its 32 neighbours), queries in the same way (exact but for 2^-22 of the row's
- * largest value), the output to BF16.  In sums of eight products, as the matrix
+ * its 32 neighbours), queries in the same way (exact but for 2^-22 of the largest
+ * value in the same half of the row), the output to BF16.  In sums of eight products, as the matrix
  * instruction makes them, what lies 2^-13 below the largest may be lost.
  * The kernel is chosen by the mean number of query rows (tokens * q_heads) per
  * sequence.

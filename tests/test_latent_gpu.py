@@ -262,6 +262,28 @@ def test_absorbed_of_mixed_magnitudes(gpu_lib, spread):
     close(lse, l, tol_lse, "lse")
 
 
+@pytest.mark.parametrize("heads", [5, 40])
+@pytest.mark.parametrize("power", [-60, 60])
+def test_absorbed_at_the_ends_of_the_scales(gpu_lib, heads, power):
+    """Powers of two of the scales pass through: scores stay, outputs move by them.
+    A weight times its scale has no meaning below 2^-121, at 2^-60 so a weight (of at
+    most 1) below 2^-61: codes are at most 448, so an output moves by at most n 448
+    2^-61, and then may round the other way, a step of BF16 being 2^-7 at most."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(heads)
+    cache = random_cache(fq, g, 8, 64, 512)
+    one = torch.ones_like(cache.scale)
+    q, qr = absorbed_inputs(g, 2, heads, 512)
+    args = (q.to(DEV), torch.zeros_like(qr).to(DEV), i32([[0, 1, 2, 3, 4], [7, 6, 5, -1, -1]]), i32([290, 129]))
+    want, lse = fq.latent_attention(fq.LatentCache(cache.c, cache.r, one), *args, scale=2.0 ** -9, return_lse=True)
+    moved = fq.LatentCache(cache.c, cache.r, one * 2.0 ** power)
+    got, same = fq.latent_attention(moved, *args, scale=2.0 ** (-9 - power), return_lse=True)
+    lost = torch.tensor([290, 129], dtype=torch.float64)[:, None, None] * 448 * 2.0 ** (-121 - power)
+    want, got = want.double().cpu(), got * 2.0 ** -power
+    assert bool(want.isfinite().all())
+    close(got, want, lost + (2.0 ** -7 * want.abs() if power < 0 else 0.0), "out")
+    close(same, lse.double().cpu(), 1e-6 * lse.abs().double().cpu() + 1e-5, "lse")
+
+
 @pytest.mark.parametrize("heads,new", [(16, [1, 1, 1, 1]), (50, [1, 1, 1, 1]), (128, [1, 1, 1, 1]), (40, [3, 1, 4, 2])])
 def test_absorbed_with_bad_pages_and_numbers(gpu_lib, heads, new):
     """Pages that are none are not seen; what lies behind a sequence, NaN and
