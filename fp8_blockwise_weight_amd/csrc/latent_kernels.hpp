@@ -313,7 +313,7 @@ __device__ __forceinline__ void unrolled(F&& f) {
 // What bounds it: up to 32 rows the loads (96 sequences of up to 16,384
 // tokens, 16 heads, 512 MB: 116 us, 4.4 TB/s, of which loading alone takes 98);
 // from 64 rows on the products and what is not hidden between them, 2.2 us a tile
-// of 64 rows by 64 keys (60 sequences of up to 12,000 tokens, 128 heads, 100
+// of 64 rows by 64 keys (60 sequences of up to 12,000 tokens, 128 heads, 103
 // GFLOP: 130 us, of which 32 are the queries' splitting, the sums' writing and
 // the join).  One wave with all channels of 32 rows, without the exchange,
 // takes 2.0 us for that but 24 us more around it.

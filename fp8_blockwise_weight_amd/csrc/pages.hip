@@ -10,7 +10,11 @@
 namespace {
 
 constexpr int32_t kMaxPageBuffers = 4096;
-constexpr int64_t kSmallPage = 1024;   // bytes: a page of fewer is copied by one wave
+// Bytes: a page of fewer is copied by one wave, with others of its number.  256
+// bytes (a latent page's scales) by workgroups of their own: 8 layers' latents,
+// 520 MB, 92 us for 88; 4 and 8 KB by a wave: 225 for 88, four forks of 27 layers 141
+// for 14.
+constexpr int64_t kSmallPage = 1024;
 
 // A range of memory that a call reads or writes.
 struct Range {
@@ -22,31 +26,38 @@ Range range_of(const void* p, uint64_t bytes) {
   return Range{at, at + static_cast<uintptr_t>(bytes)};
 }
 
-// The buffers' ranges in order, or false where something is wrong.
-bool pages_ok(const fp8bq_pages* p, std::vector<Range>& all) {
+// The buffers' ranges, in order.  (On the stack, 64 KB: nothing here may throw.)
+struct Ranges {
+  Range at[kMaxPageBuffers];
+  int32_t count;
+  const Range* begin() const { return at; }
+  const Range* end() const { return at + count; }
+};
+
+// Fills them in, or gives false where something is wrong.
+bool pages_ok(const fp8bq_pages* p, Ranges& all) {
   if (p == nullptr || kv_log2_page(p->page_size) < 0 || p->num_pages < 1 || p->num_pages > INT32_MAX) return false;
   if (p->count < 1 || p->count > kMaxPageBuffers || p->buffers == nullptr) return false;
-  all.resize(static_cast<size_t>(p->count));
+  all.count = p->count;
   for (int32_t i = 0; i < p->count; ++i) {
     const fp8bq_page_buffer& x = p->buffers[i];
     if (!x.p || !kv_aligned(x.p, 4) || x.page_bytes < 4 || x.page_bytes > INT32_MAX || x.page_bytes % 4 != 0) return false;
-    all[static_cast<size_t>(i)] =
-        range_of(x.p, static_cast<uint64_t>(p->num_pages) * static_cast<uint64_t>(x.page_bytes));
+    all.at[i] = range_of(x.p, static_cast<uint64_t>(p->num_pages) * static_cast<uint64_t>(x.page_bytes));
   }
-  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.at < b.at; });
-  for (size_t i = 1; i < all.size(); ++i) {
-    if (all[i].at < all[i - 1].end) return false;
+  std::sort(all.at, all.at + all.count, [](const Range& a, const Range& b) { return a.at < b.at; });
+  for (int32_t i = 1; i < all.count; ++i) {
+    if (all.at[i].at < all.at[i - 1].end) return false;
   }
   return true;
 }
 
 // Whether a range lies apart from all buffers.
-bool pages_apart(const std::vector<Range>& all, const void* p, uint64_t bytes) {
+bool pages_apart(const Ranges& all, const void* p, uint64_t bytes) {
   if (bytes == 0) return true;
   const Range r = range_of(p, bytes);
-  const auto after = std::upper_bound(all.begin(), all.end(), r.at, [](uintptr_t v, const Range& x) { return v < x.at; });
+  const Range* after = std::upper_bound(all.begin(), all.end(), r.at, [](uintptr_t v, const Range& x) { return v < x.at; });
   if (after != all.end() && after->at < r.end) return false;
-  return after == all.begin() || std::prev(after)->end <= r.at;
+  return after == all.begin() || (after - 1)->end <= r.at;
 }
 
 bool table_ok(const void* table, int64_t stride, int32_t count, int32_t max_pages) {
@@ -93,7 +104,7 @@ extern "C" {
 int fp8bq_cache_fork(const fp8bq_pages* pages, int32_t* block_table, int64_t table_stride, int32_t count,
                      int32_t max_pages, int32_t* seq_lens, const int32_t* parents, const int32_t* children,
                      const int32_t* fresh, int32_t forks, void* stream) {
-  std::vector<Range> all;
+  Ranges all;
   if (!pages_ok(pages, all) || !table_ok(block_table, table_stride, count, max_pages)) return FP8BQ_ERR_INVALID_ARGUMENT;
   if (forks < 0 || forks > kKvMaxBatch) return FP8BQ_ERR_INVALID_ARGUMENT;
   if (forks == 0 || count == 0) return FP8BQ_OK;
@@ -141,7 +152,7 @@ size_t fp8bq_cache_compact_workspace_bytes(int64_t num_pages) {
 int fp8bq_cache_compact(const fp8bq_pages* pages, const int32_t* block_table, int64_t table_stride, int32_t count,
                         int32_t max_pages, const int32_t* seq_lens, int32_t* table_out, int64_t out_stride,
                         int32_t* used, void* workspace, size_t workspace_bytes, void* stream) {
-  std::vector<Range> all;
+  Ranges all;
   if (!pages_ok(pages, all) || !table_ok(block_table, table_stride, count, max_pages) ||
       !table_ok(table_out, out_stride, count, max_pages) || pages->num_pages > fp8bq::kCompactPages) {
     return FP8BQ_ERR_INVALID_ARGUMENT;

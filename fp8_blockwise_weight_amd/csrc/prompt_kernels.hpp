@@ -33,9 +33,9 @@ struct PromptQuery {
 // busy for as long as the products take.
 //
 // Two prompts of 4096 tokens, 32 heads of 128 channels, 344 GFLOP: 322 us, 1070
-// TFLOP/s (a large BF16 matrix product reaches 1330); operands read when they
-// were wanted 335, without the priorities 333, a lane's place in a tile worked
-// out for every load 349.  Waves of 64 queries, one to a SIMD, with the weights
+// TFLOP/s (335 to 350 on other cards; a large BF16 matrix product reaches 1330);
+// beside it operands read when they were wanted 335, without the priorities 333,
+// a lane's place in a tile worked out for every load 349.  Waves of 64 queries, one to a SIMD, with the weights
 // of 32 keys between the products of the next, halve LDS's traffic and take 520:
 // a wave alone does not keep both units busy.
 //
