@@ -272,7 +272,8 @@ def latent_prompt_attention(q, k, k_rope, v, query_start, key_start=None, *, sca
 
     ``q`` is BF16 [tokens, heads, head_dim + 64], the rotated channels last,
     ``k`` and ``v`` BF16 [keys, heads, head_dim] (64 or 128; often two views of one
-    projection's output), ``k_rope`` BF16 [keys, 64], rotated, for all heads.
+    projection's output), ``k_rope`` BF16 [keys, 64], rotated, for all heads; their
+    token strides are below 2^23 elements.
     Sequence b's queries are the rows ``query_start[b]`` to ``query_start[b + 1]``
     (int32 [sequences + 1]), its keys the rows ``key_start[b]`` to
     ``key_start[b + 1]``, by default the same ones; its queries are its last
