@@ -285,7 +285,8 @@ def test_absorbed_at_the_ends_of_the_scales(gpu_lib, heads, power):
 
 
 @pytest.mark.parametrize("heads,new", [(16, [1, 1, 1, 1]), (50, [1, 1, 1, 1]), (128, [1, 1, 1, 1]), (40, [3, 1, 4, 2])])
-def test_absorbed_with_bad_pages_and_numbers(gpu_lib, heads, new):
+@pytest.mark.parametrize("spare", [0, 3])        # columns of the table: without shares, and with
+def test_absorbed_with_bad_pages_and_numbers(gpu_lib, heads, new, spare):
     """Pages that are none are not seen; what lies behind a sequence, NaN and
     infinite scales among it, has no effect; rows that are not numbers stay so
     and leave the others alone; rows of no sequence are left as they were."""
@@ -293,7 +294,7 @@ def test_absorbed_with_bad_pages_and_numbers(gpu_lib, heads, new):
     lens = [150, 70, 20, 0]
     starts = [2 + s for s in starts_of(new)]
     T = starts[-1] + 3
-    table = [[0, 99, 2], [3, -1, -1], [1 << 30, 1, 1], [4, 4, 4]]
+    table = [row + [5] * spare for row in ([0, 99, 2], [3, -1, -1], [1 << 30, 1, 1], [4, 4, 4])]
     cache = random_cache(fq, g, 6, 64, 512)
     hostc = host(cache)
     q, qr = (x.contiguous() for x in absorbed_inputs(g, T, heads, 512))
@@ -333,9 +334,10 @@ def test_absorbed_splits_of_one_call(gpu_lib):
 
 
 @pytest.mark.parametrize("heads", [16, 64, 128])
-def test_absorbed_strides_and_buffers(gpu_lib, heads):
+@pytest.mark.parametrize("width", [4, 9])       # without shares, and with
+def test_absorbed_strides_and_buffers(gpu_lib, heads, width):
     fq, g = gpu_lib, torch.Generator().manual_seed(heads)
-    lens, starts, table = [200, 90], [0, 2, 3], [[0, 1, 2, 3], [4, 5, 6, 7]]
+    lens, starts, table = [200, 90], [0, 2, 3], [[0, 1, 2, 3] + [-1] * (width - 4), [4, 5, 6, 7] + [-1] * (width - 4)]
     cache = random_cache(fq, g, 8, 64, 512)
     q, qr = absorbed_inputs(g, 3, heads, 512)
     want = ref.absorbed(host(cache), q, qr, table, lens, starts, 0.06)
@@ -343,6 +345,7 @@ def test_absorbed_strides_and_buffers(gpu_lib, heads):
     big = torch.full((3, heads, 520), 5.0, dtype=torch.bfloat16, device=DEV)
     head_major = torch.empty((heads, 3, 512), dtype=torch.bfloat16, device=DEV).transpose(0, 1)
     need = fq.latent_attention_workspace_bytes(cache, q, args[0])
+    assert (need > 0) == (width > 4)
     work = torch.full((need + 16,), 255, dtype=torch.uint8, device=DEV)
     for out in (big[..., :512], head_major):
         got = fq.latent_attention(cache, q.to(DEV), qr.contiguous().to(DEV), *args, scale=0.06, out=out, workspace=work)
