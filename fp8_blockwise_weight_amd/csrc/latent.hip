@@ -407,10 +407,25 @@ int fp8bq_latent_prompt_attention(const fp8bq_latent_prompt* p, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t slots = p->tokens / 128 + p->count;
   const dim3 grid(static_cast<unsigned>(slots * p->heads));
+  // Where row tiles leave CUs idle (an eighth over, as slots count a tile too many
+  // for most sequences), two sets of waves walk the keys of one: one prompt of 4096
+  // at 8 heads of 128 (264 slots) 92 -> 75 us, 500 queries over 8000 keys at 32
+  // heads (128) 171 -> 134, nine prompts of 300 at 8 heads (240) 13.5 -> 14.1; beyond
+  // it four of 700 at 16 heads (400) 28 -> 33, one of 4096 (528) 113 -> 97, at 32
+  // heads (1056) 178 -> 188.
+  const bool few = slots * p->heads <= 288;
+  const auto launch = [&](auto dim) {
+    constexpr int kDim = decltype(dim)::value;
+    if (few) {
+      hipLaunchKernelGGL((fp8bq::latent_prompt<kDim, 2>), grid, dim3(512), 0, st, d);
+    } else {
+      hipLaunchKernelGGL((fp8bq::latent_prompt<kDim, 1>), grid, dim3(256), 0, st, d);
+    }
+  };
   if (D == 128) {
-    hipLaunchKernelGGL((fp8bq::latent_prompt<128, 4>), grid, dim3(256), 0, st, d);
+    launch(std::integral_constant<int, 128>{});
   } else {
-    hipLaunchKernelGGL((fp8bq::latent_prompt<64, 4>), grid, dim3(256), 0, st, d);
+    launch(std::integral_constant<int, 64>{});
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? FP8BQ_OK : hip_failed(e);

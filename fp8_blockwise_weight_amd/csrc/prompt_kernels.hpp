@@ -25,7 +25,7 @@ struct PromptQuery {
 // The scores of 64 keys, their softmax with a running maximum, the weighted sum
 // of the values: both products on the matrix units, K Q and V W, so that a lane
 // holds one query's scores and its weights are operands where they lie.  A wave
-// holds 32 queries; W = 4 of them share the tiles in LDS, which loads put there
+// holds 32 queries; four of them share the tiles in LDS, which loads put there
 // past the registers while the tile before is worked on, and two such workgroups
 // share a CU: one's products run while the other takes exponentials, and the
 // priority that a wave has within its products keeps them taking turns.  What
@@ -35,22 +35,28 @@ struct PromptQuery {
 // Two prompts of 4096 tokens, 32 heads of 128 channels, 344 GFLOP: 322 us, 1070
 // TFLOP/s (335 to 350 on other cards; a large BF16 matrix product reaches 1330);
 // beside it operands read when they were wanted 335, without the priorities 333,
-// a lane's place in a tile worked out for every load 349.  Waves of 64 queries, one to a SIMD, with the weights
-// of 32 keys between the products of the next, halve LDS's traffic and take 520:
-// a wave alone does not keep both units busy.
+// a lane's place in a tile worked out for every load 349.  Waves of 64 queries,
+// one to a SIMD, with the weights of 32 keys between the products of the next,
+// halve LDS's traffic and take 520: a wave alone does not keep both units busy.
 //
-// A workgroup takes R = 32 W query tokens of one head.  Slot w of the grid
+// A workgroup takes R = 128 query tokens of one head.  Slot w of the grid
 // belongs to the sequence with floor(q_at[b] / R) + b <= w, which leaves every
 // sequence as many slots as it has row tiles, whatever the offsets are.
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
-  constexpr int R = 32 * W;
+//
+// With K = 2 a workgroup has as many waves again, which take every other tile, out
+// of an LDS of their own, and whose sums are joined at the end: half the tiles in
+// a row, on the whole of a CU.
+template <int D, int K>
+__global__ __launch_bounds__(256 * K, 2) void latent_prompt(PromptQuery p) {
+  constexpr int W = 4, R = 32 * W;
   constexpr int kJ = D / 16, kO = D / 32;
   constexpr int kC = D / 8;                       // 16-byte chunks of a row
   constexpr int kK = 64 * 2 * D, kR = 64 * 2 * kRope;
   constexpr int kBytes = 2 * kK + kR;             // keys, rotated keys, values
-  __shared__ __align__(1024) uint8_t lds[2 * kBytes];
-  const int32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ __align__(1024) uint8_t all_lds[K * 2 * kBytes];
+  const int32_t tid = threadIdx.x & (64 * W - 1), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t turn = K == 1 ? 0 : __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x / (64 * W));
+  uint8_t* lds = all_lds + turn * 2 * kBytes;
   const int32_t col = lane & 31, half = lane >> 5;
   const int32_t w_item = blockIdx.x / p.heads, h = blockIdx.x - w_item * p.heads;
   const auto q_row = [&](int32_t i) { return kv_clamp(p.q_at[i], p.tokens); };
@@ -122,7 +128,7 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
       }
     }
   };
-  if (last >= 0) stage(0, 0);
+  if (turn <= last) stage(turn, 0);
 
   bf16x8 q[kJ + 4];
   {
@@ -140,18 +146,20 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
   for (int i = 0; i < kO; ++i) o[i] = f32x16{};
   float m = -INFINITY, l = 0.0f;
 
-  for (int32_t tile = 0; tile <= last; ++tile) {
-    const int32_t slot = tile & 1, t0 = tile * kKeyTile;
+  const int32_t rounds = (last + K) / K;   // the same for all waves, as they wait for each other
+  for (int32_t round = 0; round < rounds; ++round) {
+    const int32_t tile = round * K + turn, slot = round & 1, t0 = tile * kKeyTile;
     uint8_t* from = lds + slot * kBytes;
     lds_arrived();
-    if (t0 + kKeyTile > see_hi) {
+    if ((round + 1) * K * kKeyTile > see_hi) {
       // values that nobody sees count as zeros, whatever is there
       for (int32_t i = tid; i < 64 * kC; i += 64 * W) {
         if (t0 + i / kC >= see_hi) *(u32x4*)(from + kK + kR + 16 * i) = u32x4{0, 0, 0, 0};
       }
       lds_written();
     }
-    if (tile < last) stage(tile + 1, slot ^ 1);
+    if (tile + K <= last) stage(tile + K, slot ^ 1);
+    if (K > 1 && tile > last) break;             // only in the last round
     __builtin_amdgcn_s_setprio(1);
     f32x16 s[2];
     s[0] = f32x16{};
@@ -242,6 +250,28 @@ __global__ __launch_bounds__(64 * W, 2) void latent_prompt(PromptQuery p) {
       });
     }
     __builtin_amdgcn_s_setprio(0);
+  }
+  if constexpr (K == 2) {
+    constexpr int kSums = 16 * kO;
+    static_assert(W * (kSums + 2) * 64 * 4 <= (int)sizeof(all_lds), "sums on their way");
+    float* pass = (float*)all_lds + wave * (kSums + 2) * 64 + lane;
+    lds_written();   // nobody reads tiles any more
+    if (turn == 1) {
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) pass[i * 64] = o[i >> 4][i & 15];
+      pass[kSums * 64] = m;
+      pass[(kSums + 1) * 64] = l;
+    }
+    lds_written();
+    if (turn == 1) return;
+    const float m1 = pass[kSums * 64], to = fmaxf(m, m1);
+    // sums without a maximum are zeros, or no numbers
+    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+    const float f1 = m1 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m1 - to);
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) o[i >> 4][i & 15] = o[i >> 4][i & 15] * f + pass[i * 64] * f1;
+    l = l * f + pass[(kSums + 1) * 64] * f1;
+    m = to;
   }
   l += __shfl_xor(l, 32);
   if (!live) return;

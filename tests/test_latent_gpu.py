@@ -387,6 +387,8 @@ EXPANDED = [
     (64, 2, [70, 5, 128], [200, 5, 640]),
     (128, 2, [130, 3], [131, 700]),
     (128, 1, [10, 5, 4], [4, 0, 4]),          # the first queries see nothing
+    (64, 24, [300] * 9, None),                # many row tiles: one set of waves each
+    (128, 33, [130, 7, 260, 0, 1, 64], [130, 400, 300, 9, 0, 65]),
 ]
 
 
