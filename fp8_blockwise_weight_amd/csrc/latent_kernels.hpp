@@ -162,7 +162,10 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // `hi` is the code of x / s, `lo` of (x - hi s) / (s / 32): with |x| < 256 s
 // the rest is at most 8 s.
 constexpr int kLoShift = 5;
-constexpr float kRise = 32.0f;   // by how much (log2) scores pass their maximum before it follows
+// By how much (log2) scores pass their maximum before it follows.  Sums stay
+// below 2^24 times the largest scale, 2^60, the largest code, 448, and 2^31 keys:
+// 2^124, where a float ends at 2^128.
+constexpr float kRise = 24.0f;
 __device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo, bool upper) {
   const float t = s * (1.0f / (1 << kLoShift));
   s16x2 h = __builtin_bit_cast(s16x2, hi), l = __builtin_bit_cast(s16x2, lo);
@@ -649,8 +652,8 @@ __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatc
         asm volatile("" : "+v"(x.top));
       } else if constexpr (n == 1) {
         x.top = half_max(x.top) * factor;
-        // The maximum follows when weights would pass 2^32: their scale goes with
-        // them, and sums are floats.
+        // The maximum follows when weights would pass 2^kRise: their scale goes
+        // with them, and sums are floats.
         x.was = m;
         m = x.top > m + kRise ? __builtin_ceilf(x.top) : m;
         asm volatile("" : "+v"(m));
@@ -717,8 +720,11 @@ __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatc
       return x;
     };
     auto follow = [&](Both& x) {
+      // The sums' maximum is the larger of the pair's, so that neither's weights
+      // pass 2^kRise of it.  Both are set in the first tile and move in steps
+      // above kRise: sums are seldom scaled.
       const float top = fmaxf(x.m0, x.m1), was = ref;
-      const bool rise = top > ref + kRise;
+      const bool rise = top > ref;
       ref = rise ? top : ref;
       // sums without a maximum yet are zeros, or no numbers
       if (__builtin_expect(__ballot(rise && was > -INFINITY) != 0, 0)) {
