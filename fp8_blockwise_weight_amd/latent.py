@@ -157,8 +157,6 @@ def latent_append(cache, c, r, block_table, seq_lens, query_start=None, *, q=Non
         positions, cos_p, sin_p = cos.shape[0], cos.data_ptr(), sin.data_ptr()
         if cos.get_device() != index or sin.get_device() != index or (cos_p | sin_p) & 15:
             raise ValueError("cos and sin must be on the cache's device and 16-byte aligned")
-        if positions == 0:
-            return q_out if q is None or q_out is not None else torch.empty_like(q)
     qp = qt = qh = op = ot = oh = heads = rop = rot = 0
     if q is not None:
         qp, qt, qh = _rows(q, tokens, None, ROPE_DIM, index, "q")
@@ -174,7 +172,7 @@ def latent_append(cache, c, r, block_table, seq_lens, query_start=None, *, q=Non
         _writable(r_out.unsqueeze(1), rot, 0, "r_out")
     if tokens > MAX_ROWS:
         raise ValueError(f"at most {MAX_ROWS} rows (tokens x heads) per call")
-    if tokens == 0 or n == 0:
+    if tokens == 0 or n == 0 or (cos is not None and positions == 0):   # all are left out
         return q_out
     packed = _TOKENS.pack(cp, rp, rop, qp, op, cos_p, sin_p, ct, rt, rot, qt, qh, ot, oh, tokens, positions, heads,
                           int(bool(interleaved)))

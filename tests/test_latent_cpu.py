@@ -5,6 +5,7 @@ struct layouts are the header's."""
 import ctypes
 import os
 import subprocess
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -276,6 +277,27 @@ def test_no_cpu_implementation():
         fq.cache_fork([c], None, None, None, None, None)
     with pytest.raises(ValueError):
         fq.cache_compact([], None, None)
+
+
+def test_append_without_positions_is_checked():
+    """Zero rows of cos and sin leave all tokens out, and let nothing pass that is
+    refused otherwise."""
+    cache = SimpleNamespace(_index=-1, latent_dim=256, device=torch.device("cpu"))     # of tensors on the CPU
+    bf = torch.bfloat16
+    c, r, q = torch.zeros((3, 256), dtype=bf), torch.zeros((3, 64), dtype=bf), torch.zeros((3, 2, 192), dtype=bf)[..., 128:]
+    args = (cache, c, r, torch.zeros((3, 1), dtype=torch.int32), torch.ones(3, dtype=torch.int32))
+    turn = dict(cos=torch.zeros((0, 32)), sin=torch.zeros((0, 32)))
+    assert fq.latent_append(*args, **turn) is None
+    out = fq.latent_append(*args, q=q, **turn)
+    assert out.shape == q.shape and out.dtype is bf and out.is_contiguous()
+    assert fq.latent_append(*args, q=q, q_out=out, r_out=r, **turn) is out
+    for bad, error in ((dict(q=q.float()), TypeError), (dict(q=q[:2]), ValueError), (dict(q=q[..., :32]), ValueError),
+                       (dict(q_out=out), ValueError), (dict(q=q, q_out=out[:, :1]), ValueError),
+                       (dict(q=q, q_out=out.float()), TypeError), (dict(q=q, q_out=out[:1].expand(3, 2, 64)), ValueError),
+                       (dict(r_out=r.float()), TypeError), (dict(r_out=r[:2]), ValueError),
+                       (dict(r_out=r[:1].expand(3, 64)), ValueError)):
+        with pytest.raises(error):
+            fq.latent_append(*args, **bad, **turn)
 
 
 # ------------------------------------------------------------- the oracle
