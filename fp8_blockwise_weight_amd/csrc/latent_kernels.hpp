@@ -131,12 +131,13 @@ struct LatentQuery {
 // 16 bytes a lane, or 4, from memory into LDS, past the registers: lane i's go to
 // lds + 16 i, lds + 4 i.  Written as assembly because the compiler, which cannot
 // tell one buffer from another, waits for all of them before any read of LDS.
+// The place is an operand in m0, not written here, so that the compiler knows
+// what m0 holds; it may come right before, and the load wants a state between.
 __device__ __forceinline__ void lds_load16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void lds_load4(const void* at, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(at) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(lds), "v"(at) : "memory");
 }
 // What this wave has loaded lies in LDS, what it reads from LDS it has read,
 // and so it is for every wave.

@@ -118,3 +118,47 @@ def test_early_touches_are_seen():
                       (".LBB0_1:\n" + move + product + wait + "\ts_cbranch_scc1 .LBB0_1\n" + leave, 0)):
         found, products = touched_early(body)
         assert (len(found), products) == (bad, body.count("v_mfma"))
+
+
+# The kernels as they ship: in the library's own unit.
+
+@pytest.fixture(scope="module")
+def library_asm(tmp_path_factory):
+    out = tmp_path_factory.mktemp("asm") / "library.s"
+    cmd = [c for c in fb.command(str(out)) if c not in ("-shared", "-fPIC")]
+    res = subprocess.run([cmd[0], "-S", "--cuda-device-only", *cmd[1:]], capture_output=True, text=True, timeout=600)
+    assert res.returncode == 0, res.stderr[-3000:]
+    return out.read_text()
+
+
+def bodies(text, kernel):
+    return re.findall(rf"^(_ZN5fp8bq\d+{kernel}I\w+):(.*?)^\.Lfunc_end", text, re.M | re.S)
+
+
+def test_sums_are_waited_for_in_the_library(library_asm):
+    kernels = bodies(library_asm, "latent_attend")
+    assert len(kernels) == 4
+    for name, body in kernels:
+        found, products = touched_early(body)
+        assert products >= 8, name
+        assert not found, (name, sorted(found)[:4])
+
+
+def written_by_hand(body):
+    """Instructions written as assembly."""
+    _, blocks = blocks_of(body)
+    return [code for block in blocks.values() for code, written in block if written]
+
+
+def test_assembly_leaves_m0_to_the_compiler(library_asm):
+    """Loads into LDS take their place from m0: as an operand, which the compiler
+    sets and knows of.  An instruction that wrote it behind the compiler's back
+    would change what the compiler's own uses of m0 read."""
+    for kernel, count in (("latent_attend", 4), ("latent_prompt", 4)):
+        kernels = bodies(library_asm, kernel)
+        assert len(kernels) == count
+        for name, body in kernels:
+            codes = written_by_hand(body)
+            assert any(code.startswith("global_load_lds") for code in codes), name
+            assert not [code for code in codes if re.search(r"\bm0\b", code)], name
+            assert re.search(r"^\ts_\w+ m0, ", body, re.M), name
