@@ -163,10 +163,13 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // `hi` is the code of x / s, `lo` of (x - hi s) / (s / 32): with |x| < 256 s
 // the rest is at most 8 s.
 constexpr int kLoShift = 5;
-// By how much (log2) scores pass their maximum before it follows.  Sums stay
-// below 2^24 times the largest scale, 2^60, the largest code, 448, and 2^31 keys:
-// 2^124, where a float ends at 2^128.
-constexpr float kRise = 24.0f;
+// By how much (log2) a maximum passes that of the sums before they follow.  Sums
+// stay below 2^27 times the largest scale, 2^60, the largest code, 448, and 2^31
+// keys: 2^126.8, where a float ends at 2^128.  Scaling sums is what costs: 96
+// sequences at 16 heads take 116.5 us with 27, 145 with 12 (in steps of 12 of the
+// waves' maxima, too), 121 where sums follow either wave's maximum at once, which
+// moves in steps of 24.
+constexpr float kRise = 27.0f;
 __device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo, bool upper) {
   const float t = s * (1.0f / (1 << kLoShift));
   s16x2 h = __builtin_bit_cast(s16x2, hi), l = __builtin_bit_cast(s16x2, lo);
@@ -653,10 +656,10 @@ __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatc
         asm volatile("" : "+v"(x.top));
       } else if constexpr (n == 1) {
         x.top = half_max(x.top) * factor;
-        // The maximum follows when weights would pass 2^kRise: their scale goes
-        // with them, and sums are floats.
+        // The maximum is a whole number at or above all scores: its changes scale
+        // the sum of weights exactly.
         x.was = m;
-        m = x.top > m + kRise ? __builtin_ceilf(x.top) : m;
+        m = x.top > m ? __builtin_ceilf(x.top) : m;
         asm volatile("" : "+v"(m));
       } else if constexpr (n == 2) {
         l *= x.was == m ? 1.0f : __builtin_amdgcn_exp2f(x.was - m);
@@ -721,11 +724,10 @@ __global__ __launch_bounds__(64 * W, 1) void latent_attend(LatentCache c, KvBatc
       return x;
     };
     auto follow = [&](Both& x) {
-      // The sums' maximum is the larger of the pair's, so that neither's weights
-      // pass 2^kRise of it.  Both are set in the first tile and move in steps
-      // above kRise: sums are seldom scaled.
+      // The sums are taken from a maximum of both waves', which weights pass by
+      // 2^kRise at most; until then their scale goes with them.
       const float top = fmaxf(x.m0, x.m1), was = ref;
-      const bool rise = top > ref;
+      const bool rise = top > ref + kRise;
       ref = rise ? top : ref;
       // sums without a maximum yet are zeros, or no numbers
       if (__builtin_expect(__ballot(rise && was > -INFINITY) != 0, 0)) {
