@@ -2,6 +2,8 @@
 // Every argument check runs before the first HIP call; the calls enqueue on
 // the caller's stream and neither allocate nor wait.
 
+#include <algorithm>
+
 #include "latent_kernels.hpp"
 #include "prompt_kernels.hpp"
 
@@ -9,6 +11,11 @@ namespace {
 
 constexpr int32_t kLatentMaxHeads = 1024;
 constexpr int64_t kPromptMaxStride = int64_t{1} << 23;   // of keys and values, elements
+// What a row tile of the absorbed form costs beyond its key tiles, in key tiles
+// (queries split, sums written): shares of 96 sequences x 16 heads, 60 x 128 and
+// 64 x 40 heads with drafts come out at 126, 139 and 59 us without it, 120, 133
+// and 51 with 3, 119, 127 and 52 with 5.
+constexpr int32_t kLatentExtra = 4;
 
 // The buffers of a cache.
 struct LatentBuffers {
@@ -107,7 +114,11 @@ LatentShape latent_shape(const fp8bq_latent_cache& c, const fp8bq_kv_batch& b, i
   s.subs = per_seq <= 64 ? 1 : (per_seq <= 128 ? 2 : 4);
   const int64_t row_tiles = tokens * heads / (s.rows * s.subs) + b.count;
   const int64_t key_tiles = ceil_div(static_cast<int64_t>(b.max_pages) * c.page_size, 64);
-  s.target = (s.rows == 32 ? 512 : 256) / s.subs;   // one round of workgroups
+  // One round of workgroups, but no more (in eights, one for each XCD) than there
+  // can be key tiles to share: one sequence of 777 tokens takes 3 MB of workspace
+  // instead of 64, and is cut up as before, a tile to a share.
+  const int64_t units = row_tiles * (key_tiles + kLatentExtra);
+  s.target = static_cast<int32_t>(std::min<int64_t>((s.rows == 32 ? 512 : 256) / s.subs, ceil_div(units, 8) * 8));
   // Short tables leave nothing to cut up: without shares, their partial sums and
   // the join, steps at 200 tokens (4 tiles) of 96 sequences take 18 instead of 24
   // at 16 heads and 24 instead of 53 at 128, one sequence 17.1 instead of 16.5; at
@@ -316,11 +327,7 @@ int fp8bq_latent_attention(const fp8bq_latent_cache* cache, const fp8bq_kv_batch
   d.k.jump = s.target;
   d.k.min_tiles = 1;
   d.k.tile_rows = s.rows * s.subs;
-  // What a row tile costs beyond its key tiles, in key tiles (queries split, sums
-  // written): shares of 96 sequences x 16 heads, 60 x 128 and 64 x 40 heads with
-  // drafts come out at 126, 139 and 59 us without it, 120, 133 and 51 with 3, 119,
-  // 127 and 52 with 5.
-  d.k.extra = 4;
+  d.k.extra = kLatentExtra;
   d.subs = s.subs;
   d.k.scale = scale;
   d.r = static_cast<const uint16_t*>(q->q_rope);

@@ -129,6 +129,21 @@ def test_workspace():
     assert lib.fp8bq_latent_attention(cache(), batch(count=0, starts=0), query(tokens=0), None, 0, None) == fq.OK
 
 
+@no_gpu
+def test_workspace_of_small_calls():
+    """Room for no more partial sums than a call can make: two for each key tile, and
+    four tiles more, of each row tile, in whole eights; and never more than the
+    largest calls take."""
+    lib = fq.load_library()
+    for dim in (256, 512):
+        for heads, rows in ((16, 32), (40, 64), (128, 128), (300, 256)):
+            for count, width in ((1, 5), (1, 13), (1, 100), (4, 6), (30, 9), (1, 100000), (200, 300)):
+                need = lib.fp8bq_latent_attention_workspace_bytes(cache(dim=dim), batch(count=count, width=width), heads, count)
+                units = (count * heads // rows + count) * (width + 4)
+                shares = min(-(-units // 8) * 8, 256 * 64 // rows)
+                assert need == 2 * shares * rows * (4 * dim + 8) + 8 * count * heads, (dim, heads, count, width)
+
+
 P = (3200, 192, 4096, 256, 64, 4096, 256, 2048, 128)
 
 
