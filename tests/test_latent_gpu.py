@@ -358,6 +358,34 @@ def test_absorbed_strides_and_buffers(gpu_lib, heads, width):
         fq.latent_attention(cache, q.to(DEV), qr.to(DEV), *args, scale=0.06, workspace=work[:need - 1])
 
 
+@pytest.mark.parametrize("heads", [16, 64, 128])
+@pytest.mark.parametrize("width", [4, 9, 40])
+def test_absorbed_workspace(gpu_lib, heads, width):
+    """One byte less than it takes is refused, nothing beyond it is written, and
+    where it takes none an empty one does."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(heads + width)
+    cache = random_cache(fq, g, 8, 64, 512)
+    q, qr = (x.to(DEV) for x in absorbed_inputs(g, 3, heads, 512))
+    table = i32([[0, 1, 2, 3] + [-1] * (width - 4), [4, 5, 6, 7] + [-1] * (width - 4)])
+    args = (cache, q, qr, table, i32([200, 90]), i32([0, 2, 3]))
+    want = fq.latent_attention(*args, scale=0.06)
+    need = fq.latent_attention_workspace_bytes(cache, q, table)
+    work = torch.full((need + 4096,), 255, dtype=torch.uint8, device=DEV)
+    got = fq.latent_attention(*args, scale=0.06, workspace=work[:need])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and bool((work[need:] == 255).all())
+    if width <= 4:
+        assert need == 0
+        return
+    out = torch.full((3, heads, 512), 7.0, dtype=torch.bfloat16, device=DEV)
+    for short in (work[:need - 1], work[:0]):
+        with pytest.raises(fq.Fp8bqError) as error:
+            fq.latent_attention(*args, scale=0.06, workspace=short, out=out)
+        assert error.value.status == fq.ERR_WORKSPACE
+    torch.cuda.synchronize()
+    assert bool((out == 7).all())
+
+
 def test_far_pages(gpu_lib):
     """Codes beyond 2^32 bytes from the cache's start."""
     fq, g = gpu_lib, torch.Generator().manual_seed(1)
@@ -527,6 +555,42 @@ def test_graphs_follow_the_lengths(gpu_lib, heads):
         torch.cuda.synchronize()
         assert torch.equal(out, step(mirror))
         assert torch.equal(cache.c.view(torch.uint8), mirror.c.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dim,heads", [(128, 4), (64, 4), (128, 40), (64, 40)])   # two sets of waves, and one
+def test_expanded_graphs_follow_the_offsets(gpu_lib, dim, heads):
+    """A captured call, replayed over other offsets, queries and keys, with eager
+    work between."""
+    fq, g = gpu_lib, torch.Generator().manual_seed(dim + heads)
+    T, K = 700, 900
+    q = torch.randn((T, heads, dim + 64), generator=g).to(torch.bfloat16).to(DEV)
+    kv = torch.randn((K, heads, 2 * dim), generator=g).to(torch.bfloat16).to(DEV)
+    kr = torch.randn((K, 64), generator=g).to(torch.bfloat16).to(DEV)
+    q_at, k_at = i32([0, 300, 300, 700]), i32([0, 400, 400, 900])
+    out, lse = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=DEV), torch.empty((T, heads), device=DEV)
+
+    def call(**to):
+        return fq.latent_prompt_attention(q, kv[..., :dim], kr, kv[..., dim:], q_at, k_at, return_lse=True, **to)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out=out, lse=lse)
+    for queries, keys in (([0, 300, 300, 700], [0, 400, 400, 900]), ([0, 1, 699, 700], [0, 1, 850, 900]),
+                          ([5, 5, 200, 600], [0, 0, 10, 700]), ([0, 0, 0, 700], [0, 0, 0, 900])):
+        q_at.copy_(i32(queries))
+        k_at.copy_(i32(keys))
+        kv.copy_(torch.randn((K, heads, 2 * dim), generator=g).to(torch.bfloat16))
+        for x in (out, lse):
+            x.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_lse = call()
+        rows = slice(queries[0], queries[-1])
+        assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows])
+        for x in (out, lse):
+            assert bool((x[:queries[0]] == 3).all()) and bool((x[queries[-1]:] == 3).all())
 
 
 def test_streams_and_threads(gpu_lib):
