@@ -108,7 +108,10 @@ LatentShape latent_shape(const fp8bq_latent_cache& c, const fp8bq_kv_batch& b, i
   // 32 rows 125 and 131; 60 of 40 rows 106 and 91, of 64 rows 113 and 99.
   // Where rows need more workgroups than one, these take the same keys side by
   // side on one XCD, whose cache serves all but the first: 60 sequences of 128
-  // rows 155 -> 151, 30 of 256 rows 144 -> 140.
+  // rows 155 -> 151, 30 of 256 rows 144 -> 140.  All of this goes by the mean, so
+  // that one long chunk among single tokens leaves most of the workgroups beside
+  // them idle: 31 sequences with a token each and one with 512 take 242 at 16 heads
+  // (calls of their own: 47 and 163), 1087 at 128 (91 and 942).
   const int64_t per_seq = ceil_div(tokens * heads, b.count);
   s.rows = per_seq <= 32 ? 32 : 64;
   s.subs = per_seq <= 64 ? 1 : (per_seq <= 128 ? 2 : 4);
@@ -417,9 +420,12 @@ int fp8bq_latent_prompt_attention(const fp8bq_latent_prompt* p, void* stream) {
   // Where row tiles leave CUs idle (an eighth over, as slots count a tile too many
   // for most sequences), two sets of waves walk the keys of one: one prompt of 4096
   // at 8 heads of 128 (264 slots) 92 -> 75 us, 500 queries over 8000 keys at 32
-  // heads (128) 171 -> 134, nine prompts of 300 at 8 heads (240) 13.5 -> 14.1; beyond
-  // it four of 700 at 16 heads (400) 28 -> 33, one of 4096 (528) 113 -> 97, at 32
-  // heads (1056) 178 -> 188.
+  // heads (128) 171 -> 134.  Beyond it one set is faster mostly: four prompts of 700
+  // at 16 heads (400) 28, with two 33; one of 4096 at 32 heads (1056) 178 and 188.
+  // The number of slots does not tell how many tiles the longest row tile has, and
+  // so it errs where that decides: nine prompts of 300 at 8 heads (240) take 14.1
+  // with two sets, 13.5 with one; one of 4096 at 16 heads (528) 113 with one, 97
+  // with two.
   const bool few = slots * p->heads <= 288;
   const auto launch = [&](auto dim) {
     constexpr int kDim = decltype(dim)::value;

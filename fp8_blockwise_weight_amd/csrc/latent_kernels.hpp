@@ -163,13 +163,6 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // `hi` is the code of x / s, `lo` of (x - hi s) / (s / 32): with |x| < 256 s
 // the rest is at most 8 s.
 constexpr int kLoShift = 5;
-// By how much (log2) a maximum passes that of the sums before they follow.  Sums
-// stay below 2^27 times the largest scale, 2^60, the largest code, 448, and 2^31
-// keys: 2^126.8, where a float ends at 2^128.  Scaling sums is what costs: 96
-// sequences at 16 heads take 116.5 us with 27, 145 with 12 (in steps of 12 of the
-// waves' maxima, too), 121 where sums follow either wave's maximum at once, which
-// moves in steps of 24.
-constexpr float kRise = 27.0f;
 __device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo, bool upper) {
   const float t = s * (1.0f / (1 << kLoShift));
   s16x2 h = __builtin_bit_cast(s16x2, hi), l = __builtin_bit_cast(s16x2, lo);
@@ -192,6 +185,14 @@ __device__ __forceinline__ int32_t split_exponent(float most) {
   return max((int32_t)((__float_as_uint(most) >> 23) & 255) - 7, 1 + kLoShift);
 }
 __device__ __forceinline__ float exponent_scale(int32_t e) { return __uint_as_float((uint32_t)e << 23); }
+
+// By how much (log2) a maximum passes that of the sums before they follow.  Sums
+// stay below 2^27 times the largest scale, 2^60, the largest code, 448, and 2^31
+// keys: 2^126.8, where a float ends at 2^128.  Scaling sums is what costs: 96
+// sequences at 16 heads take 116.5 us with 27, 145 with 12 (in steps of 12 of the
+// waves' maxima, too), 121 where sums follow either wave's maximum at once, which
+// moves in steps of 24.
+constexpr float kRise = 27.0f;
 
 template <int kSelA, int kSelB>
 __device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, const f32x16& c, int32_t sa, int32_t sb) {

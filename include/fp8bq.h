@@ -560,9 +560,10 @@ typedef struct fp8bq_latent_tokens {
  *   s   = the smallest power of two with 448 * s >= max(max|c|, FP8BQ_EPS)
  *   c   -> e4m3fn(clamp(c / s, -448, 448)), nearest, ties to even; s is its scale
  * A token's codes depend on nothing but the token.  Values must be finite: a
- * token with others gets unspecified codes (and attention wants them below 2^68).  Tokens whose page is none, or lies
- * beyond the table, are not stored, but rotated; those at negative positions, at
- * positions without a row of cos and sin, or of no sequence leave all rows as
+ * token with others gets unspecified codes, and one with values above 448 * 2^60 a
+ * scale that fp8bq_latent_attention does not take.  Tokens whose page is none, or
+ * lies beyond the table, are not stored, but rotated; those at negative positions,
+ * at positions without a row of cos and sin, or of no sequence leave all rows as
  * they were.  What is written (the cache, q_out, r_out) lies apart from the rest
  * and from each other (checked); what fp8bq_kv_append says of pages that several
  * sequences hold goes for single slots here.
@@ -606,7 +607,7 @@ size_t fp8bq_latent_attention_workspace_bytes(const fp8bq_latent_cache* cache, c
  * value in the same half of the row), the output to BF16.  In sums of eight products, as the matrix
  * instruction makes them, what lies 2^-13 below the largest may be lost.
  * The kernel is chosen by the mean number of query rows (tokens * q_heads) per
- * sequence.
+ * sequence: chunks and single tokens are served faster in calls of their own.
  * Returns an fp8bq_status.
  */
 int fp8bq_latent_attention(const fp8bq_latent_cache* cache, const fp8bq_kv_batch* batch,
